@@ -8,8 +8,9 @@ calls raise.
 
 Low level (same names as the C ABI): ``la_create``, ``la_forward``, ``la_forward_host``,
 ``la_decode_step``, ``la_status``, ``la_destroy``, ``la_last_error``,
-``la_last_launches``, ``la_version``, ``la_forward_noalloc``, ``la_noalloc_status``. Convenience: ``Handle`` takes torch
-tensors.
+``la_last_launches``, ``la_version``, ``la_forward_noalloc``, ``la_noalloc_status``,
+and the ``la_packed_*`` calls (the gated delta rule over packed requests).
+Convenience: ``Handle`` and ``PackedHandle`` take torch tensors.
 """
 from __future__ import annotations
 
@@ -25,6 +26,8 @@ LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_MISALIGNED, LA_ERR_CUDA, L
 LA_FLAG_IDENTITY_PHI = 0x1
 LA_FLAG_SEQUENTIAL_CHUNKS = 0x2
 LA_FLAG_TEST_TIMEOUT = 0x100
+LA_PLAN_FAULT_ROWS, LA_PLAN_FAULT_FREE, LA_PLAN_FAULT_SLOT = 1, 2, 4
+LA_PLAN_FAULT_OWNER, LA_PLAN_FAULT_STATE, LA_PLAN_FAULT_OVERFLOW = 8, 16, 32
 
 VARIANTS = {"norm": LA_NORM_ELU1, "gla": LA_GLA, "gdn": LA_GDN, "norm_decay": LA_NORM_DECAY, "kda": LA_KDA}
 ERRORS = {1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_MISALIGNED",
@@ -33,6 +36,12 @@ ERRORS = {1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_MISALIGNE
 
 class la_config(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("d_k", ctypes.c_int), ("d_v", ctypes.c_int),
+                ("io", ctypes.c_int), ("flags", ctypes.c_uint), ("device", ctypes.c_int)]
+
+
+class la_packed_config(ctypes.Structure):
+    _fields_ = [("max_requests", ctypes.c_int), ("max_tokens", ctypes.c_int), ("slots", ctypes.c_int),
+                ("H_k", ctypes.c_int), ("H_v", ctypes.c_int), ("d_k", ctypes.c_int), ("d_v", ctypes.c_int),
                 ("io", ctypes.c_int), ("flags", ctypes.c_uint), ("device", ctypes.c_int)]
 
 
@@ -83,6 +92,25 @@ def lib() -> ctypes.CDLL:
             L.la_forward_noalloc.restype = i
             L.la_noalloc_status.argtypes = [i, vp]
             L.la_noalloc_status.restype = i
+            ll = ctypes.c_longlong
+            L.la_packed_plan_words.argtypes = [ctypes.POINTER(la_packed_config)]
+            L.la_packed_plan_words.restype = ll
+            L.la_packed_create.argtypes = [ctypes.POINTER(la_packed_config), ctypes.POINTER(ctypes.c_void_p)]
+            L.la_packed_create.restype = i
+            L.la_packed_destroy.argtypes = [vp]
+            L.la_packed_destroy.restype = None
+            L.la_packed_plan.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, vp]
+            L.la_packed_plan.restype = i
+            L.la_packed_forward.argtypes = [vp, vp, vp, vp, vp, fp, fp, fp, vp, i, i, ll, ll, ll, i, vp]
+            L.la_packed_forward.restype = i
+            L.la_packed_decode_step.argtypes = [vp, vp, vp, vp, vp, fp, fp, fp, vp, i, i, ll, ll, ll, vp]
+            L.la_packed_decode_step.restype = i
+            L.la_packed_status.argtypes = [vp, vp]
+            L.la_packed_status.restype = i
+            L.la_packed_last_error.argtypes = [vp]
+            L.la_packed_last_error.restype = ctypes.c_char_p
+            L.la_packed_last_launches.argtypes = [vp]
+            L.la_packed_last_launches.restype = i
             _lib = L
     return _lib
 
@@ -360,3 +388,187 @@ class Handle:
     def status(self, stream=None) -> int:
         """Synchronize the stream and return (and clear) the device status."""
         return la_status(self._h, _stream_ptr(stream))
+
+
+class PackedPlan:
+    """The plan of a step (see la.h): one int32 buffer on the device and its
+    sections as views. The views follow the step the plan was last made for."""
+
+    def __init__(self, cfg: la_packed_config, words, device):
+        import torch
+        self.words = torch.empty(words, dtype=torch.int32, device=device)
+        self.cfg = cfg
+        self.requests = self.tokens = 0
+        self._views = None
+
+    def _set(self, requests, tokens):
+        if (requests, tokens) != (self.requests, self.tokens) or self._views is None:
+            self.requests, self.tokens = requests, tokens
+            pad = lambda n: (n + 3) // 4 * 4   # noqa: E731
+            R, N, w = self.cfg.max_requests, self.cfg.max_tokens, self.words
+            offsets = 8
+            slots = offsets + pad(R + 1)
+            order = slots + pad(R)
+            treq = order + 2 * pad(R)
+            tpos = treq + pad(N)
+            self._views = (w[:4], w[offsets:offsets + requests + 1], w[slots:slots + requests],
+                           w[order:order + requests], w[treq:treq + tokens], w[tpos:tpos + tokens])
+
+    @property
+    def counts(self):
+        """int32 [4]: rows used, requests taking part, free slots left, faults (LA_PLAN_FAULT_* bits)."""
+        return self._views[0]
+
+    @property
+    def offsets(self):
+        """int32 [requests + 1]: first row of every request."""
+        return self._views[1]
+
+    @property
+    def state_slots(self):
+        """int32 [requests]: state slot of a request that takes part, else -1."""
+        return self._views[2]
+
+    @property
+    def order(self):
+        """int32 [requests]: the order in which the prefill walks the requests."""
+        return self._views[3]
+
+    @property
+    def token_request(self):
+        """int32 [tokens]: every row's request, -1 in rows of none."""
+        return self._views[4]
+
+    @property
+    def token_position(self):
+        """int32 [tokens]: every row's position in its request (tokens seen before included), -1 in rows of none."""
+        return self._views[5]
+
+
+class PackedHandle:
+    """The gated delta rule over packed requests with a pool of states: one
+    configuration (head counts and sizes, io dtype, the largest step). The
+    device is the current one unless given; calls run on ``stream`` or the
+    device's current stream."""
+
+    def __init__(self, *, max_requests, max_tokens, slots, H_k, H_v, d_k, d_v, io="bf16", device=None):
+        import torch
+        if io not in ("bf16", "fp32"):
+            raise ValueError(f"io: expected 'bf16' or 'fp32', got {io!r}")
+        dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
+        self.device = dev
+        self.dtype = torch.bfloat16 if io == "bf16" else torch.float32
+        self.H_k, self.H_v, self.d_k, self.d_v, self.slots = H_k, H_v, d_k, d_v, slots
+        self.cfg = la_packed_config(max_requests, max_tokens, slots, H_k, H_v, d_k, d_v,
+                                    LA_BF16 if io == "bf16" else LA_FP32, 0, dev.index)
+        h = ctypes.c_void_p()
+        rc = lib().la_packed_create(ctypes.byref(self.cfg), ctypes.byref(h))
+        if rc != LA_OK:
+            raise LAError(rc, "la_packed_create failed")
+        self._h = h
+        self._words = lib().la_packed_plan_words(ctypes.byref(self.cfg))
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().la_packed_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _check(self, rc):
+        if rc != LA_OK:
+            raise LAError(rc, lib().la_packed_last_error(self._h).decode())
+
+    def _stream(self, stream):
+        import torch
+        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+
+    def _expect(self, name, t, shape, dtype):
+        if t.dtype is not dtype or t.device != self.device:
+            raise ValueError(f"{name}: expected a {dtype} tensor on {self.device}")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous shape {tuple(shape)}, got {tuple(t.shape)}")
+
+    def _rows(self, name, t, tokens, heads, d):
+        """A packed tensor's row stride in elements; heads and channels of a row lie together."""
+        if t.dtype is not self.dtype or t.device != self.device:
+            raise ValueError(f"{name}: expected a {self.dtype} tensor on {self.device}")
+        if t.shape != (tokens, heads, d):
+            raise ValueError(f"{name}: expected shape {(tokens, heads, d)}, got {tuple(t.shape)}")
+        st = t.stride()
+        if tokens and ((st[2] != 1 and d > 1) or (st[1] != d and heads > 1)):
+            raise ValueError(f"{name}: the heads and channels of a row have to lie together, got strides {st}")
+        return st[0] if tokens > 1 else heads * d
+
+    def new_plan(self) -> PackedPlan:
+        """A plan buffer of this handle's maxima; reusable, step after step."""
+        return PackedPlan(self.cfg, self._words, self.device)
+
+    def plan(self, lengths, seen, slots, free_slots, free_count, *, tokens, plan=None, stream=None) -> PackedPlan:
+        """The plan of a step, made on the device: lengths, seen, slots int32
+        [requests], free_slots int32 [slots], free_count int32 [1]; slots and
+        the free stack are updated in place. ``tokens``: rows of the step's
+        packed tensors. Returns ``plan`` (a new one if None)."""
+        import torch
+        if plan is None:
+            plan = self.new_plan()
+        elif plan.words.numel() != self._words or plan.words.device != self.device:
+            raise ValueError("plan: made by a handle of another configuration or device")
+        requests = lengths.numel()
+        for name, t, n in (("lengths", lengths, requests), ("seen", seen, requests), ("slots", slots, requests),
+                           ("free_slots", free_slots, self.slots), ("free_count", free_count, 1)):
+            self._expect(name, t, (n,), torch.int32)
+        self._check(lib().la_packed_plan(self._h, lengths.data_ptr(), seen.data_ptr(), slots.data_ptr(),
+                                         free_slots.data_ptr(), free_count.data_ptr(), plan.words.data_ptr(), requests,
+                                         tokens, self._stream(stream)))
+        plan._set(requests, tokens)
+        return plan
+
+    def _step(self, call, plan, q, k, v, gate, beta, states, out, stream, *more):
+        import torch
+        n = plan.tokens
+        if plan.words.numel() != self._words or plan.words.device != self.device:
+            raise ValueError("plan: made by a handle of another configuration or device")
+        qs = self._rows("q", q, n, self.H_k, self.d_k)
+        ks = self._rows("k", k, n, self.H_k, self.d_k)
+        vs = self._rows("v", v, n, self.H_v, self.d_v)
+        self._expect("gate", gate, (n, self.H_v), torch.float32)
+        self._expect("beta", beta, (n, self.H_v), torch.float32)
+        self._expect("states", states, (self.slots, self.H_v, self.d_v, self.d_k), torch.float32)
+        if out is None:
+            if stream is None:
+                out = torch.empty((n, self.H_v, self.d_v), dtype=self.dtype, device=self.device)
+            else:
+                with torch.cuda.stream(stream):   # the memory belongs to the stream that writes it
+                    out = torch.empty((n, self.H_v, self.d_v), dtype=self.dtype, device=self.device)
+        else:
+            self._expect("out", out, (n, self.H_v, self.d_v), self.dtype)
+        self._check(call(self._h, plan.words.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
+                         beta.data_ptr(), states.data_ptr(), out.data_ptr(), plan.requests, n, qs, ks, vs, *more,
+                         self._stream(stream)))
+        return out
+
+    def forward(self, plan, q, k, v, gate, beta, states, *, chunk=0, out=None, stream=None):
+        """Every token of every request of the plan: q, k [tokens, H_k, d_k],
+        v [tokens, H_v, d_v] (rows may be strided), gate, beta fp32 [tokens,
+        H_v], states fp32 [slots, H_v, d_v, d_k] updated in place. Returns out
+        [tokens, H_v, d_v]; rows of no request are not written. ``chunk``: 0
+        the default, 1 token by token, 32 in blocks."""
+        return self._step(lib().la_packed_forward, plan, q, k, v, gate, beta, states, out, stream, chunk)
+
+    def decode_step(self, plan, q, k, v, gate, beta, states, *, out=None, stream=None):
+        """The same for one or a few tokens per request: token by token, each
+        state read and written once."""
+        return self._step(lib().la_packed_decode_step, plan, q, k, v, gate, beta, states, out, stream)
+
+    def last_launches(self) -> int:
+        """Kernels the last call enqueued."""
+        return lib().la_packed_last_launches(self._h)
+
+    def status(self, stream=None) -> int:
+        """Synchronize the stream and return (and clear) the device status."""
+        return lib().la_packed_status(self._h, self._stream(stream))

@@ -1,0 +1,261 @@
+// C ABI of the packed gated delta rule (declared in include/la.h): argument
+// validation and kernel selection. The handle holds the configuration and one
+// device status word; plans, states and tensors are the caller's.
+#include <cstdint>
+#include <cstdio>
+#include <new>
+
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include "../../include/la.h"
+#include "kernels.h"
+#include "packed.h"
+
+struct la_packed {
+    la_packed_config cfg;
+    la::packed::PlanLayout lay;
+    int sm_count;
+    int* d_status;
+    PFN_cuTensorMapEncodeTiled_v12000 encode;
+    char last_error[256];
+    int last_launches;
+};
+
+namespace {
+
+using la::packed::PlanLayout;
+using la::packed::StepArgs;
+
+int fail(la_packed* h, int code, const char* msg) {
+    std::snprintf(h->last_error, sizeof(h->last_error), "%s", msg);
+    return code;
+}
+int fail_for(la_packed* h, int code, const char* name, const char* msg) {
+    std::snprintf(h->last_error, sizeof(h->last_error), "%s %s", name, msg);
+    return code;
+}
+int cuda_fail(la_packed* h, cudaError_t e, const char* what) {
+    std::snprintf(h->last_error, sizeof(h->last_error), "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+    return LA_ERR_CUDA;
+}
+
+bool supported_d(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Make the handle's device current for the duration of a call.
+struct DeviceGuard {
+    int prev = -1;
+    bool ok = false;
+    explicit DeviceGuard(int dev) {
+        if (cudaGetDevice(&prev) != cudaSuccess) return;
+        ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
+    }
+    ~DeviceGuard() {
+        int cur = -1;
+        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+    }
+};
+
+// What a configuration has to satisfy; LA_OK or the error.
+int check_config(const la_packed_config* c) {
+    if (!c) return LA_ERR_INVALID_ARG;
+    if (c->max_requests < 1 || c->max_tokens < 1 || c->slots < 1 || c->H_k < 1 || c->H_v < 1) return LA_ERR_INVALID_ARG;
+    if (c->H_v % c->H_k) return LA_ERR_INVALID_ARG;
+    if (c->io != LA_BF16 && c->io != LA_FP32) return LA_ERR_INVALID_ARG;
+    if (c->flags) return LA_ERR_INVALID_ARG;
+    if (!supported_d(c->d_k) || !supported_d(c->d_v)) return LA_ERR_UNSUPPORTED;
+    if (c->max_requests > la::packed::kMaxRequests || c->max_tokens > la::packed::kMaxTokens) return LA_ERR_UNSUPPORTED;
+    if (c->slots > (1 << 28) || c->H_v > 4096) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+int run_step(la_packed* h, const int* plan, const void* q, const void* k, const void* v, const float* gate,
+             const float* beta, float* states, void* out, int requests, int tokens, long long q_stride,
+             long long k_stride, long long v_stride, int chunk, void* cuda_stream) {
+    if (!h) return LA_ERR_INVALID_ARG;
+    h->last_error[0] = 0;
+    h->last_launches = 0;
+    const la_packed_config& c = h->cfg;
+    if (requests < 0 || tokens < 0) return fail(h, LA_ERR_INVALID_ARG, "requests and tokens must be >= 0");
+    if (requests > c.max_requests || tokens > c.max_tokens)
+        return fail(h, LA_ERR_INVALID_ARG, "requests or tokens above the handle's maxima");
+    if (chunk != 0 && chunk != 1 && chunk != la::packed::kBlock)
+        return fail(h, LA_ERR_UNSUPPORTED, "chunk must be 0 (default), 1 (recurrent) or 32");
+    const bool blocks_ok = c.io == LA_BF16 && c.d_k >= 64 && c.d_v >= 64;
+    if (chunk == la::packed::kBlock && !blocks_ok)
+        return fail(h, LA_ERR_UNSUPPORTED, "chunk 32 needs bf16 io and d_k, d_v in {64, 128}");
+    if (requests == 0 || tokens == 0) return LA_OK;
+    const void* ptrs[] = {plan, q, k, v, gate, beta, states, out};
+    const char* names[] = {"plan", "q", "k", "v", "gate", "beta", "states", "out"};
+    for (int i = 0; i < 8; ++i) {
+        if (!ptrs[i]) return fail_for(h, LA_ERR_INVALID_ARG, names[i], "is required");
+        const bool scalars = i == 4 || i == 5;   // gate, beta: read one by one, so any row of them may come first
+        if (scalars ? (reinterpret_cast<uintptr_t>(ptrs[i]) & 3u) != 0 : !aligned16(ptrs[i]))
+            return fail_for(h, LA_ERR_MISALIGNED, names[i], scalars ? "is not 4-byte aligned" : "is not 16-byte aligned");
+    }
+    const long long es = c.io == LA_BF16 ? 2 : 4;
+    const long long strides[] = {q_stride, k_stride, v_stride};
+    const long long least[] = {static_cast<long long>(c.H_k) * c.d_k, static_cast<long long>(c.H_k) * c.d_k,
+                               static_cast<long long>(c.H_v) * c.d_v};
+    for (int i = 0; i < 3; ++i) {
+        if (strides[i] < least[i]) return fail_for(h, LA_ERR_INVALID_ARG, names[1 + i], "has rows that overlap");
+        if (strides[i] > (1LL << 32)) return fail_for(h, LA_ERR_UNSUPPORTED, names[1 + i], "has rows too far apart");
+        if (strides[i] * es % 16) return fail_for(h, LA_ERR_MISALIGNED, names[1 + i], "has rows that are not 16-byte aligned");
+    }
+    StepArgs a;
+    a.plan = plan;
+    a.lay = h->lay;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.gate = gate;
+    a.beta = beta;
+    a.states = states;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.requests = requests;
+    a.rows = tokens;
+    a.Hk = c.H_k;
+    a.Hv = c.H_v;
+    a.dk = c.d_k;
+    a.dv = c.d_v;
+    a.io = c.io == LA_FP32 ? la::kFp32 : la::kBf16;
+    a.sm_count = h->sm_count;
+    a.status = h->d_status;
+    DeviceGuard g(c.device);
+    if (!g.ok) return fail(h, LA_ERR_CUDA, "cannot select the handle's device");
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    const cudaError_t e = chunk != 1 && blocks_ok ? la::packed::launch_chunk(a, s, h->encode) : la::packed::launch_step(a, s);
+    if (e != cudaSuccess) return cuda_fail(h, e, chunk != 1 && blocks_ok ? "packed prefill launch" : "packed step launch");
+    h->last_launches = 1;
+    return LA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+long long la_packed_plan_words(const la_packed_config* cfg) {
+    if (check_config(cfg) != LA_OK) return 0;
+    return static_cast<long long>(PlanLayout{cfg->max_requests, cfg->max_tokens, cfg->slots}.words());
+}
+
+int la_packed_create(const la_packed_config* cfg, la_packed** out) {
+    if (!out) return LA_ERR_INVALID_ARG;
+    *out = nullptr;
+    const int rc = check_config(cfg);
+    if (rc != LA_OK) return rc;
+    int ndev = 0;
+    if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) {
+        cudaGetLastError();
+        return LA_ERR_CUDA;
+    }
+    if (cfg->device < 0 || cfg->device >= ndev) return LA_ERR_INVALID_ARG;
+    cudaDeviceProp prop;
+    if (cudaGetDeviceProperties(&prop, cfg->device) != cudaSuccess) return LA_ERR_CUDA;
+    if (!(prop.major == 10 && prop.minor == 3)) return LA_ERR_UNSUPPORTED;   // built for sm_103a only
+    la_packed* h = new (std::nothrow) la_packed();
+    if (!h) return LA_ERR_CUDA;
+    h->cfg = *cfg;
+    h->lay = PlanLayout{cfg->max_requests, cfg->max_tokens, cfg->slots};
+    h->sm_count = prop.multiProcessorCount;
+    h->d_status = nullptr;
+    h->last_launches = 0;
+    h->last_error[0] = 0;
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    DeviceGuard g(cfg->device);
+    if (!g.ok || cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn || cudaMalloc(&h->d_status, sizeof(int)) != cudaSuccess ||
+        cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) {
+        cudaGetLastError();
+        if (h->d_status) cudaFree(h->d_status);
+        delete h;
+        return LA_ERR_CUDA;
+    }
+    h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    *out = h;
+    return LA_OK;
+}
+
+void la_packed_destroy(la_packed* h) {
+    if (!h) return;
+    {
+        DeviceGuard g(h->cfg.device);
+        if (h->d_status) cudaFree(h->d_status);
+    }
+    delete h;
+}
+
+int la_packed_plan(la_packed* h, const int* lengths, const int* seen, int* slots, int* free_slots, int* free_count,
+                   int* plan, int requests, int tokens, void* cuda_stream) {
+    if (!h) return LA_ERR_INVALID_ARG;
+    h->last_error[0] = 0;
+    h->last_launches = 0;
+    const la_packed_config& c = h->cfg;
+    if (requests < 0 || tokens < 0) return fail(h, LA_ERR_INVALID_ARG, "requests and tokens must be >= 0");
+    if (requests > c.max_requests || tokens > c.max_tokens)
+        return fail(h, LA_ERR_INVALID_ARG, "requests or tokens above the handle's maxima");
+    const void* ptrs[] = {lengths, seen, slots, free_slots, free_count, plan};
+    const char* names[] = {"lengths", "seen", "slots", "free_slots", "free_count", "plan"};
+    for (int i = 0; i < 6; ++i) {
+        if (!ptrs[i] && (i >= 3 || requests > 0)) return fail_for(h, LA_ERR_INVALID_ARG, names[i], "is required");
+        if (reinterpret_cast<uintptr_t>(ptrs[i]) & 3u) return fail_for(h, LA_ERR_MISALIGNED, names[i], "is not 4-byte aligned");
+    }
+    if (!aligned16(plan)) return fail(h, LA_ERR_MISALIGNED, "plan is not 16-byte aligned");
+    la::packed::PlanArgs a;
+    a.lengths = lengths;
+    a.seen = seen;
+    a.slots = slots;
+    a.free_slots = free_slots;
+    a.free_count = free_count;
+    a.plan = plan;
+    a.lay = h->lay;
+    a.requests = requests;
+    a.rows = tokens;
+    DeviceGuard g(c.device);
+    if (!g.ok) return fail(h, LA_ERR_CUDA, "cannot select the handle's device");
+    const cudaError_t e = la::packed::launch_plan(a, static_cast<cudaStream_t>(cuda_stream));
+    if (e != cudaSuccess) return cuda_fail(h, e, "plan launch");
+    h->last_launches = 1;
+    return LA_OK;
+}
+
+int la_packed_forward(la_packed* h, const int* plan, const void* q, const void* k, const void* v, const float* gate,
+                      const float* beta, float* states, void* out, int requests, int tokens, long long q_stride,
+                      long long k_stride, long long v_stride, int chunk, void* cuda_stream) {
+    return run_step(h, plan, q, k, v, gate, beta, states, out, requests, tokens, q_stride, k_stride, v_stride, chunk,
+                    cuda_stream);
+}
+
+int la_packed_decode_step(la_packed* h, const int* plan, const void* q, const void* k, const void* v,
+                          const float* gate, const float* beta, float* states, void* out, int requests, int tokens,
+                          long long q_stride, long long k_stride, long long v_stride, void* cuda_stream) {
+    return run_step(h, plan, q, k, v, gate, beta, states, out, requests, tokens, q_stride, k_stride, v_stride, 1,
+                    cuda_stream);
+}
+
+int la_packed_status(la_packed* h, void* cuda_stream) {
+    if (!h) return LA_ERR_INVALID_ARG;
+    DeviceGuard g(h->cfg.device);
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream));
+    if (e != cudaSuccess) return cuda_fail(h, e, "stream synchronize");
+    int word = 0;
+    e = cudaMemcpy(&word, h->d_status, sizeof(int), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail(h, e, "status read");
+    if (word != 0) {
+        e = cudaMemset(h->d_status, 0, sizeof(int));
+        if (e != cudaSuccess) return cuda_fail(h, e, "status clear");
+        return fail(h, LA_ERR_TIMEOUT, "a bounded device wait expired");
+    }
+    return LA_OK;
+}
+
+const char* la_packed_last_error(const la_packed* h) { return h ? h->last_error : "null handle"; }
+
+int la_packed_last_launches(const la_packed* h) { return h ? h->last_launches : 0; }
+
+}  // extern "C"

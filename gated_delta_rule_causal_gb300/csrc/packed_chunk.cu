@@ -1,0 +1,563 @@
+// The gated delta rule over packed requests in blocks of 32 tokens: bf16 q, k
+// and v, fp32 states in a pool.
+//
+// Per value head (key head h * Hk / Hv), state X [dv][dk] at a block's start,
+// tokens t, j of the block, g and b the gates:
+//   D_tj = prod_{j < s <= t} g_s,  G_t = prod_{s <= t} g_s
+//   A_tj = b_t D_tj k_t.k_j  (j < t),   T = (I + A)^-1,   P_tj = D_tj q_t.k_j  (j <= t)
+//   R = diag(b) (V - diag(G) K X^T),   U = T R             [token][dv]
+//   O = diag(G) Q X^T + P U,           X <- G_31 X + U^T diag(D_31,.) K
+// The decays are running products, never quotients or logarithms: any gate,
+// zero among them, gives what the recurrence gives.
+//
+// Work split. One CTA per (request, value head, 64 rows of the state), longest
+// requests first: rows of the state are independent. Four chain warps own 16
+// rows each, for the whole request. With X^T's products written as
+// [dv][token], a warp's accumulators (X, Z = X K^T, R, U) turn into the next
+// product's A operand inside its own registers, so from the state's load to
+// its store the chain exchanges nothing between warps. K, Q, V tiles come by
+// TMA into a ring of three stages; two prep warps compute T and P of a block
+// each, ahead of the chain. The last chain warp to leave a stage issues the
+// loads that reuse it.
+//
+// Precision. q, k, v are bf16 and enter the MMAs as they are. What the state
+// depends on (X in K X^T, R and T in T R, U in U^T K) is split into two bf16
+// parts, high and low, whose sum is off by at most 2^-16 of the value;
+// products of two low parts (2^-16 again) are dropped. Measured: states off by
+// 3.6e-6 of themselves against float64 (one part alone: about 2e-3). What only an output depends on, rounded to bf16 itself,
+// keeps one part where the other factor is exact: X in Q X^T, P in P U.
+// Accumulators, gates, A and the inverse are fp32.
+//
+// Rows past a request's end belong to the next request: they are zeroed in the
+// tiles before anything reads them, with gate 1 and beta 0, and are not
+// written.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "launch.cuh"
+#include "packed.h"
+#include "ptx.cuh"
+
+namespace la {
+namespace packed {
+namespace {
+
+constexpr int C = kBlock;
+constexpr int kChain = 4;                  // chain warps: 16 state rows each
+constexpr int kRows = 16 * kChain;         // state rows of a CTA
+constexpr int kPrep = 2;                   // prep warps
+constexpr int kThreads = 32 * (kChain + kPrep);
+constexpr int kStages = 3;
+constexpr int kTStride = 80;               // bytes per row of a 32x32 bf16 tile: 16-byte chunks of 8 rows hit all banks
+constexpr int kSStride = 40;               // floats per row of the prep warps' 32x32 fp32 scratch
+
+template <int DK>
+struct Layout {
+    static constexpr int KA = DK / 64;                       // 64-channel atoms of [32][64] bf16, 4 KB, 128-byte swizzle
+    static constexpr uint32_t K = 0;
+    static constexpr uint32_t Q = K + KA * 4096;
+    static constexpr uint32_t V = Q + KA * 4096;             // [32][64]: the CTA's own rows of the state
+    static constexpr uint32_t TX = V + 4096;                 // bytes a stage's loads bring
+    static constexpr uint32_t TH = TX;                       // T, high and low parts, [t][j]
+    static constexpr uint32_t TL = TH + C * kTStride;
+    static constexpr uint32_t P = TL + C * kTStride;
+    static constexpr uint32_t VEC = P + C * kTStride;        // fp32: b, b G, G, D_31 [32 each]
+    static constexpr uint32_t STAGE = (VEC + 4 * C * 4 + 1023) / 1024 * 1024;
+    static constexpr uint32_t SCRATCH = kStages * STAGE;     // per prep warp: K K^T and Q K^T, fp32
+    static constexpr uint32_t BAR = SCRATCH + kPrep * 2 * C * kSStride * 4;
+    static constexpr uint32_t BYTES = BAR + 128;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// D (16x8, fp32) += A (16x16) B (16x8), bf16. With g = lane / 4, c = lane % 4:
+// A: a0 (g, 2c..), a1 (g + 8, 2c..), a2 (g, 2c + 8..), a3 (g + 8, 2c + 8..);
+// B: b0 (2c.., g), b1 (2c + 8.., g); D: d0, d1 (g, 2c..), d2, d3 (g + 8, 2c..).
+// So the D tiles of columns 16i and 16i + 8 are the A fragment of columns
+// 16i .. 16i + 15, packed.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo, both bf16, |x - hi - lo| <= 2^-16 |x|; a pair at a time.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16(x, y);
+    lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+__device__ __forceinline__ void split_tiles(const float (&x)[4], const float (&y)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    split2(x[0], x[1], hi[0], lo[0]);
+    split2(x[2], x[3], hi[1], lo[1]);
+    split2(y[0], y[1], hi[2], lo[2]);
+    split2(y[2], y[3], hi[3], lo[3]);
+}
+// 8x8 b16 matrix spread over the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, __nv_bfloat16 x) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(x)) : "memory");
+}
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(addr), "r"(0) : "memory");
+}
+
+struct Item {
+    int head, khead, split;
+    Request rq;
+    int blocks;
+};
+
+// ---------------------------------------------------------------- prep warps
+// T (two bf16 parts), P and the gate vectors of blocks pw, pw + kPrep, ...
+template <int DK>
+__device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uint8_t* sm, uint32_t sbase, int pw,
+                                          uint64_t* full, uint64_t* ready, volatile int* abort_flag) {
+    using L = Layout<DK>;
+    const int lane = threadIdx.x & 31, gq = lane >> 2, cq = lane & 3;
+    float* kk = reinterpret_cast<float*>(sm + L::SCRATCH) + pw * 2 * C * kSStride;   // raw K K^T, then A
+    float* qk = kk + C * kSStride;                                                   // raw Q K^T
+    // A fragment rows of an m16 x k16 tile by ldmatrix: lane -> row, 16-byte chunk
+    const int fr = (lane & 7) + ((lane >> 3) & 1) * 8, fc = lane >> 4;
+    auto gates = [&](int c, float& g, float& b) {   // token `lane` of block c; gate 1, beta 0 past the end
+        const int t = c * C + lane;
+        g = 1.f;
+        b = 0.f;
+        if (t < it.rq.len) {
+            const size_t i = static_cast<size_t>(it.rq.row0 + t) * a.Hv + it.head;
+            g = __ldg(a.gate + i);
+            b = __ldg(a.beta + i);
+        }
+    };
+    float gn, bn;
+    gates(pw, gn, bn);
+    for (int c = pw; c < it.blocks; c += kPrep) {
+        const int s = c % kStages;
+        const uint32_t st = sbase + s * L::STAGE;
+        const float g = gn, b = bn;
+        gates(c + kPrep, gn, bn);
+        bool ok = mbar_wait_or_abort(&full[s], (c / kStages) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return;
+        const int n = it.rq.len - c * C;   // tokens of the block
+        if (n < C) {                       // rows of the next request (or past the tensor): zero
+            for (int i = lane; i < (C - n) * 8; i += 32) {
+                const uint32_t o = sw128_off(n + i / 8, i % 8);
+#pragma unroll
+                for (int at = 0; at < L::KA; ++at) {
+                    st_shared_zero16(st + L::K + at * 4096 + o);
+                    st_shared_zero16(st + L::Q + at * 4096 + o);
+                }
+                st_shared_zero16(st + L::V + o);
+            }
+            __syncwarp();
+        }
+        // ---- K K^T and Q K^T, lower tiles only; a key fragment serves as A and as B ----
+        float dk[6][4] = {}, dq[6][4] = {};   // tiles (m, n): (0,0) (0,1) (1,0) (1,1) (1,2) (1,3)
+#pragma unroll
+        for (int x = 0; x < DK / 16; ++x) {
+            uint32_t k0[4], k1[4], q0[4], q1[4];
+            const uint32_t at = (x / 4) * 4096, ch = (x % 4) * 2 + fc;
+            ldsm4(k0, st + L::K + at + sw128_off(fr, ch));
+            ldsm4(k1, st + L::K + at + sw128_off(16 + fr, ch));
+            ldsm4(q0, st + L::Q + at + sw128_off(fr, ch));
+            ldsm4(q1, st + L::Q + at + sw128_off(16 + fr, ch));
+            mma(dk[0], k0, k0[0], k0[2]);
+            mma(dk[1], k0, k0[1], k0[3]);
+            mma(dk[2], k1, k0[0], k0[2]);
+            mma(dk[3], k1, k0[1], k0[3]);
+            mma(dk[4], k1, k1[0], k1[2]);
+            mma(dk[5], k1, k1[1], k1[3]);
+            mma(dq[0], q0, k0[0], k0[2]);
+            mma(dq[1], q0, k0[1], k0[3]);
+            mma(dq[2], q1, k0[0], k0[2]);
+            mma(dq[3], q1, k0[1], k0[3]);
+            mma(dq[4], q1, k1[0], k1[2]);
+            mma(dq[5], q1, k1[1], k1[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            const int row = (i < 2 ? 0 : 16) + gq, col = (i < 2 ? i : i - 2) * 8 + 2 * cq;
+            *reinterpret_cast<float2*>(kk + row * kSStride + col) = make_float2(dk[i][0], dk[i][1]);
+            *reinterpret_cast<float2*>(kk + (row + 8) * kSStride + col) = make_float2(dk[i][2], dk[i][3]);
+            *reinterpret_cast<float2*>(qk + row * kSStride + col) = make_float2(dq[i][0], dq[i][1]);
+            *reinterpret_cast<float2*>(qk + (row + 8) * kSStride + col) = make_float2(dq[i][2], dq[i][3]);
+        }
+        __syncwarp();
+        // ---- A and P, lane j takes column j: D_tj is its running product ------------------
+        float d = 0.f;
+#pragma unroll
+        for (int t = 0; t < C; ++t) {
+            const float gt = __shfl_sync(0xffffffffu, g, t), bt = __shfl_sync(0xffffffffu, b, t);
+            d = t == lane ? 1.f : d * gt;   // zero above the diagonal
+            const float p = t >= lane ? d * qk[t * kSStride + lane] : 0.f;
+            const float ax = t > lane ? bt * d * kk[t * kSStride + lane] : 0.f;
+            st_shared_u16(st + L::P + t * kTStride + 2 * lane, __float2bfloat16_rn(p));
+            kk[t * kSStride + lane] = ax;
+        }
+        float G = g;   // product of the gates up to token `lane`
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, G, o);
+            if (lane >= o) G *= y;
+        }
+        float* vec = reinterpret_cast<float*>(sm + s * L::STAGE + L::VEC);
+        vec[lane] = b;
+        vec[C + lane] = b * G;
+        vec[2 * C + lane] = G;
+        vec[3 * C + lane] = d;
+        __syncwarp();
+        // ---- T = (I + A)^-1 by forward substitution, lane j takes column j ------------------
+        float x[C];
+#pragma unroll
+        for (int t = 0; t < C; ++t) {
+            float s0 = t == lane ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int i = 0; i < t; i += 4) {
+                const float4 r = *reinterpret_cast<const float4*>(kk + t * kSStride + i);
+                s0 -= r.x * x[i];
+                if (i + 1 < t) s1 -= r.y * x[i + 1];
+                if (i + 2 < t) s2 -= r.z * x[i + 2];
+                if (i + 3 < t) s3 -= r.w * x[i + 3];
+            }
+            x[t] = (s0 + s1) + (s2 + s3);
+        }
+#pragma unroll
+        for (int t = 0; t < C; ++t) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(x[t]);
+            st_shared_u16(st + L::TH + t * kTStride + 2 * lane, hi);
+            st_shared_u16(st + L::TL + t * kTStride + 2 * lane, __float2bfloat16_rn(x[t] - __bfloat162float(hi)));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ready[s]);
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 2)
+chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+             const __grid_constant__ CUtensorMap tmv, const StepArgs a) {
+    using L = Layout<DK>;
+    constexpr int NT = DK / 8;   // n-tiles of a warp's state rows
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t* sm = smem_raw + (sbase - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BAR);   // [kStages] TMA: a block's tiles have arrived
+    uint64_t* ready = full + kStages;                            // [kStages] prep: T, P and vectors are written
+    int* left = reinterpret_cast<int*>(ready + kStages);         // [kStages] chain warps that have left the stage
+    volatile int* issued = left + kStages;                       // blocks whose loads were issued
+    volatile int* abort_flag = left + kStages + 1;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&ready[i], 1);
+            left[i] = 0;
+        }
+        *issued = 0;
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmq);
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
+    griddep_wait();
+    Item it;
+    {
+        const int splits = a.dv / kRows;
+        const int per_req = a.Hv * splits;
+        const int rank = blockIdx.x / per_req, hs = blockIdx.x % per_req;
+        if (rank >= plan_requests(a)) return;
+        const int r = a.plan[a.lay.order() + rank];
+        if (r < 0 || r >= plan_requests(a) || !read_request(a, r, it.rq)) return;
+        it.head = hs / splits;
+        it.split = hs % splits;
+        it.khead = it.head / (a.Hv / a.Hk);
+        it.blocks = (it.rq.len + C - 1) / C;
+    }
+    __syncthreads();
+
+    auto issue = [&](int c) {   // loads of block c (one thread); rows past the tensor read as zeros
+        const int s = c % kStages, row = it.rq.row0 + c * C;
+        uint8_t* st = sm + s * L::STAGE;
+        mbar_arrive_expect_tx(&full[s], L::TX);
+#pragma unroll
+        for (int x = 0; x < L::KA; ++x) {
+            tma_load_3d(&tmk, &full[s], st + L::K + x * 4096, x * 64, it.khead, row);
+            tma_load_3d(&tmq, &full[s], st + L::Q + x * 4096, x * 64, it.khead, row);
+        }
+        tma_load_3d(&tmv, &full[s], st + L::V, it.split * kRows, it.head, row);
+        *issued = c + 1;
+    };
+    if (tid == 0)
+        for (int c = 0; c < kStages && c < it.blocks; ++c) issue(c);
+
+    bool failed = false;
+    if (warp >= kChain) {
+        prep_warp<DK>(a, it, sm, sbase, warp - kChain, full, ready, abort_flag);
+    } else {
+        // ======================= chain warp: rows r0 + g and r0 + g + 8 ====================
+        const int gq = lane >> 2, cq = lane & 3;
+        const int r0 = it.split * kRows + 16 * warp;
+        float* sp = a.states + ((static_cast<size_t>(it.rq.slot) * a.Hv + it.head) * a.dv + r0 + gq) * DK + 2 * cq;
+        float X[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float2 u = make_float2(0.f, 0.f), w = u;
+            if (!it.rq.fresh) {
+                u = *reinterpret_cast<const float2*>(sp + 8 * n);
+                w = *reinterpret_cast<const float2*>(sp + 8 * DK + 8 * n);
+            }
+            X[n][0] = u.x;
+            X[n][1] = u.y;
+            X[n][2] = w.x;
+            X[n][3] = w.y;
+        }
+        // ldmatrix lane addresses: B fragments of two n-tiles (rows = n, 16-byte
+        // chunks along k) and, transposed, of K as [k = token][n = channel]
+        const int br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;
+        const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = lane >> 4;
+        __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) +
+                            (static_cast<size_t>(it.rq.row0) * a.Hv + it.head) * a.dv + r0 + 2 * cq;
+        const size_t ostep = static_cast<size_t>(a.Hv) * a.dv;
+
+        for (int c = 0; c < it.blocks; ++c) {
+            const int s = c % kStages;
+            const uint32_t ph = (c / kStages) & 1;
+            const uint32_t st = sbase + s * L::STAGE;
+            bool ok = mbar_wait_or_abort(&full[s], ph, abort_flag) && mbar_wait_or_abort(&ready[s], ph, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) {
+                failed = true;
+                break;
+            }
+            // ---- Z = X K^T (both parts of X), O = X Q^T (the high part) -----------------
+            float Z[4][4] = {}, O[4][4] = {};
+#pragma unroll
+            for (int x = 0; x < DK / 16; ++x) {
+                uint32_t hi[4], lo[4], b0[4], b1[4];
+                split_tiles(X[2 * x], X[2 * x + 1], hi, lo);
+                const uint32_t at = (x / 4) * 4096, ch = (x % 4) * 2 + bc;
+                ldsm4(b0, st + L::K + at + sw128_off(br, ch));
+                ldsm4(b1, st + L::K + at + sw128_off(16 + br, ch));
+                mma(Z[0], hi, b0[0], b0[1]);
+                mma(Z[1], hi, b0[2], b0[3]);
+                mma(Z[2], hi, b1[0], b1[1]);
+                mma(Z[3], hi, b1[2], b1[3]);
+                mma(Z[0], lo, b0[0], b0[1]);
+                mma(Z[1], lo, b0[2], b0[3]);
+                mma(Z[2], lo, b1[0], b1[1]);
+                mma(Z[3], lo, b1[2], b1[3]);
+                ldsm4(b0, st + L::Q + at + sw128_off(br, ch));
+                ldsm4(b1, st + L::Q + at + sw128_off(16 + br, ch));
+                mma(O[0], hi, b0[0], b0[1]);
+                mma(O[1], hi, b0[2], b0[3]);
+                mma(O[2], hi, b1[0], b1[1]);
+                mma(O[3], hi, b1[2], b1[3]);
+            }
+            // ---- R = b (V - G Z), in Z; O scaled by G ------------------------------------
+            const float* vec = reinterpret_cast<const float*>(sm + s * L::STAGE + L::VEC);
+#pragma unroll
+            for (int n = 0; n < 4; n += 2) {
+                uint32_t v4[4];   // (token 8n, row g) (.., row g + 8) (token 8n + 8, ..) (..)
+                ldsm4t(v4, st + L::V + sw128_off(8 * n + (lane & 7) + (lane >> 4) * 8, 2 * warp + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = 8 * (n + i) + 2 * cq;
+                    const float2 b = *reinterpret_cast<const float2*>(vec + t);
+                    const float2 bg = *reinterpret_cast<const float2*>(vec + C + t);
+                    const float2 g = *reinterpret_cast<const float2*>(vec + 2 * C + t);
+                    const float2 vl = unpack_bf16(v4[2 * i]), vh = unpack_bf16(v4[2 * i + 1]);
+                    float(&z)[4] = Z[n + i];
+                    z[0] = b.x * vl.x - bg.x * z[0];
+                    z[1] = b.y * vl.y - bg.y * z[1];
+                    z[2] = b.x * vh.x - bg.x * z[2];
+                    z[3] = b.y * vh.y - bg.y * z[3];
+                    float(&o)[4] = O[n + i];
+                    o[0] *= g.x;
+                    o[1] *= g.y;
+                    o[2] *= g.x;
+                    o[3] *= g.y;
+                }
+            }
+            // ---- U = R T^T: lower triangular, columns j < 16 reach every t, j >= 16 only t >= 16
+            float U[4][4] = {};
+            {
+                uint32_t h0[4], l0[4], h1[4], l1[4], t0[4], t1[4], t2[4];
+                split_tiles(Z[0], Z[1], h0, l0);
+                split_tiles(Z[2], Z[3], h1, l1);
+                const uint32_t th = st + L::TH + br * kTStride + bc * 16, tl = st + L::TL + br * kTStride + bc * 16;
+                ldsm4(t0, th);                         // t 0..15, j 0..15
+                ldsm4(t1, th + 16 * kTStride);         // t 16..31, j 0..15
+                ldsm4(t2, th + 16 * kTStride + 32);    // t 16..31, j 16..31
+                mma(U[0], h0, t0[0], t0[1]);
+                mma(U[1], h0, t0[2], t0[3]);
+                mma(U[2], h0, t1[0], t1[1]);
+                mma(U[3], h0, t1[2], t1[3]);
+                mma(U[0], l0, t0[0], t0[1]);
+                mma(U[1], l0, t0[2], t0[3]);
+                mma(U[2], l0, t1[0], t1[1]);
+                mma(U[3], l0, t1[2], t1[3]);
+                mma(U[2], h1, t2[0], t2[1]);
+                mma(U[3], h1, t2[2], t2[3]);
+                mma(U[2], l1, t2[0], t2[1]);
+                mma(U[3], l1, t2[2], t2[3]);
+                ldsm4(t0, tl);
+                ldsm4(t1, tl + 16 * kTStride);
+                ldsm4(t2, tl + 16 * kTStride + 32);
+                mma(U[0], h0, t0[0], t0[1]);
+                mma(U[1], h0, t0[2], t0[3]);
+                mma(U[2], h0, t1[0], t1[1]);
+                mma(U[3], h0, t1[2], t1[3]);
+                mma(U[2], h1, t2[0], t2[1]);
+                mma(U[3], h1, t2[2], t2[3]);
+            }
+            // ---- O += U P^T ------------------------------------------------------------
+            {
+                uint32_t h0[4], l0[4], h1[4], l1[4], t0[4], t1[4], t2[4];
+                split_tiles(U[0], U[1], h0, l0);
+                split_tiles(U[2], U[3], h1, l1);
+                const uint32_t tp = st + L::P + br * kTStride + bc * 16;
+                ldsm4(t0, tp);
+                ldsm4(t1, tp + 16 * kTStride);
+                ldsm4(t2, tp + 16 * kTStride + 32);
+                mma(O[0], h0, t0[0], t0[1]);
+                mma(O[1], h0, t0[2], t0[3]);
+                mma(O[2], h0, t1[0], t1[1]);
+                mma(O[3], h0, t1[2], t1[3]);
+                mma(O[0], l0, t0[0], t0[1]);
+                mma(O[1], l0, t0[2], t0[3]);
+                mma(O[2], l0, t1[0], t1[1]);
+                mma(O[3], l0, t1[2], t1[3]);
+                mma(O[2], h1, t2[0], t2[1]);
+                mma(O[3], h1, t2[2], t2[3]);
+                mma(O[2], l1, t2[0], t2[1]);
+                mma(O[3], l1, t2[2], t2[3]);
+            }
+            // ---- X = G_31 X + (U D_31) K ---------------------------------------------------
+            {
+                const float gc = vec[2 * C + C - 1];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 dc = *reinterpret_cast<const float2*>(vec + 3 * C + 8 * n + 2 * cq);
+                    U[n][0] *= dc.x;
+                    U[n][1] *= dc.y;
+                    U[n][2] *= dc.x;
+                    U[n][3] *= dc.y;
+                }
+                uint32_t h0[4], l0[4], h1[4], l1[4];
+                split_tiles(U[0], U[1], h0, l0);
+                split_tiles(U[2], U[3], h1, l1);
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t b0[4], b1[4];
+                    const uint32_t at = st + L::K + (n / 8) * 4096, ch = n % 8 + tc;
+                    ldsm4t(b0, at + sw128_off(tr, ch));
+                    ldsm4t(b1, at + sw128_off(16 + tr, ch));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        X[n][i] *= gc;
+                        X[n + 1][i] *= gc;
+                    }
+                    mma(X[n], h0, b0[0], b0[1]);
+                    mma(X[n + 1], h0, b0[2], b0[3]);
+                    mma(X[n], h1, b1[0], b1[1]);
+                    mma(X[n + 1], h1, b1[2], b1[3]);
+                    mma(X[n], l0, b0[0], b0[1]);
+                    mma(X[n + 1], l0, b0[2], b0[3]);
+                    mma(X[n], l1, b1[0], b1[1]);
+                    mma(X[n + 1], l1, b1[2], b1[3]);
+                }
+            }
+            // this warp has read the stage: the last one to say so reloads it
+            __syncwarp();
+            if (lane == 0) {
+                int before;
+                asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(&left[s])) : "memory");
+                if (before == kChain - 1 && c + kStages < it.blocks) {
+                    left[s] = 0;
+                    issue(c + kStages);
+                }
+            }
+            // ---- output: [dv][token] fragments to [token][dv] pairs -------------------------
+            const int nv = it.rq.len - c * C;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const uint32_t y0 = transpose8x8(pack_bf16(O[n][0], O[n][1]));   // token 8n + g, rows 2c, 2c + 1
+                const uint32_t y1 = transpose8x8(pack_bf16(O[n][2], O[n][3]));   // rows 8 + 2c, ..
+                if (8 * n + gq < nv) {
+                    __nv_bfloat16* o = op + static_cast<size_t>(c * C + 8 * n + gq) * ostep;
+                    *reinterpret_cast<uint32_t*>(o) = y0;
+                    *reinterpret_cast<uint32_t*>(o + 8) = y1;
+                }
+            }
+        }
+        if (!failed) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                *reinterpret_cast<float2*>(sp + 8 * n) = make_float2(X[n][0], X[n][1]);
+                *reinterpret_cast<float2*>(sp + 8 * DK + 8 * n) = make_float2(X[n][2], X[n][3]);
+            }
+        } else if (lane == 0) {
+            *abort_flag = 1;
+            atomicOr(a.status, kStatusTmaWait);
+        }
+    }
+    if (failed) {   // let the loads in flight land before the CTA leaves (bounded)
+        if (lane == 0)
+            for (int c = max(0, *issued - kStages); c < *issued; ++c)
+                mbar_wait(&full[c % kStages], (c / kStages) & 1, 100000000ull);
+    }
+}
+
+// 3-D map over a packed tensor [rows][H][d], rows `stride` elements apart:
+// boxes of 32 rows of one head's 64 channels, 128-byte swizzle.
+bool make_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, int d, int H, int rows,
+              long long stride) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[3] = {64, 1, C};
+    cuuint32_t one[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK>
+cudaError_t run(const StepArgs& a, cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v) {
+    constexpr uint32_t smem = Layout<DK>::BYTES + 1024;
+    static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
+    const cudaError_t e = cudaFuncSetAttribute(chunk_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long grid = static_cast<long long>(a.requests) * a.Hv * (a.dv / kRows);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_pdl(chunk_kernel<DK>, static_cast<unsigned>(grid), kThreads, smem, s, q, k, v, a);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk(const StepArgs& a, cudaStream_t s, PFN_cuTensorMapEncodeTiled_v12000 enc) {
+    CUtensorMap q, k, v;
+    if (!make_map(enc, &q, a.q, a.dk, a.Hk, a.rows, a.q_stride) || !make_map(enc, &k, a.k, a.dk, a.Hk, a.rows, a.k_stride) ||
+        !make_map(enc, &v, a.v, a.dv, a.Hv, a.rows, a.v_stride))
+        return cudaErrorInvalidValue;
+    if (a.dk == 64) return run<64>(a, s, q, k, v);
+    if (a.dk == 128) return run<128>(a, s, q, k, v);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace packed
+}  // namespace la

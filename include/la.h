@@ -364,6 +364,140 @@ int la_backward_gated(la_handle* h, const void* q, const void* k, const void* v,
  * the forward's + 2 for LA_NORM_DECAY). */
 int la_last_launches(const la_handle* h);
 
+/* ------------------------------------------------------------------------
+ * The gated delta rule over packed requests (serving).
+ *
+ * A step works on R requests whose tokens lie behind each other, token-major,
+ * in packed tensors of N rows: request r's rows are offsets[r] ..
+ * offsets[r + 1] - 1. Its state lives in a slot of a pool and is updated in
+ * place. H_v value heads share H_k key heads (value head h reads key head
+ * h / (H_v / H_k)). For each value head the recurrence of LA_GDN:
+ *   S_t = g_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,  o_t = S_t q_t.
+ *
+ *   q, k       [N, H_k, d_k]   io dtype; rows q_stride (k_stride) elements
+ *   v          [N, H_v, d_v]   (v_stride) apart, a multiple of 16 bytes, at
+ *                              least a row's own extent: slices of one
+ *                              projection's rows need no copy
+ *   gate, beta [N, H_v]        fp32, contiguous. Any finite value (the gate
+ *                              enters as a factor, zero included)
+ *   out        [N, H_v, d_v]   io dtype, contiguous; written only in rows of
+ *                              requests that take part
+ *   states     [slots, H_v, d_v, d_k] fp32; only the slots of requests that
+ *                              take part are read or written
+ * Keys are assumed to have unit L2 norm. No input may overlap out or states.
+ * A NaN or infinity in a request's rows stays with that request.
+ *
+ * A step is a plan, made on the GPU from the requests' lengths, then one or
+ * more calls that read it (one per layer, each with its own states and
+ * tensors). Sizes that change from step to step (the lengths, the slots) are
+ * read on the device, so a captured graph of a step replays with new ones.
+ * Pointers, ownership, streams and errors are as for the calls above: the
+ * caller owns every buffer, the plan among them, and the library allocates
+ * nothing after la_packed_create. Calls on one handle may overlap on the GPU
+ * (different streams) if they use different plans, outputs and state slots.
+ */
+typedef struct la_packed la_packed;
+
+typedef struct {
+    int max_requests; /* R at most: 1 .. 16384 */
+    int max_tokens;   /* N at most: 1 .. 2^24 */
+    int slots;        /* states in a pool, >= 1 */
+    int H_k;          /* key/query heads */
+    int H_v;          /* value heads, a multiple of H_k */
+    int d_k;          /* 16, 32, 64 or 128 */
+    int d_v;          /* 16, 32, 64 or 128 */
+    la_dtype io;      /* dtype of q, k, v, out */
+    unsigned flags;   /* 0 */
+    int device;       /* CUDA device ordinal the handle is bound to */
+} la_packed_config;
+
+/* int32 words of a plan buffer of this configuration (0: not a valid one). */
+long long la_packed_plan_words(const la_packed_config* cfg);
+
+/* Create / destroy a handle (one device status word; NULL may be destroyed). */
+int la_packed_create(const la_packed_config* cfg, la_packed** out);
+void la_packed_destroy(la_packed* h);
+
+/* Word offsets of a plan's sections (R = max_requests, N = max_tokens). */
+#define LA_PLAN_PAD(n) (((long long)(n) + 3) / 4 * 4)
+#define LA_PLAN_COUNTS 0                                             /* [4] */
+#define LA_PLAN_OFFSETS 8                                            /* [R + 1] */
+#define LA_PLAN_SLOTS(R) (LA_PLAN_OFFSETS + LA_PLAN_PAD((R) + 1))    /* [R] */
+#define LA_PLAN_ORDER(R) (LA_PLAN_SLOTS(R) + LA_PLAN_PAD(R))         /* [R] */
+#define LA_PLAN_TOKEN_REQUEST(R) (LA_PLAN_ORDER(R) + 2 * LA_PLAN_PAD(R))               /* [N] */
+#define LA_PLAN_TOKEN_POSITION(R, N) (LA_PLAN_TOKEN_REQUEST(R) + LA_PLAN_PAD(N))       /* [N] */
+
+/* Faults of a plan (bits of counts[3]); the requests concerned take no part. */
+enum {
+    LA_PLAN_FAULT_ROWS = 1,    /* a request's rows end past `tokens` */
+    LA_PLAN_FAULT_FREE = 2,    /* no free slot for a new request */
+    LA_PLAN_FAULT_SLOT = 4,    /* a slot number outside the pool */
+    LA_PLAN_FAULT_OWNER = 8,   /* a slot claimed twice (the lowest request keeps it) */
+    LA_PLAN_FAULT_STATE = 16,  /* a request that has seen tokens but has no slot */
+    LA_PLAN_FAULT_OVERFLOW = 32 /* more slots given back than the pool has */
+};
+
+/*
+ * The plan of a step of `requests` requests over `tokens` packed rows.
+ *   lengths    [requests] int32: tokens of this step; 0: idle, keeps its
+ *              slot; negative: ended, gives its slot back
+ *   seen       [requests] int32: tokens absorbed before this step. 0: the
+ *              request starts from a zero state, whatever its slot holds
+ *   slots      [requests] int32, in and out: the request's state slot, -1 =
+ *              none. A request with tokens, none seen and no slot is given
+ *              one; an ended request's becomes -1
+ *   free_slots [slots] int32, in and out: a stack of free slots, its top at
+ *              free_count - 1. Ended requests' slots are pushed in the
+ *              requests' order, then new requests pop in theirs
+ *   free_count [1] int32, in and out
+ * All are device pointers. Writes to plan (la_packed_plan_words int32, 16-byte
+ * aligned):
+ *   counts[0..3]    rows used, requests taking part, free slots left, faults
+ *   offsets[r]      min(sum of the lengths before r, tokens + 1)
+ *   slots[r]        the request's slot if it takes part (it has tokens, its
+ *                   rows end by `tokens`, and a slot of its own), else -1
+ *   order[r]        the requests, most 32-token blocks first (to a power of
+ *                   two, else in their own order), those without part last
+ *   token_request[i], token_position[i]  for i < tokens: the row's request
+ *                   and its position (seen + index in the request); -1 in
+ *                   rows behind the last request or of one that ends past
+ *                   `tokens`
+ * Every result is independent of the order in which threads run. One launch.
+ */
+int la_packed_plan(la_packed* h, const int* lengths, const int* seen, int* slots, int* free_slots, int* free_count,
+                   int* plan, int requests, int tokens, void* cuda_stream);
+
+/*
+ * Every token of every request of a plan; requests and tokens as given to
+ * la_packed_plan.
+ *   chunk  0 = default: blocks of 32 tokens (bf16, d_k and d_v in {64, 128}),
+ *          else token by token. 1 = token by token. 32 = blocks, or
+ *          LA_ERR_UNSUPPORTED where they cannot be.
+ * The blockwise form keeps the state to a few 10^-6 of itself (q, k and v enter
+ * its matrix products exactly, what the state depends on in two bf16 parts,
+ * 2^-16 each); outputs are off by a few roundings to bf16. A NaN or infinity in
+ * a request's rows may reach that request's outputs from the start of its
+ * 32-token block on. One launch, no workspace.
+ * Errors: LA_ERR_INVALID_ARG (a NULL or rows that overlap, sizes above the
+ * handle's), LA_ERR_MISALIGNED (a pointer or a row not 16-byte aligned; gate
+ * and beta need 4 bytes),
+ * LA_ERR_UNSUPPORTED, LA_ERR_CUDA. requests or tokens 0: nothing to do.
+ */
+int la_packed_forward(la_packed* h, const int* plan, const void* q, const void* k, const void* v, const float* gate,
+                      const float* beta, float* states, void* out, int requests, int tokens, long long q_stride,
+                      long long k_stride, long long v_stride, int chunk, void* cuda_stream);
+
+/* The same for steps of one or a few tokens per request: each state is read
+ * once and written once, token by token (chunk 1). */
+int la_packed_decode_step(la_packed* h, const int* plan, const void* q, const void* k, const void* v,
+                          const float* gate, const float* beta, float* states, void* out, int requests, int tokens,
+                          long long q_stride, long long k_stride, long long v_stride, void* cuda_stream);
+
+/* As la_status, la_last_error and la_last_launches, of a packed handle. */
+int la_packed_status(la_packed* h, void* cuda_stream);
+const char* la_packed_last_error(const la_packed* h);
+int la_packed_last_launches(const la_packed* h);
+
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
 int la_version(void);
 

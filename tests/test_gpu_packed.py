@@ -1,0 +1,554 @@
+"""The packed gated delta rule on the GPU against plain float64 references:
+plans against their definition, exactly; outputs and states within what the
+kernels' roundings can add up to (bounds in _packed.py)."""
+import random
+
+import numpy as np
+import pytest
+
+import _packed as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import gated_delta_rule_causal_gb300 as la  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    la.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ plans
+
+class PlanCase:
+    def __init__(self, lengths, seen, slots, free, count, pool, rows, max_requests=None, max_tokens=None):
+        self.args = (lengths, seen, slots, free, count, pool, rows)
+        R = len(lengths)
+        self.h = la.PackedHandle(max_requests=max_requests or max(R, 1), max_tokens=max_tokens or max(rows, 1), slots=pool,
+                                 H_k=1, H_v=1, d_k=16, d_v=16)
+        self.dev = [i32(lengths), i32(seen), i32(slots), i32(free), i32([count])]
+
+    def run(self, **kw):
+        return self.h.plan(*self.dev, tokens=self.args[-1], **kw)
+
+    def check(self, plan):
+        want = ref.plan(*self.args)
+        torch.cuda.synchronize()
+        for name in ("counts", "offsets", "state_slots", "order", "token_request", "token_position"):
+            assert getattr(plan, name).tolist() == want[name], name
+        assert self.dev[2].tolist() == want["slots"]
+        assert self.dev[3].tolist() == want["free_slots"]
+        assert self.dev[4].tolist() == want["free_count"]
+        return want
+
+
+def serving_case(R, rows, seed, long=False):
+    """Consistent slots: live requests own different ones, the others are free."""
+    rng = random.Random(seed)
+    pool = R + R // 3 + 2
+    perm = list(range(pool))
+    rng.shuffle(perm)
+    lengths, seen, slots = [], [], []
+    left = rows
+    for r in range(R):
+        new = rng.random() < 0.3
+        n = rng.choice((0, 1, 1, 1, 2, 31, 32, 33, 64, 65, 130) if not long else (1, 700, 3, 4096, 64))
+        n = min(n, left)
+        left -= n
+        if not new and rng.random() < 0.15:
+            n = -rng.randint(1, 3)
+        lengths.append(n)
+        seen.append(0 if new else rng.randint(0, 5000))
+        slots.append(-1 if new else perm.pop())
+    lengths[0] += max(0, left - 5) if R > 2 and lengths[0] >= 0 else 0
+    return PlanCase(lengths, seen, slots, perm + [0] * (pool - len(perm)), len(perm), pool, rows)
+
+
+@pytest.mark.parametrize("R,rows", [(1, 1), (1, 5000), (2, 64), (7, 33), (31, 200), (33, 4096), (64, 4097), (1000, 9000),
+                                    (1024, 12345), (1025, 8192), (2500, 30001), (16384, 40000)])
+def test_plan_of_a_serving_step(R, rows):
+    c = serving_case(R, rows, seed=R * 7 + rows)
+    want = c.check(c.run())
+    assert want["counts"][3] == 0
+    assert c.h.last_launches() == 1
+
+
+def test_plan_of_nothing():
+    c = PlanCase([], [], [], [3, 1], 1, 2, 6)
+    want = c.check(c.run())
+    assert want["counts"] == [0, 0, 1, 0] and want["token_request"] == [-1] * 6
+    c = PlanCase([0, 0], [1, 0], [1, -1], [0, 0], 1, 2, 0, max_tokens=4)
+    c.check(c.run())
+
+
+def test_plan_in_a_buffer_of_larger_maxima_leaves_the_rest():
+    c = PlanCase([2, 1], [4, 0], [0, -1], [1, 0, 0], 1, 3, 5, max_requests=50, max_tokens=70)
+    plan = c.h.new_plan()
+    plan.words.fill_(-77)
+    c.check(c.run(plan=plan))
+    plan._set(50, 70)
+    assert plan.offsets[3:].eq(-77).all() and plan.state_slots[2:].eq(-77).all() and plan.order[2:].eq(-77).all()
+    assert plan.token_request[5:].eq(-77).all() and plan.token_position[5:].eq(-77).all()
+
+
+@pytest.mark.parametrize("name,args,faults", [
+    ("rows", ([3, 5, 0, 2], [1, 1, 1, 0], [0, 1, 2, -1], [3, 4, 0, 0, 0], 2, 5, 6), la.LA_PLAN_FAULT_ROWS),
+    ("rows saturate", ([2 ** 31 - 1] * 5, [0] * 5, [-1] * 5, [0, 1, 2, 3, 4], 5, 5, 100), la.LA_PLAN_FAULT_ROWS),
+    ("no free slot", ([1, 2, 3], [0, 0, 0], [-1, -1, -1], [4, 0, 0, 0, 0], 1, 5, 10), la.LA_PLAN_FAULT_FREE),
+    ("outside", ([1, 1, 1, -1], [0, 1, 1, 1], [5, -2, -2 ** 31, 9], [0, 1, 0, 0, 0], 2, 5, 10), la.LA_PLAN_FAULT_SLOT),
+    ("claimed twice", ([1, 1, 1], [1, 1, 1], [2, 2, 2], [0, 1, 3, 0, 0], 3, 5, 10), la.LA_PLAN_FAULT_OWNER),
+    ("given back twice", ([-1, -1, 1], [1, 1, 1], [2, 2, 2], [0, 1, 3, 0, 0], 3, 5, 10), la.LA_PLAN_FAULT_OWNER),
+    ("free and owned", ([1, 4], [0, 3], [-1, 2], [0, 2, 0, 0, 0], 2, 5, 10), la.LA_PLAN_FAULT_OWNER),
+    ("free twice", ([1, 4], [0, 0], [-1, -1], [3, 3, 0, 0, 0], 2, 5, 10), la.LA_PLAN_FAULT_OWNER),
+    ("free holds nonsense", ([1, 4], [0, 0], [-1, -1], [77, -5, 0, 0, 0], 2, 5, 10), la.LA_PLAN_FAULT_SLOT),
+    ("no state", ([1, 4], [9, 0], [-1, 2], [0, 1, 0, 0, 0], 2, 5, 10), la.LA_PLAN_FAULT_STATE),
+    ("overflow", ([-1, -1], [1, 1], [2, 3], [0, 1, 2, 3, 4], 5, 5, 10), la.LA_PLAN_FAULT_OVERFLOW),
+    ("count above the pool", ([1], [0], [-1], [0, 1, 4], 99, 3, 4), la.LA_PLAN_FAULT_SLOT),
+    ("count below zero", ([1], [0], [-1], [0, 1, 4], -99, 3, 4), la.LA_PLAN_FAULT_FREE),
+])
+def test_plan_faults_drop_the_request_alone(name, args, faults):
+    c = PlanCase(*args)
+    want = c.check(c.run())
+    assert want["counts"][3] == faults
+
+
+# ------------------------------------------------------------------ the rule
+
+def handle_for(lens, Hk, Hv, dk, dv, io, pool, extra_rows=0):
+    return la.PackedHandle(max_requests=len(lens), max_tokens=max(1, sum(lens) + extra_rows), slots=pool, H_k=Hk, H_v=Hv,
+                           d_k=dk, d_v=dv, io=io)
+
+
+def draw(lens, Hk, Hv, dk, dv, io, seed, pad=0, extra_rows=0, gates="usual"):
+    """Packed inputs of requests, rows strided by `pad` elements between the tensors' own, and a pool."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    n, rnd = sum(lens) + extra_rows, lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    k = rnd(n, Hk, dk)
+    k = k / k.norm(dim=-1, keepdim=True)
+    x = {}
+    for name, t, w in (("q", rnd(n, Hk, dk), Hk * dk), ("k", k, Hk * dk), ("v", rnd(n, Hv, dv), Hv * dv)):
+        buf = torch.full((n, w + pad), float("nan"), device="cuda", dtype=dt)
+        buf[:, :w] = t.reshape(n, w).to(dt)
+        x[name] = buf[:, :w].view(n, t.shape[1], t.shape[2])
+    x["gate"] = torch.sigmoid(rnd(n, Hv) + 4)
+    x["beta"] = torch.sigmoid(rnd(n, Hv))
+    if gates == "strong":
+        x["gate"] = torch.sigmoid(rnd(n, Hv) * 4)
+    elif gates == "zero":
+        x["gate"][torch.rand(n, Hv, generator=gen, device="cuda") < 0.2] = 0.0
+        x["gate"][torch.rand(n, Hv, generator=gen, device="cuda") < 0.1] = 1e-38
+        x["beta"][torch.rand(n, Hv, generator=gen, device="cuda") < 0.2] = 1.0
+        x["beta"][torch.rand(n, Hv, generator=gen, device="cuda") < 0.2] = 0.0
+    elif gates == "none":
+        x["gate"].fill_(1.0)
+        x["beta"].fill_(1.0)
+    pool = len(lens) + 3
+    x["states"] = rnd(pool, Hv, dv, dk) * 0.5
+    perm = torch.randperm(pool, generator=gen, device="cuda").tolist()
+    x["slots"] = perm[:len(lens)]
+    return x, pool
+
+
+def make_plan(h, lens, seen, slots, rows=None):
+    pool = h.slots
+    return h.plan(i32(lens), i32(seen), i32(slots), i32([0] * pool), i32([0]), tokens=sum(lens) if rows is None else rows)
+
+
+def check(x, lens, seen, states_before, out, io, by_blocks, only=None):
+    """Every request's outputs and state against the references; returns the largest share of a bound used."""
+    worst = 0.0
+    d = lambda t: t.double().cpu().numpy()   # noqa: E731
+    q, k, v, g, b = (d(x[n]) for n in ("q", "k", "v", "gate", "beta"))
+    after, before, o = d(x["states"]), d(states_before), d(out)
+    Hk, Hv = q.shape[1], v.shape[1]
+    row = 0
+    for r, n in enumerate(lens):
+        if n > 0 and (only is None or r in only):
+            s = slice(row, row + n)
+            for h in range(Hv):
+                hk = h * Hk // Hv
+                X0 = before[x["slots"][r], h] if seen[r] else np.zeros_like(before[0, 0])
+                args = (q[s, hk], k[s, hk], v[s, h], g[s, h], b[s, h], X0)
+                want, X, bo, E = ref.rule_by_blocks(*args) if by_blocks else ref.rule_by_tokens(
+                    *args, ref.H if io == "bf16" else ref.F)
+                used = np.max(np.abs(o[s, h] - want) / (bo + 1e-30))
+                assert used <= 1.0, f"request {r} head {h}: output {used:.3g} of its bound"
+                err = np.linalg.norm(after[x["slots"][r], h] - X)
+                assert err <= E, f"request {r} head {h}: state off by {err:.3g}, bound {E:.3g}"
+                worst = max(worst, used, err / (E + 1e-30))
+        row += max(0, n)
+    return worst
+
+
+LENS = [[1], [31, 1, 33], [64, 0, 65, 32], [130, 7, 0, 0, 97, 1], [513]]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=lambda x: "-".join(map(str, x)))
+@pytest.mark.parametrize("Hk,Hv,dk,dv", [(1, 1, 64, 64), (2, 4, 128, 128), (1, 3, 128, 64), (2, 2, 64, 128)])
+def test_prefill_by_blocks(lens, Hk, Hv, dk, dv):
+    x, pool = draw(lens, Hk, Hv, dk, dv, "bf16", seed=sum(lens) + dk, pad=8, extra_rows=3)
+    h = handle_for(lens, Hk, Hv, dk, dv, "bf16", pool, extra_rows=3)
+    seen = [r % 2 * 11 for r in range(len(lens))]
+    plan = make_plan(h, lens, seen, x["slots"], rows=sum(lens) + 3)
+    before = x["states"].clone()
+    out = torch.full((sum(lens) + 3, Hv, dv), -7.5, device="cuda", dtype=torch.bfloat16)
+    h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], out=out, chunk=32)
+    assert h.status() == la.LA_OK and h.last_launches() == 1
+    check(x, lens, seen, before, out, "bf16", True)
+    # rows behind the last request, states of idle requests and of nobody: as they were
+    assert out[sum(lens):].eq(-7.5).all()
+    others = [s for s in range(pool) if s not in [x["slots"][r] for r, n in enumerate(lens) if n > 0]]
+    assert torch.equal(x["states"][others], before[others])
+
+
+@pytest.mark.parametrize("gates", ["strong", "zero", "none"])
+@pytest.mark.parametrize("dk", [64, 128])
+def test_prefill_gates(gates, dk):
+    lens = [70, 129]
+    x, pool = draw(lens, 1, 2, dk, 64, "bf16", seed=5, gates=gates)
+    if gates == "none":   # the same key again and again, and its negative
+        x["k"][:, 0] = x["k"][0, 0]
+        x["k"][1::3, 0] *= -1
+    h = handle_for(lens, 1, 2, dk, 64, "bf16", pool)
+    plan = make_plan(h, lens, [0, 3], x["slots"])
+    before = x["states"].clone()
+    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"])
+    assert h.status() == la.LA_OK
+    check(x, lens, [0, 3], before, out, "bf16", True)
+
+
+@pytest.mark.parametrize("chunk", [1, 32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nothing_leaks_between_requests(bad, chunk):
+    # requests 1 and 3 and the rows behind the last request hold NaN or infinities,
+    # as do the slots of new requests and of nobody
+    lens, Hk, Hv, dk, dv = [37, 5, 50, 20, 33], 2, 2, 64, 128
+    x, pool = draw(lens, Hk, Hv, dk, dv, "bf16", seed=9, extra_rows=40)
+    seen = [0, 1, 6, 1, 0]
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    for a, e in ((starts[1], starts[2]), (starts[3], starts[4]), (starts[5], sum(lens) + 40)):
+        for name in ("q", "k", "v", "gate", "beta"):
+            x[name][a:e] = bad
+    for s in range(pool):
+        if s != x["slots"][2]:
+            x["states"][s] = bad
+    h = handle_for(lens, Hk, Hv, dk, dv, "bf16", pool, extra_rows=40)
+    plan = make_plan(h, lens, seen, x["slots"], rows=sum(lens) + 40)
+    before = x["states"].clone()
+    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], chunk=chunk)
+    assert h.status() == la.LA_OK
+    check(x, lens, seen, before, out, "bf16", chunk == 32, only=(0, 2, 4))
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("dk,dv", [(16, 16), (32, 64), (64, 16), (128, 128), (16, 128), (128, 32), (64, 64), (32, 16)])
+@pytest.mark.parametrize("lens", [[1, 1, 1], [0, 3, 1, 17]], ids=["ones", "few"])
+def test_token_by_token(io, dk, dv, lens):
+    Hk, Hv = 2, 4
+    x, pool = draw(lens, Hk, Hv, dk, dv, io, seed=dk + dv, pad=16, extra_rows=2)
+    h = handle_for(lens, Hk, Hv, dk, dv, io, pool, extra_rows=2)
+    seen = [r % 2 for r in range(len(lens))]
+    plan = make_plan(h, lens, seen, x["slots"], rows=sum(lens) + 2)
+    before = x["states"].clone()
+    out = torch.full((sum(lens) + 2, Hv, dv), 3.25, device="cuda", dtype=h.dtype)
+    h.decode_step(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], out=out)
+    assert h.status() == la.LA_OK and h.last_launches() == 1
+    check(x, lens, seen, before, out, io, False)
+    assert out[sum(lens):].eq(3.25).all()
+    others = [s for s in range(pool) if s not in [x["slots"][r] for r, n in enumerate(lens) if n > 0]]
+    assert torch.equal(x["states"][others], before[others])
+
+
+def test_default_form_by_type():
+    # fp32 and small heads have no blockwise form: the default is token by token, bit for bit the decode step
+    for io, dk, dv in (("fp32", 64, 64), ("bf16", 32, 64), ("bf16", 64, 32)):
+        lens = [40, 3]
+        x, pool = draw(lens, 1, 2, dk, dv, io, seed=3)
+        h = handle_for(lens, 1, 2, dk, dv, io, pool)
+        plan = make_plan(h, lens, [1, 0], x["slots"])
+        s1, s2 = x["states"].clone(), x["states"].clone()
+        a = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], s1)
+        b = h.decode_step(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], s2)
+        assert torch.equal(a, b) and torch.equal(s1, s2)
+        with pytest.raises(la.LAError) as e:
+            h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], s1, chunk=32)
+        assert e.value.code == la.LA_ERR_UNSUPPORTED
+
+
+def test_many_requests_and_heads():
+    # more CTAs than are resident, long and short ones mixed; every head of a few requests checked
+    rng = random.Random(4)
+    lens = [rng.choice((0, 1, 2, 33, 64, 200, 260)) for _ in range(150)]
+    x, pool = draw(lens, 4, 8, 128, 128, "bf16", seed=8)
+    h = handle_for(lens, 4, 8, 128, 128, "bf16", pool)
+    seen = [r % 3 for r in range(len(lens))]
+    plan = make_plan(h, lens, seen, x["slots"])
+    before = x["states"].clone()
+    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"])
+    assert h.status() == la.LA_OK
+    check(x, lens, seen, before, out, "bf16", True, only=range(0, 150, 19))
+    # the same inputs again: the same bits
+    again = before.clone()
+    out2 = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], again)
+    assert torch.equal(again, x["states"])
+    for r in range(150):
+        a, e = int(plan.offsets[r]), int(plan.offsets[r + 1])
+        assert torch.equal(out[a:e], out2[a:e])
+
+
+def test_a_prompt_in_two_steps_is_the_prompt():
+    lens = [200]
+    x, pool = draw(lens, 1, 2, 128, 128, "bf16", seed=12)
+    h = handle_for(lens, 1, 2, 128, 128, "bf16", pool)
+    t = lambda a, e: [x[n][a:e] for n in ("q", "k", "v", "gate", "beta")]   # noqa: E731
+    before = x["states"].clone()
+    out = torch.empty(200, 2, 128, device="cuda", dtype=torch.bfloat16)
+    for a, e in ((0, 77), (77, 78), (78, 200)):
+        plan = make_plan(h, [e - a], [a], x["slots"])
+        h.forward(plan, *t(a, e), x["states"], out=out[a:e])
+    # blocks elsewhere, so the bound of each part's own blocks adds up: three times the one call's is above it
+    d = lambda y: y.double().cpu().numpy()   # noqa: E731
+    for hd in range(2):
+        want, X, bo, E = ref.rule_by_blocks(*(d(x[n])[:, 0] for n in ("q", "k")), d(x["v"])[:, hd],
+                                            d(x["gate"])[:, hd], d(x["beta"])[:, hd], np.zeros((128, 128)))
+        assert np.all(np.abs(d(out)[:, hd] - want) <= 3 * bo)
+        assert np.linalg.norm(d(x["states"])[x["slots"][0], hd] - X) <= 3 * E
+    assert not torch.equal(before, x["states"])
+
+
+def test_offsets_past_32_bits():
+    # states: slot 65600 of [2, 128, 128] lies past 2^31 elements; rows: 2^21 rows of 1088 elements
+    # lie past 2^31 elements too, before the request that takes part (the first has no slot: no part)
+    Hk, Hv, d = 1, 2, 128
+    skip, n = 2 ** 21, 70
+    pool = 65601
+    h = la.PackedHandle(max_requests=2, max_tokens=skip + n, slots=pool, H_k=Hk, H_v=Hv, d_k=d, d_v=d)
+    states = torch.zeros(pool, Hv, d, d, device="cuda")
+    x, _ = draw([n], Hk, Hv, d, d, "bf16", seed=2)
+    wide = torch.zeros(skip + n, 1088, device="cuda", dtype=torch.bfloat16)
+    packed = {}
+    at = 0
+    for name, heads in (("q", Hk), ("k", Hk), ("v", Hv)):
+        packed[name] = wide[:, at:at + heads * d].view(skip + n, heads, d)
+        packed[name][skip:] = x[name]
+        at += heads * d
+    for name in ("gate", "beta"):
+        packed[name] = torch.ones(skip + n, Hv, device="cuda")
+        packed[name][skip:] = x[name]
+    slot = pool - 1
+    start = torch.randn(Hv, d, d, device="cuda") * 0.5
+    plan = h.plan(i32([skip, n]), i32([4, 4]), i32([-1, slot]), i32([0] * pool), i32([0]), tokens=skip + n)
+    assert plan.counts.tolist() == [skip + n, 1, 0, la.LA_PLAN_FAULT_STATE]
+    out = torch.zeros(skip + n, Hv, d, device="cuda", dtype=torch.bfloat16)
+    for chunk in (32, 1):
+        states[slot] = start
+        h.forward(plan, packed["q"], packed["k"], packed["v"], packed["gate"], packed["beta"], states, out=out, chunk=chunk)
+        assert h.status() == la.LA_OK
+        y = dict(x, states=states[slot:], slots=[0])
+        check(y, [n], [1], start[None], out[skip:], "bf16", chunk == 32)
+        assert not out[:skip].any() and not states[:slot].any()
+
+
+# ------------------------------------------------------------------ a serving loop
+
+class Server:
+    """Requests over several steps: the device side through the library, the
+    references kept per request in float64."""
+
+    def __init__(self, Hk=2, Hv=4, dk=64, dv=64, pool=9, max_requests=6, max_tokens=200, seed=0):
+        self.dims, self.pool, self.R, self.N = (Hk, Hv, dk, dv), pool, max_requests, max_tokens
+        self.h = la.PackedHandle(max_requests=max_requests, max_tokens=max_tokens, slots=pool, H_k=Hk, H_v=Hv, d_k=dk, d_v=dv)
+        self.states = torch.full((pool, Hv, dv, dk), float("nan"), device="cuda")
+        self.lengths, self.seen, self.slots = i32([0] * self.R), i32([0] * self.R), i32([-1] * self.R)
+        self.free, self.count = i32(list(range(pool))), i32([pool])
+        self.plan = self.h.new_plan()
+        self.x, _ = draw([max_tokens], Hk, Hv, dk, dv, "bf16", seed)
+        self.out = torch.zeros(max_tokens, Hv, dv, device="cuda", dtype=torch.bfloat16)
+        self.want = [None] * self.R    # per request: [tokens, state per head, state error per head]
+
+    def step(self, decode):
+        """What a program enqueues for a step; capturable."""
+        self.h.plan(self.lengths, self.seen, self.slots, self.free, self.count, tokens=self.N, plan=self.plan)
+        f = self.h.decode_step if decode else self.h.forward
+        f(self.plan, *(self.x[n] for n in ("q", "k", "v", "gate", "beta")), self.states, out=self.out)
+
+    def feed(self, lens, seed):
+        x, _ = draw([self.N], *self.dims, "bf16", seed)
+        for n in ("q", "k", "v", "gate", "beta"):
+            self.x[n].copy_(x[n])
+        self.lengths.copy_(i32(lens))
+        self.seen.copy_(i32([w[0] if w else 0 for w in self.want]))
+
+    def check(self, lens, decode):
+        torch.cuda.synchronize()
+        assert self.h.status() == la.LA_OK and self.plan.counts.tolist()[3] == 0
+        Hk, Hv, dk, dv = self.dims
+        d = lambda t: t.double().cpu().numpy()   # noqa: E731
+        q, k, v, g, b = (d(self.x[n]) for n in ("q", "k", "v", "gate", "beta"))
+        states, out, slots, row = d(self.states), d(self.out), self.slots.tolist(), 0
+        held = [s for s in slots if s >= 0]
+        free = self.free.tolist()[:int(self.count)]
+        assert sorted(held + free) == list(range(self.pool))       # no slot lost, none twice
+        for r, n in enumerate(lens):
+            if n < 0:
+                self.want[r] = None
+                assert slots[r] == -1
+            if n > 0:
+                w = self.want[r] or [0, [np.zeros((dv, dk))] * Hv, [0.0] * Hv]
+                s, new = slice(row, row + n), [w[0] + n, [], []]
+                for h in range(Hv):
+                    hk = h * Hk // Hv
+                    args = (q[s, hk], k[s, hk], v[s, h], g[s, h], b[s, h], w[1][h])
+                    o, X, bo, E = ref.rule_by_tokens(*args, ref.H) if decode else ref.rule_by_blocks(*args)
+                    carried = w[2][h] * (1 + np.linalg.norm(q[s, hk], axis=1).max() * n)   # of the state before
+                    assert np.all(np.abs(out[s, h] - o) <= bo + carried)
+                    E += w[2][h]
+                    assert np.linalg.norm(states[slots[r], h] - X) <= E
+                    new[1].append(X)
+                    new[2].append(E)
+                self.want[r] = new
+                row += n
+
+
+STEPS = [([40, 3, 0, 65, 1, 33], False), ([1, 1, 10, 1, 1, 1], False), ([1, 2, 1, 1, 3, 1], True), ([-1, 1, 1, 0, -1, 1], True),
+         ([90, 1, 1, 1, 50, 1], False), ([1, 1, 1, 1, 1, 1], True), ([-1] * 6, True), ([5, 0, 0, 0, 0, 100], False)]
+
+
+def test_serving_steps():
+    s = Server()
+    for i, (lens, decode) in enumerate(STEPS):
+        s.feed(lens, seed=100 + i)
+        s.step(decode)
+        s.check(lens, decode)
+
+
+def test_serving_steps_replayed_from_graphs():
+    # one graph of a prefill step and one of a decode step, replayed with new lengths, slots and values
+    s = Server(seed=1)
+    graphs = {}
+    side = torch.cuda.Stream()
+    for decode in (False, True):
+        graphs[decode] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[decode], stream=side):
+            s.step(decode)
+    for i, (lens, decode) in enumerate(STEPS):
+        s.feed(lens, seed=200 + i)
+        graphs[decode].replay()
+        s.check(lens, decode)
+
+
+def test_two_servers_on_two_streams():
+    # two handles, then one handle with two plans, pools and outputs, at once on two streams
+    for shared in (False, True):
+        a, b = Server(seed=3), Server(seed=4)
+        if shared:
+            b.h = a.h
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        torch.cuda.synchronize()
+        for i, (lens, decode) in enumerate(STEPS):
+            for j, s in enumerate((a, b)):
+                s.feed(lens, seed=300 + 10 * i + j)
+            torch.cuda.synchronize()
+            for s, st in zip((a, b), streams):
+                with torch.cuda.stream(st):
+                    s.step(decode)
+            torch.cuda.synchronize()
+            for s in (a, b):
+                s.check(lens, decode)
+
+
+def test_a_stream_given_by_argument():
+    lens = [50, 9]
+    x, pool = draw(lens, 1, 2, 64, 64, "bf16", seed=31)
+    h = handle_for(lens, 1, 2, 64, 64, "bf16", pool)
+    st = torch.cuda.Stream()
+    before = x["states"].clone()
+    args = [i32(lens), i32([1, 1]), i32(x["slots"]), i32([0] * pool), i32([0])]
+    torch.cuda.synchronize()
+    plan = h.plan(*args, tokens=59, stream=st)
+    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], stream=st)
+    assert h.status(stream=st) == la.LA_OK
+    check(x, lens, [1, 1], before, out, "bf16", True)
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_python_refuses_wrong_tensors():
+    lens = [5, 4]
+    x, pool = draw(lens, 2, 2, 64, 64, "bf16", seed=1)
+    h = handle_for(lens, 2, 2, 64, 64, "bf16", pool)
+    plan = make_plan(h, lens, [0, 0], x["slots"])
+    good = [x[n] for n in ("q", "k", "v", "gate", "beta", "states")]
+    bad = [(0, x["q"].float()), (0, x["q"].cpu()), (0, x["q"][:8]), (0, x["q"].transpose(1, 2)), (1, x["k"][:, :1]),
+           (2, x["v"].transpose(0, 1).contiguous().transpose(0, 1)), (3, x["gate"].half()), (3, x["gate"].t()),
+           (4, x["beta"][:, :1]), (5, x["states"].bfloat16()), (5, x["states"][:-1]), (5, x["states"].transpose(2, 3))]
+    before = x["states"].clone()
+    for i, t in bad:
+        args = list(good)
+        args[i] = t
+        with pytest.raises(ValueError):
+            h.forward(plan, *args)
+    with pytest.raises(ValueError):
+        h.forward(plan, *good, out=torch.empty(9, 2, 64, device="cuda"))
+    with pytest.raises(ValueError):
+        make_plan(h, [1, 1], [0, 0], [0])
+    with pytest.raises(ValueError):
+        h.plan(i32([1]), i32([1]).long(), i32([0]), i32([0] * pool), i32([0]), tokens=1)
+    with pytest.raises(ValueError):   # a plan of other maxima
+        h.forward(handle_for([1], 2, 2, 64, 64, "bf16", pool).new_plan(), *good)
+    torch.cuda.synchronize()
+    assert torch.equal(before, x["states"])
+
+
+def test_the_library_refuses_before_it_launches():
+    lens = [5, 4]
+    x, pool = draw(lens, 2, 2, 64, 64, "bf16", seed=1)
+    h = handle_for(lens, 2, 2, 64, 64, "bf16", pool)
+    plan = make_plan(h, lens, [0, 0], x["slots"])
+    out = torch.zeros(9, 2, 64, device="cuda", dtype=torch.bfloat16)
+    P = [plan.words.data_ptr(), *(x[n].data_ptr() for n in ("q", "k", "v", "gate", "beta", "states")), out.data_ptr()]
+    L, stream = la.lib(), torch.cuda.current_stream().cuda_stream
+    call = lambda p=P, R=2, n=9, s=(128, 128, 128), chunk=0: L.la_packed_forward(h._h, *p, R, n, *s, chunk, stream)   # noqa: E731
+    for i in range(8):
+        assert call([None if j == i else y for j, y in enumerate(P)]) == la.LA_ERR_INVALID_ARG
+        assert call([y + (2 if i in (4, 5) else 8) if j == i else y for j, y in enumerate(P)]) == la.LA_ERR_MISALIGNED
+    assert call(R=-1) == call(n=-1) == call(R=3) == call(n=10) == la.LA_ERR_INVALID_ARG
+    assert call(s=(127, 128, 128)) == call(s=(128, 0, 128)) == call(s=(128, 128, -128)) == la.LA_ERR_INVALID_ARG
+    assert call(s=(129, 128, 128)) == call(s=(128, 132, 128)) == la.LA_ERR_MISALIGNED
+    assert call(s=(1 << 40, 128, 128)) == la.LA_ERR_UNSUPPORTED
+    assert call(chunk=64) == call(chunk=2) == call(chunk=-1) == la.LA_ERR_UNSUPPORTED
+    assert L.la_packed_last_launches(h._h) == 0 and L.la_packed_last_error(h._h)
+    assert call(R=0) == call(n=0) == la.LA_OK and L.la_packed_last_launches(h._h) == 0
+    ints = [i32([1, 1]).data_ptr(), i32([1, 1]).data_ptr(), i32([0, 1]).data_ptr(), i32([0] * pool).data_ptr(),
+            i32([0]).data_ptr(), plan.words.data_ptr()]
+    pl = lambda p=ints, R=2, n=9: L.la_packed_plan(h._h, *p, R, n, stream)   # noqa: E731
+    for i in range(6):
+        assert pl([None if j == i else y for j, y in enumerate(ints)]) == la.LA_ERR_INVALID_ARG
+        assert pl([y + 1 if j == i else y for j, y in enumerate(ints)]) == la.LA_ERR_MISALIGNED
+    assert pl([y + 4 if j == 5 else y for j, y in enumerate(ints)]) == la.LA_ERR_MISALIGNED
+    assert pl(R=3) == pl(n=10) == pl(R=-1) == pl(n=-1) == la.LA_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert not out.any()
+
+
+def test_a_buffer_no_plan_was_made_in_reaches_nothing():
+    # any words: the kernels take only what lies inside the tensors; here no word does
+    lens = [40, 20]
+    for words in (-1, 0, 2 ** 31 - 1, -2 ** 31, 1000):
+        x, pool = draw(lens, 1, 1, 64, 64, "bf16", seed=6)
+        h = handle_for(lens, 1, 1, 64, 64, "bf16", pool)
+        plan = make_plan(h, lens, [1, 1], x["slots"])
+        plan.words.fill_(words)
+        before = x["states"].clone()
+        out = torch.zeros(60, 1, 64, device="cuda", dtype=torch.bfloat16)
+        for f in (h.forward, h.decode_step):
+            f(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], out=out)
+        assert h.status() == la.LA_OK
+        assert not out.any() and torch.equal(before, x["states"])
