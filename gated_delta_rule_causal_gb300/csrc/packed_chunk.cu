@@ -50,7 +50,11 @@ constexpr int kPrep = 2;                   // prep warps
 constexpr int kThreads = 32 * (kChain + kPrep);
 constexpr int kStages = 3;
 constexpr int kTStride = 80;               // bytes per row of a 32x32 bf16 tile: 16-byte chunks of 8 rows hit all banks
-constexpr int kSStride = 40;               // floats per row of the prep warps' 32x32 fp32 scratch
+// prep warps' fp32 scratch: two 16x16 sub-blocks each of K K^T and Q K^T, rows and blocks so far apart that the MMA
+// fragments' stores and the column reads of both halves of the warp hit all banks; then the gates
+constexpr int kSStride = 24;
+constexpr int kSBlock = 16 * kSStride + 16;
+constexpr int kScratch = 4 * kSBlock + C;
 
 template <int DK>
 struct Layout {
@@ -64,8 +68,8 @@ struct Layout {
     static constexpr uint32_t P = TL + C * kTStride;
     static constexpr uint32_t VEC = P + C * kTStride;        // fp32: b, b G, G, D_31 [32 each]
     static constexpr uint32_t STAGE = (VEC + 4 * C * 4 + 1023) / 1024 * 1024;
-    static constexpr uint32_t SCRATCH = kStages * STAGE;     // per prep warp: K K^T and Q K^T, fp32
-    static constexpr uint32_t BAR = SCRATCH + kPrep * 2 * C * kSStride * 4;
+    static constexpr uint32_t SCRATCH = kStages * STAGE;     // kScratch floats per prep warp
+    static constexpr uint32_t BAR = SCRATCH + kPrep * kScratch * 4;
     static constexpr uint32_t BYTES = BAR + 128;
 };
 
@@ -108,6 +112,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, __nv_bfloat16 x) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(x)) : "memory");
 }
+__device__ __forceinline__ void st_shared_b32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(addr), "r"(0) : "memory");
 }
@@ -120,14 +127,22 @@ struct Item {
 
 // ---------------------------------------------------------------- prep warps
 // T (two bf16 parts), P and the gate vectors of blocks pw, pw + kPrep, ...
+//
+// By 16x16 sub-blocks: the diagonal ones by forward substitution in fp32, lane
+// l one column of sub-block l / 16; the one below them as T21 = -T22 (A21 T11)
+// on the tensor cores, operands in two bf16 parts. Between the halves the
+// decay factors: D_tj = (g_16 .. g_t)(g_{j+1} .. g_15) for j < 16 <= t.
 template <int DK>
 __device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uint8_t* sm, uint32_t sbase, int pw,
                                           uint64_t* full, uint64_t* ready, volatile int* abort_flag) {
     using L = Layout<DK>;
     const int lane = threadIdx.x & 31, gq = lane >> 2, cq = lane & 3;
-    float* kk = reinterpret_cast<float*>(sm + L::SCRATCH) + pw * 2 * C * kSStride;   // raw K K^T, then A
-    float* qk = kk + C * kSStride;                                                   // raw Q K^T
-    // A fragment rows of an m16 x k16 tile by ldmatrix: lane -> row, 16-byte chunk
+    const int blk = lane >> 4, col = lane & 15;
+    float* kk = reinterpret_cast<float*>(sm + L::SCRATCH) + pw * kScratch;   // diagonal sub-blocks of K K^T, then A
+    float* qk = kk + 2 * kSBlock;                                            // and of Q K^T
+    float* gs = qk + 2 * kSBlock;                                            // gates [32]
+    // A fragment of an m16 x k16 tile by ldmatrix: lane -> row, 16-byte chunk
+    // (the same addresses, transposed, give the B fragments of a k16 x n16 tile)
     const int fr = (lane & 7) + ((lane >> 3) & 1) * 8, fc = lane >> 4;
     auto gates = [&](int c, float& g, float& b) {   // token `lane` of block c; gate 1, beta 0 past the end
         const int t = c * C + lane;
@@ -146,8 +161,23 @@ __device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uin
         const uint32_t st = sbase + s * L::STAGE;
         const float g = gn, b = bn;
         gates(c + kPrep, gn, bn);
+        // ---- gate vectors: products inside each half, then over the block ----------------
+        float G = g;
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, G, o);
+            if (col >= o) G *= y;
+        }
+        const float Gq = G;   // (second half) the gates from 16 up to this token
+        const float G15 = __shfl_sync(0xffffffffu, G, 15), G31 = __shfl_sync(0xffffffffu, G, 31);
+        if (blk) G *= G15;
+        gs[lane] = g;
         bool ok = mbar_wait_or_abort(&full[s], (c / kStages) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) return;
+        float* vec = reinterpret_cast<float*>(sm + s * L::STAGE + L::VEC);
+        vec[lane] = b;
+        vec[C + lane] = b * G;
+        vec[2 * C + lane] = G;
         const int n = it.rq.len - c * C;   // tokens of the block
         if (n < C) {                       // rows of the next request (or past the tensor): zero
             for (int i = lane; i < (C - n) * 8; i += 32) {
@@ -163,67 +193,82 @@ __device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uin
         }
         // ---- K K^T and Q K^T, lower tiles only; a key fragment serves as A and as B ----
         float dk[6][4] = {}, dq[6][4] = {};   // tiles (m, n): (0,0) (0,1) (1,0) (1,1) (1,2) (1,3)
+        uint32_t f[2][4][4];                  // fragments k rows 0-15, 16-31, q rows 0-15, 16-31; one step ahead
+        auto load = [&](int x, uint32_t (&w)[4][4]) {
+            const uint32_t at = (x / 4) * 4096, ch = (x % 4) * 2 + fc;
+            ldsm4(w[0], st + L::K + at + sw128_off(fr, ch));
+            ldsm4(w[1], st + L::K + at + sw128_off(16 + fr, ch));
+            ldsm4(w[2], st + L::Q + at + sw128_off(fr, ch));
+            ldsm4(w[3], st + L::Q + at + sw128_off(16 + fr, ch));
+        };
+        load(0, f[0]);
 #pragma unroll
         for (int x = 0; x < DK / 16; ++x) {
-            uint32_t k0[4], k1[4], q0[4], q1[4];
-            const uint32_t at = (x / 4) * 4096, ch = (x % 4) * 2 + fc;
-            ldsm4(k0, st + L::K + at + sw128_off(fr, ch));
-            ldsm4(k1, st + L::K + at + sw128_off(16 + fr, ch));
-            ldsm4(q0, st + L::Q + at + sw128_off(fr, ch));
-            ldsm4(q1, st + L::Q + at + sw128_off(16 + fr, ch));
-            mma(dk[0], k0, k0[0], k0[2]);
-            mma(dk[1], k0, k0[1], k0[3]);
-            mma(dk[2], k1, k0[0], k0[2]);
-            mma(dk[3], k1, k0[1], k0[3]);
-            mma(dk[4], k1, k1[0], k1[2]);
-            mma(dk[5], k1, k1[1], k1[3]);
-            mma(dq[0], q0, k0[0], k0[2]);
-            mma(dq[1], q0, k0[1], k0[3]);
-            mma(dq[2], q1, k0[0], k0[2]);
-            mma(dq[3], q1, k0[1], k0[3]);
-            mma(dq[4], q1, k1[0], k1[2]);
-            mma(dq[5], q1, k1[1], k1[3]);
+            if (x + 1 < DK / 16) load(x + 1, f[(x + 1) & 1]);
+            const auto& w = f[x & 1];
+            mma(dk[0], w[0], w[0][0], w[0][2]);
+            mma(dk[1], w[0], w[0][1], w[0][3]);
+            mma(dk[2], w[1], w[0][0], w[0][2]);
+            mma(dk[3], w[1], w[0][1], w[0][3]);
+            mma(dk[4], w[1], w[1][0], w[1][2]);
+            mma(dk[5], w[1], w[1][1], w[1][3]);
+            mma(dq[0], w[2], w[0][0], w[0][2]);
+            mma(dq[1], w[2], w[0][1], w[0][3]);
+            mma(dq[2], w[3], w[0][0], w[0][2]);
+            mma(dq[3], w[3], w[0][1], w[0][3]);
+            mma(dq[4], w[3], w[1][0], w[1][2]);
+            mma(dq[5], w[3], w[1][1], w[1][3]);
         }
 #pragma unroll
-        for (int i = 0; i < 6; ++i) {
-            const int row = (i < 2 ? 0 : 16) + gq, col = (i < 2 ? i : i - 2) * 8 + 2 * cq;
-            *reinterpret_cast<float2*>(kk + row * kSStride + col) = make_float2(dk[i][0], dk[i][1]);
-            *reinterpret_cast<float2*>(kk + (row + 8) * kSStride + col) = make_float2(dk[i][2], dk[i][3]);
-            *reinterpret_cast<float2*>(qk + row * kSStride + col) = make_float2(dq[i][0], dq[i][1]);
-            *reinterpret_cast<float2*>(qk + (row + 8) * kSStride + col) = make_float2(dq[i][2], dq[i][3]);
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float* k0 = kk + h * kSBlock + gq * kSStride + 8 * i + 2 * cq;
+                float* q0 = qk + h * kSBlock + gq * kSStride + 8 * i + 2 * cq;
+                const float(&x)[4] = dk[4 * h + i];
+                const float(&y)[4] = dq[4 * h + i];
+                *reinterpret_cast<float2*>(k0) = make_float2(x[0], x[1]);
+                *reinterpret_cast<float2*>(k0 + 8 * kSStride) = make_float2(x[2], x[3]);
+                *reinterpret_cast<float2*>(q0) = make_float2(y[0], y[1]);
+                *reinterpret_cast<float2*>(q0 + 8 * kSStride) = make_float2(y[2], y[3]);
+            }
         __syncwarp();
-        // ---- A and P, lane j takes column j: D_tj is its running product ------------------
-        float d = 0.f;
+        // ---- A and P of the diagonal sub-blocks: D_tj is the lane's running product -------
+        float* ak = kk + blk * kSBlock;
+        const float* aq = qk + blk * kSBlock;
+        float kc[16], qc[16], gt[16], bt[16];
 #pragma unroll
-        for (int t = 0; t < C; ++t) {
-            const float gt = __shfl_sync(0xffffffffu, g, t), bt = __shfl_sync(0xffffffffu, b, t);
-            d = t == lane ? 1.f : d * gt;   // zero above the diagonal
-            const float p = t >= lane ? d * qk[t * kSStride + lane] : 0.f;
-            const float ax = t > lane ? bt * d * kk[t * kSStride + lane] : 0.f;
-            st_shared_u16(st + L::P + t * kTStride + 2 * lane, __float2bfloat16_rn(p));
-            kk[t * kSStride + lane] = ax;
+        for (int t = 0; t < 16; ++t) {
+            kc[t] = ak[t * kSStride + col];
+            qc[t] = aq[t * kSStride + col];
         }
-        float G = g;   // product of the gates up to token `lane`
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, G, o);
-            if (lane >= o) G *= y;
+        for (int t = 0; t < 16; t += 4) {
+            *reinterpret_cast<float4*>(&gt[t]) = *reinterpret_cast<const float4*>(gs + 16 * blk + t);
+            *reinterpret_cast<float4*>(&bt[t]) = *reinterpret_cast<const float4*>(vec + 16 * blk + t);
         }
-        float* vec = reinterpret_cast<float*>(sm + s * L::STAGE + L::VEC);
-        vec[lane] = b;
-        vec[C + lane] = b * G;
-        vec[2 * C + lane] = G;
-        vec[3 * C + lane] = d;
+        float d = 0.f;   // zero above the diagonal
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            d = t == col ? 1.f : d * gt[t];
+            kc[t] = t > col ? bt[t] * d * kc[t] : 0.f;
+            qc[t] = t >= col ? d * qc[t] : 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            ak[t * kSStride + col] = kc[t];
+            st_shared_u16(st + L::P + (16 * blk + t) * kTStride + 2 * lane, __float2bfloat16_rn(qc[t]));
+        }
+        vec[3 * C + lane] = blk ? d : d * G31;
         __syncwarp();
-        // ---- T = (I + A)^-1 by forward substitution, lane j takes column j ------------------
-        float x[C];
+        // ---- their inverses by forward substitution ----------------------------------------
+        float x[16];
 #pragma unroll
-        for (int t = 0; t < C; ++t) {
-            float s0 = t == lane ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        for (int t = 0; t < 16; ++t) {
+            float s0 = t == col ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
             for (int i = 0; i < t; i += 4) {
-                const float4 r = *reinterpret_cast<const float4*>(kk + t * kSStride + i);
+                const float4 r = *reinterpret_cast<const float4*>(ak + t * kSStride + i);
                 s0 -= r.x * x[i];
                 if (i + 1 < t) s1 -= r.y * x[i + 1];
                 if (i + 2 < t) s2 -= r.z * x[i + 2];
@@ -232,11 +277,71 @@ __device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uin
             x[t] = (s0 + s1) + (s2 + s3);
         }
 #pragma unroll
-        for (int t = 0; t < C; ++t) {
+        for (int t = 0; t < 16; ++t) {
             const __nv_bfloat16 hi = __float2bfloat16_rn(x[t]);
-            st_shared_u16(st + L::TH + t * kTStride + 2 * lane, hi);
-            st_shared_u16(st + L::TL + t * kTStride + 2 * lane, __float2bfloat16_rn(x[t] - __bfloat162float(hi)));
+            st_shared_u16(st + L::TH + (16 * blk + t) * kTStride + 2 * lane, hi);
+            st_shared_u16(st + L::TL + (16 * blk + t) * kTStride + 2 * lane, __float2bfloat16_rn(x[t] - __bfloat162float(hi)));
         }
+        // ---- the sub-block below: P21 = Q S qk, A21 = b Q S kk (Q by token, S by column) --------
+        const float Q0 = __shfl_sync(0xffffffffu, Gq, 16 + gq), Q1 = __shfl_sync(0xffffffffu, Gq, 24 + gq);
+        const float b0 = __shfl_sync(0xffffffffu, b, 16 + gq), b1 = __shfl_sync(0xffffffffu, b, 24 + gq);
+        uint32_t ah[4], al[4];
+        {
+            float S[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                S[i][0] = __shfl_sync(0xffffffffu, d, 8 * i + 2 * cq);
+                S[i][1] = __shfl_sync(0xffffffffu, d, 8 * i + 2 * cq + 1);
+                float(&y)[4] = dq[2 + i];
+                st_shared_b32(st + L::P + (16 + gq) * kTStride + 16 * i + 4 * cq, pack_bf16(Q0 * S[i][0] * y[0], Q0 * S[i][1] * y[1]));
+                st_shared_b32(st + L::P + (24 + gq) * kTStride + 16 * i + 4 * cq, pack_bf16(Q1 * S[i][0] * y[2], Q1 * S[i][1] * y[3]));
+                float(&z)[4] = dk[2 + i];
+                z[0] *= b0 * Q0 * S[i][0];
+                z[1] *= b0 * Q0 * S[i][1];
+                z[2] *= b1 * Q1 * S[i][0];
+                z[3] *= b1 * Q1 * S[i][1];
+            }
+            split_tiles(dk[2], dk[3], ah, al);
+        }
+        __syncwarp();
+        float M[2][4] = {}, N[2][4] = {};
+        {
+            uint32_t th[4], tl[4];   // T11 [k = s][n = j]
+            ldsm4t(th, st + L::TH + fr * kTStride + 16 * fc);
+            ldsm4t(tl, st + L::TL + fr * kTStride + 16 * fc);
+            mma(M[0], ah, th[0], th[1]);
+            mma(M[1], ah, th[2], th[3]);
+            mma(M[0], al, th[0], th[1]);
+            mma(M[1], al, th[2], th[3]);
+            mma(M[0], ah, tl[0], tl[1]);
+            mma(M[1], ah, tl[2], tl[3]);
+        }
+        {
+            uint32_t th[4], tl[4], mh[4], ml[4];   // T22 [t][s]; M [k = s][n = j], transposed between lanes
+            ldsm4(th, st + L::TH + (16 + fr) * kTStride + 32 + 16 * fc);
+            ldsm4(tl, st + L::TL + (16 + fr) * kTStride + 32 + 16 * fc);
+            split_tiles(M[0], M[1], mh, ml);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mh[i] = transpose8x8(mh[i]);
+                ml[i] = transpose8x8(ml[i]);
+            }
+            mma(N[0], th, mh[0], mh[1]);
+            mma(N[1], th, mh[2], mh[3]);
+            mma(N[0], tl, mh[0], mh[1]);
+            mma(N[1], tl, mh[2], mh[3]);
+            mma(N[0], th, ml[0], ml[1]);
+            mma(N[1], th, ml[2], ml[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t hi, lo;
+                split2(-N[i][2 * h], -N[i][2 * h + 1], hi, lo);
+                st_shared_b32(st + L::TH + (16 + 8 * h + gq) * kTStride + 16 * i + 4 * cq, hi);
+                st_shared_b32(st + L::TL + (16 + 8 * h + gq) * kTStride + 16 * i + 4 * cq, lo);
+            }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ready[s]);
     }
@@ -334,6 +439,19 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) +
                             (static_cast<size_t>(it.rq.row0) * a.Hv + it.head) * a.dv + r0 + 2 * cq;
         const size_t ostep = static_cast<size_t>(a.Hv) * a.dv;
+        // outputs of the block before, rounded: [dv][token] fragments, turned
+        // to [token][dv] pairs when they leave
+        uint32_t Y[4][2] = {};
+        auto store_out = [&](int n, int c) {   // tokens 8n .. 8n + 7 of block c
+            const uint32_t y0 = transpose8x8(Y[n][0]);   // token 8n + g, rows 2c, 2c + 1
+            const uint32_t y1 = transpose8x8(Y[n][1]);   // rows 8 + 2c, ..
+            const int t = c * C + 8 * n + gq;
+            if (c >= 0 && t < it.rq.len) {
+                __nv_bfloat16* o = op + static_cast<size_t>(t) * ostep;
+                *reinterpret_cast<uint32_t*>(o) = y0;
+                *reinterpret_cast<uint32_t*>(o + 8) = y1;
+            }
+        };
 
         for (int c = 0; c < it.blocks; ++c) {
             const int s = c % kStages;
@@ -344,31 +462,45 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 failed = true;
                 break;
             }
-            // ---- Z = X K^T (both parts of X), O = X Q^T (the high part) -----------------
+            // ---- Z = X K^T, both parts of X; the block before's outputs leave meanwhile ----
             float Z[4][4] = {}, O[4][4] = {};
 #pragma unroll
             for (int x = 0; x < DK / 16; ++x) {
                 uint32_t hi[4], lo[4], b0[4], b1[4];
+                const uint32_t at = st + L::K + (x / 4) * 4096, ch = (x % 4) * 2 + bc;
+                ldsm4(b0, at + sw128_off(br, ch));
+                ldsm4(b1, at + sw128_off(16 + br, ch));
                 split_tiles(X[2 * x], X[2 * x + 1], hi, lo);
-                const uint32_t at = (x / 4) * 4096, ch = (x % 4) * 2 + bc;
-                ldsm4(b0, st + L::K + at + sw128_off(br, ch));
-                ldsm4(b1, st + L::K + at + sw128_off(16 + br, ch));
                 mma(Z[0], hi, b0[0], b0[1]);
                 mma(Z[1], hi, b0[2], b0[3]);
                 mma(Z[2], hi, b1[0], b1[1]);
                 mma(Z[3], hi, b1[2], b1[3]);
+                if (x < 4) store_out(x, c - 1);
                 mma(Z[0], lo, b0[0], b0[1]);
                 mma(Z[1], lo, b0[2], b0[3]);
                 mma(Z[2], lo, b1[0], b1[1]);
                 mma(Z[3], lo, b1[2], b1[3]);
-                ldsm4(b0, st + L::Q + at + sw128_off(br, ch));
-                ldsm4(b1, st + L::Q + at + sw128_off(16 + br, ch));
-                mma(O[0], hi, b0[0], b0[1]);
-                mma(O[1], hi, b0[2], b0[3]);
-                mma(O[2], hi, b1[0], b1[1]);
-                mma(O[3], hi, b1[2], b1[3]);
             }
-            // ---- R = b (V - G Z), in Z; O scaled by G ------------------------------------
+            // ---- O = X Q^T, the high part, in two runs between the steps of U --------------
+            auto read_out = [&](int x0, int x1) {
+#pragma unroll
+                for (int x = x0; x < x1; ++x) {
+                    uint32_t hi[4], b0[4], b1[4];
+                    const uint32_t at = st + L::Q + (x / 4) * 4096, ch = (x % 4) * 2 + bc;
+                    ldsm4(b0, at + sw128_off(br, ch));
+                    ldsm4(b1, at + sw128_off(16 + br, ch));
+                    hi[0] = pack_bf16(X[2 * x][0], X[2 * x][1]);
+                    hi[1] = pack_bf16(X[2 * x][2], X[2 * x][3]);
+                    hi[2] = pack_bf16(X[2 * x + 1][0], X[2 * x + 1][1]);
+                    hi[3] = pack_bf16(X[2 * x + 1][2], X[2 * x + 1][3]);
+                    mma(O[0], hi, b0[0], b0[1]);
+                    mma(O[1], hi, b0[2], b0[3]);
+                    mma(O[2], hi, b1[0], b1[1]);
+                    mma(O[3], hi, b1[2], b1[3]);
+                }
+            };
+            read_out(0, DK / 32);
+            // ---- R = b (V - G Z), in Z --------------------------------------------------------
             const float* vec = reinterpret_cast<const float*>(sm + s * L::STAGE + L::VEC);
 #pragma unroll
             for (int n = 0; n < 4; n += 2) {
@@ -379,30 +511,24 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                     const int t = 8 * (n + i) + 2 * cq;
                     const float2 b = *reinterpret_cast<const float2*>(vec + t);
                     const float2 bg = *reinterpret_cast<const float2*>(vec + C + t);
-                    const float2 g = *reinterpret_cast<const float2*>(vec + 2 * C + t);
                     const float2 vl = unpack_bf16(v4[2 * i]), vh = unpack_bf16(v4[2 * i + 1]);
                     float(&z)[4] = Z[n + i];
                     z[0] = b.x * vl.x - bg.x * z[0];
                     z[1] = b.y * vl.y - bg.y * z[1];
                     z[2] = b.x * vh.x - bg.x * z[2];
                     z[3] = b.y * vh.y - bg.y * z[3];
-                    float(&o)[4] = O[n + i];
-                    o[0] *= g.x;
-                    o[1] *= g.y;
-                    o[2] *= g.x;
-                    o[3] *= g.y;
                 }
             }
             // ---- U = R T^T: lower triangular, columns j < 16 reach every t, j >= 16 only t >= 16
             float U[4][4] = {};
             {
                 uint32_t h0[4], l0[4], h1[4], l1[4], t0[4], t1[4], t2[4];
-                split_tiles(Z[0], Z[1], h0, l0);
-                split_tiles(Z[2], Z[3], h1, l1);
                 const uint32_t th = st + L::TH + br * kTStride + bc * 16, tl = st + L::TL + br * kTStride + bc * 16;
                 ldsm4(t0, th);                         // t 0..15, j 0..15
                 ldsm4(t1, th + 16 * kTStride);         // t 16..31, j 0..15
                 ldsm4(t2, th + 16 * kTStride + 32);    // t 16..31, j 16..31
+                split_tiles(Z[0], Z[1], h0, l0);
+                split_tiles(Z[2], Z[3], h1, l1);
                 mma(U[0], h0, t0[0], t0[1]);
                 mma(U[1], h0, t0[2], t0[3]);
                 mma(U[2], h0, t1[0], t1[1]);
@@ -425,15 +551,26 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 mma(U[2], h1, t2[0], t2[1]);
                 mma(U[3], h1, t2[2], t2[3]);
             }
-            // ---- O += U P^T ------------------------------------------------------------
+            read_out(DK / 32, DK / 16);
+            // ---- O = G O + U P^T; X = G_31 X + (U D_31) K --------------------------------------
+            uint32_t h0[4], l0[4], h1[4], l1[4];
+            const float gc = vec[2 * C + C - 1];
             {
-                uint32_t h0[4], l0[4], h1[4], l1[4], t0[4], t1[4], t2[4];
-                split_tiles(U[0], U[1], h0, l0);
-                split_tiles(U[2], U[3], h1, l1);
+                uint32_t t0[4], t1[4], t2[4];
                 const uint32_t tp = st + L::P + br * kTStride + bc * 16;
                 ldsm4(t0, tp);
                 ldsm4(t1, tp + 16 * kTStride);
                 ldsm4(t2, tp + 16 * kTStride + 32);
+                split_tiles(U[0], U[1], h0, l0);
+                split_tiles(U[2], U[3], h1, l1);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 g = *reinterpret_cast<const float2*>(vec + 2 * C + 8 * n + 2 * cq);
+                    O[n][0] *= g.x;
+                    O[n][1] *= g.y;
+                    O[n][2] *= g.x;
+                    O[n][3] *= g.y;
+                }
                 mma(O[0], h0, t0[0], t0[1]);
                 mma(O[1], h0, t0[2], t0[3]);
                 mma(O[2], h0, t1[0], t1[1]);
@@ -447,40 +584,35 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 mma(O[2], l1, t2[0], t2[1]);
                 mma(O[3], l1, t2[2], t2[3]);
             }
-            // ---- X = G_31 X + (U D_31) K ---------------------------------------------------
-            {
-                const float gc = vec[2 * C + C - 1];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 dc = *reinterpret_cast<const float2*>(vec + 3 * C + 8 * n + 2 * cq);
-                    U[n][0] *= dc.x;
-                    U[n][1] *= dc.y;
-                    U[n][2] *= dc.x;
-                    U[n][3] *= dc.y;
+            for (int n = 0; n < 4; ++n) {
+                const float2 dc = *reinterpret_cast<const float2*>(vec + 3 * C + 8 * n + 2 * cq);
+                U[n][0] *= dc.x;
+                U[n][1] *= dc.y;
+                U[n][2] *= dc.x;
+                U[n][3] *= dc.y;
+            }
+            split_tiles(U[0], U[1], h0, l0);
+            split_tiles(U[2], U[3], h1, l1);
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t b0[4], b1[4];
+                const uint32_t at = st + L::K + (n / 8) * 4096, ch = n % 8 + tc;
+                ldsm4t(b0, at + sw128_off(tr, ch));
+                ldsm4t(b1, at + sw128_off(16 + tr, ch));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    X[n][i] *= gc;
+                    X[n + 1][i] *= gc;
                 }
-                uint32_t h0[4], l0[4], h1[4], l1[4];
-                split_tiles(U[0], U[1], h0, l0);
-                split_tiles(U[2], U[3], h1, l1);
-#pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    uint32_t b0[4], b1[4];
-                    const uint32_t at = st + L::K + (n / 8) * 4096, ch = n % 8 + tc;
-                    ldsm4t(b0, at + sw128_off(tr, ch));
-                    ldsm4t(b1, at + sw128_off(16 + tr, ch));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        X[n][i] *= gc;
-                        X[n + 1][i] *= gc;
-                    }
-                    mma(X[n], h0, b0[0], b0[1]);
-                    mma(X[n + 1], h0, b0[2], b0[3]);
-                    mma(X[n], h1, b1[0], b1[1]);
-                    mma(X[n + 1], h1, b1[2], b1[3]);
-                    mma(X[n], l0, b0[0], b0[1]);
-                    mma(X[n + 1], l0, b0[2], b0[3]);
-                    mma(X[n], l1, b1[0], b1[1]);
-                    mma(X[n + 1], l1, b1[2], b1[3]);
-                }
+                mma(X[n], h0, b0[0], b0[1]);
+                mma(X[n + 1], h0, b0[2], b0[3]);
+                mma(X[n], h1, b1[0], b1[1]);
+                mma(X[n + 1], h1, b1[2], b1[3]);
+                mma(X[n], l0, b0[0], b0[1]);
+                mma(X[n + 1], l0, b0[2], b0[3]);
+                mma(X[n], l1, b1[0], b1[1]);
+                mma(X[n + 1], l1, b1[2], b1[3]);
             }
             // this warp has read the stage: the last one to say so reloads it
             __syncwarp();
@@ -492,18 +624,15 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                     issue(c + kStages);
                 }
             }
-            // ---- output: [dv][token] fragments to [token][dv] pairs -------------------------
-            const int nv = it.rq.len - c * C;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const uint32_t y0 = transpose8x8(pack_bf16(O[n][0], O[n][1]));   // token 8n + g, rows 2c, 2c + 1
-                const uint32_t y1 = transpose8x8(pack_bf16(O[n][2], O[n][3]));   // rows 8 + 2c, ..
-                if (8 * n + gq < nv) {
-                    __nv_bfloat16* o = op + static_cast<size_t>(c * C + 8 * n + gq) * ostep;
-                    *reinterpret_cast<uint32_t*>(o) = y0;
-                    *reinterpret_cast<uint32_t*>(o + 8) = y1;
-                }
+                Y[n][0] = pack_bf16(O[n][0], O[n][1]);
+                Y[n][1] = pack_bf16(O[n][2], O[n][3]);
             }
+        }
+        if (!failed) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) store_out(n, it.blocks - 1);
         }
         if (!failed) {
 #pragma unroll
