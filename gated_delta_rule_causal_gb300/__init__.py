@@ -409,7 +409,7 @@ class PackedPlan:
             offsets = 8
             slots = offsets + pad(R + 1)
             order = slots + pad(R)
-            treq = order + 2 * pad(R)
+            treq = order + pad(R) + 4 * R
             tpos = treq + pad(N)
             self._views = (w[:4], w[offsets:offsets + requests + 1], w[slots:slots + requests],
                            w[order:order + requests], w[treq:treq + tokens], w[tpos:tpos + tokens])

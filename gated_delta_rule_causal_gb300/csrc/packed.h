@@ -23,7 +23,7 @@ constexpr int kMaxTokens = 1 << 24;
 //   offsets[R + 1]       first row of every request (rows + 1 where it lies past the rows given)
 //   slots[R]             state slot of a request that takes part, else -1
 //   order[R]             requests, most blocks first (to a power of two), those without a part last
-//   seen[R]              tokens a request had absorbed before
+//   items[R][4]          the requests in that order: first row, length, slot (-1: no part), tokens seen before
 //   token_request[N], token_position[N]
 //   owner[S]             scratch: which request claims a slot
 struct PlanLayout {
@@ -32,8 +32,8 @@ struct PlanLayout {
     __host__ __device__ size_t offsets() const { return 8; }
     __host__ __device__ size_t slots() const { return offsets() + pad(static_cast<size_t>(R) + 1); }
     __host__ __device__ size_t order() const { return slots() + pad(R); }
-    __host__ __device__ size_t seen() const { return order() + pad(R); }
-    __host__ __device__ size_t token_request() const { return seen() + pad(R); }
+    __host__ __device__ size_t items() const { return order() + pad(R); }
+    __host__ __device__ size_t token_request() const { return items() + 4 * static_cast<size_t>(R); }
     __host__ __device__ size_t token_position() const { return token_request() + pad(N); }
     __host__ __device__ size_t owner() const { return token_position() + pad(N); }
     __host__ __device__ size_t words() const { return owner() + pad(S); }
@@ -82,27 +82,40 @@ struct StepArgs {
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
 // In blocks of 32 tokens, warp-level MMAs: bf16, dk and dv in {64, 128}.
 cudaError_t launch_chunk(const StepArgs& a, cudaStream_t s, PFN_cuTensorMapEncodeTiled_v12000 enc);
+// In blocks of 64 tokens on the tcgen05 tensor cores: bf16, dk in {64, 128}, dv 128.
+cudaError_t launch_tc(const StepArgs& a, cudaStream_t s, PFN_cuTensorMapEncodeTiled_v12000 enc);
 
-// The requests of a plan as the kernels read them, every word checked against
-// what the tensors hold, so that a plan of other sizes or a buffer that no
-// plan was made in reaches no memory outside them.
+// 3-D map over a packed tensor [rows][H][d], rows `stride` elements apart:
+// boxes of `block` rows of one head's 64 channels, 128-byte swizzle. Rows past
+// the tensor read as zeros.
+inline bool make_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* base, int d, int H, int rows,
+              long long stride, int block) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(block)};
+    cuuint32_t one[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+
+// The rank-th request of a plan as the kernels read it, every word checked
+// against what the tensors hold, so that a plan of other sizes or a buffer
+// that no plan was made in reaches no memory outside them.
 struct Request {
     int row0, len, slot;
     bool fresh;   // no token seen: the state starts at zero
 };
-__device__ __forceinline__ bool read_request(const StepArgs& a, int r, Request& x) {
-    const int* p = a.plan;
-    const int lo = p[a.lay.offsets() + r], hi = p[a.lay.offsets() + r + 1];
-    x.slot = p[a.lay.slots() + r];
-    x.fresh = p[a.lay.seen() + r] <= 0;
-    x.row0 = lo;
-    x.len = hi - lo;
-    return x.slot >= 0 && x.slot < a.lay.S && lo >= 0 && hi > lo && hi <= a.rows;
-}
-// Requests of the plan that this call may walk.
-__device__ __forceinline__ int plan_requests(const StepArgs& a) {
+__device__ __forceinline__ bool read_request(const StepArgs& a, int rank, Request& x) {
     const int n = a.plan[4];
-    return n < a.requests ? n : a.requests;
+    const int4 w = reinterpret_cast<const int4*>(a.plan + a.lay.items())[rank];
+    x.row0 = w.x;
+    x.len = w.y;
+    x.slot = w.z;
+    x.fresh = w.w <= 0;
+    return rank < n && x.slot >= 0 && x.slot < a.lay.S && x.len > 0 && x.len <= a.rows && x.row0 >= 0 &&
+           x.row0 <= a.rows - x.len;
 }
 
 }  // namespace packed

@@ -128,7 +128,9 @@ int run_step(la_packed* h, const int* plan, const void* q, const void* k, const 
     DeviceGuard g(c.device);
     if (!g.ok) return fail(h, LA_ERR_CUDA, "cannot select the handle's device");
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    const cudaError_t e = chunk != 1 && blocks_ok ? la::packed::launch_chunk(a, s, h->encode) : la::packed::launch_step(a, s);
+    const cudaError_t e = chunk == 1 || !blocks_ok ? la::packed::launch_step(a, s)
+                          : c.d_v == 128       ? la::packed::launch_tc(a, s, h->encode)
+                                               : la::packed::launch_chunk(a, s, h->encode);
     if (e != cudaSuccess) return cuda_fail(h, e, chunk != 1 && blocks_ok ? "packed prefill launch" : "packed step launch");
     h->last_launches = 1;
     return LA_OK;

@@ -241,7 +241,6 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const PlanArgs a) {
             }
             a.slots[r] = now;
             a.plan[a.lay.slots() + r] = ok ? now : -1;
-            a.plan[a.lay.seen() + r] = a.seen[r];
             if (ok) {
                 key = 32 - __clz((n + kBlock - 1) / kBlock);
                 ++part;
@@ -285,7 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const PlanArgs a) {
         const int base = r < w1 ? hist[warp * 32 + key] : 0;
         __syncwarp();
         if (r < w1) {
+            const int use = a.plan[a.lay.slots() + r];   // this thread's own, from above
             a.plan[a.lay.order() + base + rank] = r;
+            reinterpret_cast<int4*>(a.plan + a.lay.items())[base + rank] =
+                make_int4(off[r], use >= 0 ? a.lengths[r] : 0, use, a.seen[r]);
             if (rank == 0) hist[warp * 32 + key] = base + __popc(peers);
         }
         __syncwarp();

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
     griddep_launch_dependents();
     griddep_wait();   // the plan and the states of the step before are complete
     const int per_req = a.Hv * uph;
-    const long long units = static_cast<long long>(plan_requests(a)) * per_req;
+    const long long units = static_cast<long long>(a.requests) * per_req;
     for (long long u = warp0; u < units; u += nwarps) {
         const int r = static_cast<int>(u / per_req);
         const int hu = static_cast<int>(u % per_req);

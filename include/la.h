@@ -424,7 +424,7 @@ void la_packed_destroy(la_packed* h);
 #define LA_PLAN_OFFSETS 8                                            /* [R + 1] */
 #define LA_PLAN_SLOTS(R) (LA_PLAN_OFFSETS + LA_PLAN_PAD((R) + 1))    /* [R] */
 #define LA_PLAN_ORDER(R) (LA_PLAN_SLOTS(R) + LA_PLAN_PAD(R))         /* [R] */
-#define LA_PLAN_TOKEN_REQUEST(R) (LA_PLAN_ORDER(R) + 2 * LA_PLAN_PAD(R))               /* [N] */
+#define LA_PLAN_TOKEN_REQUEST(R) (LA_PLAN_ORDER(R) + LA_PLAN_PAD(R) + 4LL * (R))         /* [N] */
 #define LA_PLAN_TOKEN_POSITION(R, N) (LA_PLAN_TOKEN_REQUEST(R) + LA_PLAN_PAD(N))       /* [N] */
 
 /* Faults of a plan (bits of counts[3]); the requests concerned take no part. */
