@@ -1,26 +1,27 @@
 // The gated delta rule over packed requests on the tcgen05 tensor cores: bf16
-// q, k and v, value heads of 128, blocks of 64 tokens. The algebra and the
-// precision are those of packed_chunk.cu (value heads of 64, warp-level MMAs):
-//   R = diag(b) (V - diag(G) K X^T),   U = T R,   T = (I + A)^-1
-//   O = diag(G) Q X^T + P U,           X <- G_63 X + U^T diag(D_63,.) K
-// with q, k, v exact, X, R, T and U in two bf16 parts wherever the state
-// depends on them, X in Q X^T and P in one.
+// q, k and v, value heads of 128, blocks of 64 tokens. The algebra is that of
+// packed_chunk.cu (value heads of 64, warp-level MMAs), with b's columns in T:
+//   T' = (I + A)^-1 diag(b),   U = T' (V - diag(G) K X^T)
+//   O = diag(G) Q X^T + P U,   X <- G_63 X + U^T diag(D_63,.) K
+// and so is the precision: q, k, v exact; X, G Z, T' and U in two bf16 parts
+// wherever the state depends on them; X in Q X^T and P in one.
 //
 // Work split. One CTA per (request, value head), the state's 128 rows on the
 // 128 tensor-memory lanes, so that every product of the chain is an M = 128
-// MMA with its A operand (X, R, U: bf16 parts) in tensor memory and its B
-// operand (K, Q, T, P) in shared memory:
-//   Z = X K^T, O = X Q^T  [dv][token],  U = R T^T,  dX = U' K,  O += U P^T
+// MMA with its A operand (X, R = -G Z, U: bf16 parts) in tensor memory and its
+// B operand (K, Q, T', P) in shared memory:
+//   Z = X K^T, O1 = X Q^T  [dv][token],  U = V^T T'^T + R T'^T,
+//   dX = U' K,  O2 = U P^T
 // Eight warps convert between them: thread (row r, half hh) holds half of row
 // r of X in fp32 registers and takes half the columns of each product. Four
-// prep warps compute T and P of the next block meanwhile; of the others one
+// prep warps compute T' and P of the next block meanwhile; of the others one
 // issues the chain's MMAs, one the loads, and one copies the outputs out.
 //
 // The chain's steps depend on one another, so what bounds a long request is
-// their latency: four products (Z 512 clocks at the rate of the tensor cores,
-// U 384, dX 512) with a conversion after each. Outputs are kept off that path:
-// Q X^T runs while R is formed, is scaled by G while U is computed, and the
-// block's outputs are read while the next block's Z runs.
+// their latency: three products (Z, R T'^T, dX) with a conversion after each.
+// High parts are published first, so that a product starts while the low ones
+// are still formed. V^T T'^T, Q X^T and the outputs run in the gaps: the
+// outputs of a block are read while the next one's Z runs.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -50,7 +51,7 @@ constexpr uint32_t kBarPrep = 1;      // named barrier of the prep warps
 constexpr int kTiles = 3;             // ring of K, Q and V tiles
 constexpr int kAStride = 68;          // floats per row of A
 constexpr int kMStride = 80;          // bytes per row of the 32x32 bf16 product between the two merges
-constexpr int kVec = 5 * C;           // floats of a block's gate vectors: g, b, b G, G, D_63
+constexpr int kVec = 4 * C;           // floats of a block's gate vectors: g, b, G, D_63
 
 template <int DK>
 struct TcLayout {
@@ -71,10 +72,12 @@ struct TcLayout {
     // high parts, then DK/4 of low ones; dX (fp32, DK columns) takes the same
     // columns once Z and Q X^T are done, each half over its own.
     static constexpr uint32_t COL_X = 0;
-    static constexpr uint32_t COL_Z = 128;     // Z, then U
-    static constexpr uint32_t COL_R = 192;     // R high, low (32 columns each); then U high, low
-    static constexpr uint32_t COL_UD = 256;    // U' high, low
-    static constexpr uint32_t COL_O = 320;     // two buffers of 64
+    // Z; R over it, per half of the tokens 16 columns of high parts, then 16 of low ones
+    static constexpr uint32_t COL_Z = 128;
+    static constexpr uint32_t COL_U = 192;     // U; its parts over it, like R
+    static constexpr uint32_t COL_UD = 256;    // parts of U'
+    static constexpr uint32_t COL_O1 = 320;
+    static constexpr uint32_t COL_O2 = 384;
     static constexpr uint32_t COL_G = 448;     // [K;Q] K^T
     static constexpr uint32_t TMEM_COLS = 512;
 };
@@ -92,8 +95,8 @@ struct Bars {
     uint64_t ot_full[kTiles];                    // converters: the output tile is written (8)
     uint64_t ready[2], tp_free[2];               // prep warps: T, P and vectors (4); MMA: T and P are read
     uint64_t g;                                  // MMA: [K;Q] K^T
-    uint64_t x, r, up, uo;                       // converters: X, R, U', (U and O scaled) published (8 each)
-    uint64_t z, o1, u, dx, o;                    // MMA: Z, Q X^T, U, dX, O done
+    uint64_t xh, xl, rh, rl, dh, dl, uo;         // converters: parts of X, R, U' and both of U published (8 each)
+    uint64_t z, u, dx, o;                        // MMA: Z, U, dX, O done
     uint64_t drain[2];                           // after a failure: MMAs of either issuer are done
     uint32_t tmem;
     int abort;
@@ -112,12 +115,51 @@ struct Ring3 {
 };
 
 // ---------------------------------------------------------------- prep warps
-// Four warps, block by block: [K;Q] K^T on the tensor cores, A and P row by
-// row (lane = tensor-memory lane = row; D_tj is a running product from the
-// diagonal leftwards), then T: 16x16 diagonal blocks by forward substitution
-// in fp32 (warps 0 and 1, a half-warp each), merged twice by
-// T21 = -T22 (A21 T11) on warp-level MMAs with two bf16 parts. Warp 3 computes
-// the next block's gate vectors while warps 0 and 1 solve.
+
+// A fragment of rows r0.., columns c0.. of an fp32 matrix in shared memory, in two bf16 parts.
+__device__ __forceinline__ void load_split(const float* m, int r0, int c0, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    const int lane = threadIdx.x & 31;
+    const float* p = m + (r0 + (lane >> 2)) * kAStride + c0 + 2 * (lane & 3);
+    const float2 y0 = *reinterpret_cast<const float2*>(p), y1 = *reinterpret_cast<const float2*>(p + 8 * kAStride);
+    const float2 y2 = *reinterpret_cast<const float2*>(p + 8), y3 = *reinterpret_cast<const float2*>(p + 8 * kAStride + 8);
+    split2(y0.x, y0.y, hi[0], lo[0]);
+    split2(y1.x, y1.y, hi[1], lo[1]);
+    split2(y2.x, y2.y, hi[2], lo[2]);
+    split2(y3.x, y3.y, hi[3], lo[3]);
+}
+// d[2] (16x16) += A B, A and B (two n-tiles) in two parts, the product of the low ones dropped.
+__device__ __forceinline__ void mma_split(float (&d)[2][4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                          const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
+    mma_16816(d[0], ah, bh[0], bh[1]);
+    mma_16816(d[1], ah, bh[2], bh[3]);
+    mma_16816(d[0], al, bh[0], bh[1]);
+    mma_16816(d[1], al, bh[2], bh[3]);
+    mma_16816(d[0], ah, bl[0], bl[1]);
+    mma_16816(d[1], ah, bl[2], bl[3]);
+}
+// -d as rows r0.., columns c0.. of T' (swizzled tiles of high and low parts).
+__device__ __forceinline__ void store_negated(uint32_t aTH, uint32_t aTL, int r0, int c0, const float (&d)[2][4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t hi, lo;
+            split2(-d[i][2 * h], -d[i][2 * h + 1], hi, lo);
+            const uint32_t o = sw128_off(r0 + 8 * h + (lane >> 2), c0 / 8 + i) + 4 * (lane & 3);
+            st_shared_b32(aTH + o, hi);
+            st_shared_b32(aTL + o, lo);
+        }
+}
+
+// Four warps, block by block: [K;Q] K^T on the tensor cores; E_tj = D_tj
+// k_t.k_j (j < t; warps 0, 1) and P_tj = D_tj q_t.k_j (j <= t; warps 2, 3) row
+// by row (lane = tensor-memory lane = row; D_tj is a running product from the
+// diagonal leftwards); then T' (A = diag(b) E): 16x16 diagonal blocks by
+// forward substitution in fp32 (warps 0 and 1, a half-warp each), merged twice
+// by T'_21 = -T'_22 (E_21 T'_11) on warp-level MMAs with two bf16 parts.
+// Meanwhile warp 2 issues the next block's [K;Q] K^T and warp 3 computes its
+// gate vectors.
 template <int DK>
 __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uint8_t* sm, uint32_t sbase, Bars* B,
                                            uint32_t tmem) {
@@ -126,10 +168,10 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
     const int gq = lane >> 2, cq = lane & 3;
     const int fr = (lane & 7) + ((lane >> 3) & 1) * 8, fc = lane >> 4;
     const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * pw) << 16);
+    const bool issuer = ptid == 64;
     volatile int* abort = &B->abort;
-    float* As = reinterpret_cast<float*>(sm + L::A);
+    float* E = reinterpret_cast<float*>(sm + L::A);
     const uint32_t aM = sbase + L::M;
-    constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
 
     // gate vectors of block c from tokens 2 lane, 2 lane + 1 (past the end: gate 1, beta 0)
     float2 gn = make_float2(1.f, 1.f), bn = make_float2(0.f, 0.f);
@@ -159,35 +201,43 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
         float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
         if (lane == 0) before = 1.f;
         if (lane == 31) after = 1.f;
-        const float G0 = before * gn.x;
         reinterpret_cast<float2*>(vec)[lane] = gn;
         reinterpret_cast<float2*>(vec + C)[lane] = bn;
-        reinterpret_cast<float2*>(vec + 2 * C)[lane] = make_float2(bn.x * G0, bn.y * pre);
-        reinterpret_cast<float2*>(vec + 3 * C)[lane] = make_float2(G0, pre);
-        reinterpret_cast<float2*>(vec + 4 * C)[lane] = make_float2(gn.y * after, after);
+        reinterpret_cast<float2*>(vec + 2 * C)[lane] = make_float2(before * gn.x, pre);
+        reinterpret_cast<float2*>(vec + 3 * C)[lane] = make_float2(gn.y * after, after);
+    };
+    auto issue_products = [&](int s) {   // [K;Q] K^T of the block in stage s
+        constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
+        const uint64_t d0 = kmaj(sbase + L::KQ + s * L::KQ_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < DK / 16; ++kk) {
+            const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
+            mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
+        }
+        mma_commit(&B->g);
     };
     if (pw == 3) {
         load_gates(0);
         write_gates(0);
     }
-    // T's sub-blocks above the diagonal stay zero: the MMAs read whole tiles
-    for (int i = ptid; i < 2 * 2 * 8192 / 16; i += kPrepThreads) {
-        const int b = i / 1024, o = i % 1024;   // buffer, 16-byte chunk of T high and low
-        st_shared_v4(sbase + L::TP + b * L::TP_BYTES + o * 16, 0, 0, 0, 0);
-    }
+    // T' and P above their diagonal blocks stay zero: the MMAs read whole tiles
+    for (int i = ptid; i < 2 * static_cast<int>(L::TP_BYTES) / 16; i += kPrepThreads)
+        st_shared_v4(sbase + L::TP + i * 16, 0, 0, 0, 0);
     named_sync(kBarPrep, kPrepThreads);
 
+    bool early = false;   // (issuer) this block's products were issued during the block before
     Ring3 at;
     for (int c = 0; c < w.blocks; ++c, at.next()) {
         const uint32_t kq = sbase + L::KQ + at.s * L::KQ_BYTES;
-        const uint32_t tp = sbase + L::TP + (c & 1) * L::TP_BYTES;
-        const uint32_t aTH = tp, aTL = tp + 8192, aP = tp + 16384;
+        const uint32_t aTH = sbase + L::TP + (c & 1) * L::TP_BYTES, aTL = aTH + 8192, aP = aTH + 16384;
         const float* vec = reinterpret_cast<const float*>(sm + L::VEC) + at.s * kVec;
+        Ring3 nx = at;
+        nx.next();
         if (pw == 3 && c + 1 < w.blocks) load_gates(c + 1);
-        bool ok = mbar_wait_or_abort(&B->kq_full[at.s], at.phase, abort);
+        bool ok = true;
         const int n = w.rq.len - c * C;
         if (n < C) {   // rows of the next request (or past the tensor): K and V zero, so that they leave the state alone
-            ok = ok && mbar_wait_or_abort(&B->v_full[at.s], at.phase, abort);
+            ok = mbar_wait_or_abort(&B->kq_full[at.s], at.phase, abort) && mbar_wait_or_abort(&B->v_full[at.s], at.phase, abort);
             if (ok) {
                 const uint32_t v = sbase + L::V + at.s * L::V_BYTES;
                 for (int i = ptid; i < (C - n) * 8; i += kPrepThreads) {
@@ -199,76 +249,93 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
                 }
             }
             fence_proxy_async_smem();
+            if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
         }
-        // the products of the block before are read, this one's tiles are whole
-        tc_fence_before();
-        if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
-        tc_fence_after();
-        if (ptid == 0) {
-#pragma unroll
-            for (int kk = 0; kk < DK / 16; ++kk) {
-                const uint64_t d = kmaj(kq + (kk / 4) * 16384 + (kk % 4) * 32);
-                mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
-            }
-            mma_commit(&B->g);
+        if (issuer && !early) {
+            ok = mbar_wait_or_abort(&B->kq_full[at.s], at.phase, abort);
+            if (ok) issue_products(at.s);
         }
-        ok = mbar_wait_or_abort(&B->g, c & 1, abort);
+        early = false;
+        __syncwarp();
+        ok = ok && mbar_wait_or_abort(&B->g, c & 1, abort);
         if (ok && c >= 2) ok = mbar_wait_or_abort(&B->tp_free[c & 1], ((c - 2) >> 1) & 1, abort);
         tc_fence_after();
-        if (!__all_sync(0xffffffffu, ok)) ok = false;
-        // ---- A (warps 0, 1) and P (warps 2, 3): row t, columns from the right ----------
-        const int t = 32 * (pw & 1) + lane;
+        ok = __all_sync(0xffffffffu, ok);
+        // ---- E and P by rows; D is zero right of the diagonal --------------------------
         if (ok) {
-            const float bt = vec[C + t];
-            float d = 0.f;
+            const bool isP = pw >= 2;
+            const int hd = pw & 1;   // the half of the columns with this warp's diagonal
+            const int t = 32 * hd + lane;
+            float x[32], d = 0.f;
+            tmem_ld32(tlane + L::COL_G + 32 * hd, x);
+            tmem_ld_wait();
+            const float* g = vec + 32 * hd;
+            float carry = 0.f;   // gate of the column to the right
 #pragma unroll
-            for (int h = 1; h >= 0; --h) {
-                float x[32];
-                tmem_ld32(tlane + L::COL_G + 32 * h, x);
+            for (int q4 = 7; q4 >= 0; --q4) {
+                const float4 g4 = *reinterpret_cast<const float4*>(g + 4 * q4);
+                const float gr[4] = {g4.y, g4.z, g4.w, carry};
+                carry = g4.x;
+#pragma unroll
+                for (int i = 3; i >= 0; --i) {
+                    const int j = 4 * q4 + i;
+                    d *= gr[i];
+                    if (lane == j) d = 1.f;
+                    x[j] *= d;
+                    if (lane == j && !isP) x[j] = 0.f;
+                }
+            }
+            auto store = [&](int h) {
+                if (isP) {
+                    chunk::store_row32_bf16(aP, t, 4 * h, x);
+                } else {
+#pragma unroll
+                    for (int q4 = 0; q4 < 8; ++q4)
+                        *reinterpret_cast<float4*>(E + t * kAStride + 32 * h + 4 * q4) =
+                            make_float4(x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]);
+                }
+            };
+            store(hd);
+            if (hd) {   // rows 32..63: columns 0..31 too
+                tmem_ld32(tlane + L::COL_G, x);
                 tmem_ld_wait();
-                float carry = 0.f;   // gate of the column to the right
-                if (h == 0) carry = vec[32];
 #pragma unroll
                 for (int q4 = 7; q4 >= 0; --q4) {
-                    const float4 g4 = *reinterpret_cast<const float4*>(vec + 32 * h + 4 * q4);
+                    const float4 g4 = *reinterpret_cast<const float4*>(vec + 4 * q4);
                     const float gr[4] = {g4.y, g4.z, g4.w, carry};
                     carry = g4.x;
 #pragma unroll
                     for (int i = 3; i >= 0; --i) {
-                        const int j = 32 * h + 4 * q4 + i;
-                        d = j == t ? 1.f : d * gr[i];
-                        const bool in = pw < 2 ? j < t : j <= t;
-                        x[4 * q4 + i] = in ? (pw < 2 ? bt * d : d) * x[4 * q4 + i] : 0.f;
+                        d *= gr[i];
+                        x[4 * q4 + i] *= d;
                     }
                 }
-                if (pw < 2) {
-#pragma unroll
-                    for (int q4 = 0; q4 < 8; ++q4)
-                        *reinterpret_cast<float4*>(As + t * kAStride + 32 * h + 4 * q4) =
-                            make_float4(x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]);
-                } else {
-                    chunk::store_row32_bf16(aP, t, 4 * h, x);
-                }
+                store(0);
             }
         }
+        tc_fence_before();
         if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
         if (pw < 2) {
-            // ---- diagonal blocks 2 pw and 2 pw + 1, lane = (block, column) -----------------
+            // ---- diagonal blocks 2 pw and 2 pw + 1, lane = (block, column): x_i = b_i (1_ij - sum E_is x_s),
+            //      column by column of E, four at a time ----------------------------------------
             const int blk = 2 * pw + (lane >> 4), col = lane & 15;
-            const float* ab = As + 16 * blk * kAStride + 16 * blk;
+            const float* eb = E + 16 * blk * kAStride + 16 * blk;
             float x[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s0 = i == col ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+            for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
 #pragma unroll
-                for (int j = 0; j < i; j += 4) {
-                    const float4 r = *reinterpret_cast<const float4*>(ab + i * kAStride + j);
-                    s0 -= r.x * x[j];
-                    if (j + 1 < i) s1 -= r.y * x[j + 1];
-                    if (j + 2 < i) s2 -= r.z * x[j + 2];
-                    if (j + 3 < i) s3 -= r.w * x[j + 3];
-                }
-                x[i] = (s0 + s1) + (s2 + s3);
+            for (int s4 = 0; s4 < 16; s4 += 4) {
+                const float4 b4 = *reinterpret_cast<const float4*>(vec + C + 16 * blk + s4);
+                float4 e[16];
+#pragma unroll
+                for (int i = s4 + 1; i < 16; ++i) e[i] = *reinterpret_cast<const float4*>(eb + i * kAStride + s4);
+                x[s4] *= b4.x;
+                x[s4 + 1] = b4.y * (x[s4 + 1] - e[s4 + 1].x * x[s4]);
+                x[s4 + 2] = b4.z * (x[s4 + 2] - e[s4 + 2].x * x[s4] - e[s4 + 2].y * x[s4 + 1]);
+                x[s4 + 3] = b4.w * (x[s4 + 3] - e[s4 + 3].x * x[s4] - e[s4 + 3].y * x[s4 + 1] - e[s4 + 3].z * x[s4 + 2]);
+#pragma unroll
+                for (int i = s4 + 4; i < 16; ++i)
+                    x[i] = x[i] - e[i].x * x[s4] - e[i].y * x[s4 + 1] - e[i].z * x[s4 + 2] - e[i].w * x[s4 + 3];
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -278,28 +345,14 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
                 st_shared_u16(aTL + o, __float2bfloat16_rn(x[i] - __bfloat162float(hi)));
             }
             __syncwarp();
-            // ---- the 16x16 block below: -T22 (A21 T11) -------------------------------------
+            // ---- the 16x16 block below: -T'_22 (E_21 T'_11) ----------------------------------
             const int rb = 32 * pw + 16, cb = 32 * pw;   // its first row and column
-            uint32_t ah[4], al[4], th[4], tl[4];
-            {
-                const float* p = As + (rb + gq) * kAStride + cb + 2 * cq;
-                const float2 y0 = *reinterpret_cast<const float2*>(p), y1 = *reinterpret_cast<const float2*>(p + 8 * kAStride);
-                const float2 y2 = *reinterpret_cast<const float2*>(p + 8), y3 = *reinterpret_cast<const float2*>(p + 8 * kAStride + 8);
-                split2(y0.x, y0.y, ah[0], al[0]);
-                split2(y1.x, y1.y, ah[1], al[1]);
-                split2(y2.x, y2.y, ah[2], al[2]);
-                split2(y3.x, y3.y, ah[3], al[3]);
-            }
-            float Mx[2][4] = {}, N[2][4] = {};
+            uint32_t ah[4], al[4], th[4], tl[4], mh[4], ml[4];
+            load_split(E, rb, cb, ah, al);
             ldsm4t(th, aTH + sw128_off(cb + fr, cb / 8 + fc));
             ldsm4t(tl, aTL + sw128_off(cb + fr, cb / 8 + fc));
-            mma_16816(Mx[0], ah, th[0], th[1]);
-            mma_16816(Mx[1], ah, th[2], th[3]);
-            mma_16816(Mx[0], al, th[0], th[1]);
-            mma_16816(Mx[1], al, th[2], th[3]);
-            mma_16816(Mx[0], ah, tl[0], tl[1]);
-            mma_16816(Mx[1], ah, tl[2], tl[3]);
-            uint32_t mh[4], ml[4];
+            float Mx[2][4] = {}, N[2][4] = {};
+            mma_split(Mx, ah, al, th, tl);
             split_tiles(Mx[0], Mx[1], mh, ml);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -308,54 +361,34 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
             }
             ldsm4(th, aTH + sw128_off(rb + fr, rb / 8 + fc));
             ldsm4(tl, aTL + sw128_off(rb + fr, rb / 8 + fc));
-            mma_16816(N[0], th, mh[0], mh[1]);
-            mma_16816(N[1], th, mh[2], mh[3]);
-            mma_16816(N[0], tl, mh[0], mh[1]);
-            mma_16816(N[1], tl, mh[2], mh[3]);
-            mma_16816(N[0], th, ml[0], ml[1]);
-            mma_16816(N[1], th, ml[2], ml[3]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t hi, lo;
-                    split2(-N[i][2 * h], -N[i][2 * h + 1], hi, lo);
-                    const uint32_t o = sw128_off(rb + 8 * h + gq, cb / 8 + i) + 4 * cq;
-                    st_shared_b32(aTH + o, hi);
-                    st_shared_b32(aTL + o, lo);
-                }
-        } else if (pw == 3 && c + 1 < w.blocks) {
-            Ring3 nx = at;
-            nx.next();
-            // the slot's vectors of block c - 2 are read (its phase is the one before block c + 1's)
-            if (c + 1 < kTiles || __all_sync(0xffffffffu, mbar_wait_or_abort(&B->vec_free[nx.s], nx.phase ^ 1, abort)))
-                write_gates(nx.s);
-            else
-                ok = false;
+            mma_split(N, th, tl, mh, ml);
+            store_negated(aTH, aTL, rb, cb, N);
+        } else if (pw == 3) {
+            if (c + 1 < w.blocks) {
+                // the slot's vectors of block c - 2 are read (its phase is the one before block c + 1's)
+                if (c + 1 < kTiles || __all_sync(0xffffffffu, mbar_wait_or_abort(&B->vec_free[nx.s], nx.phase ^ 1, abort)))
+                    write_gates(nx.s);
+                else
+                    ok = false;
+            }
+        } else if (issuer && w.rq.len - (c + 1) * C >= C && mbar_try_wait(smem_u32(&B->kq_full[nx.s]), nx.phase)) {
+            // the next block is whole and here: its products now (this one's are read)
+            tc_fence_after();
+            issue_products(nx.s);
+            early = true;
         }
         if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
-        // ---- rows 32..63, columns 0..31: -T_B (A_BA T_A), a 16x16 tile per warp -----------
+        // ---- rows 32..63, columns 0..31: -T'_B (E_BA T'_A), a 16x16 tile per warp -----------
         {
             const int mi = pw >> 1, ni = pw & 1;
-            float Mx[2][4] = {};
+            float Mx[2][4] = {}, N[2][4] = {};
+            uint32_t ah[4], al[4], th[4], tl[4];
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                uint32_t ah[4], al[4], th[4], tl[4];
-                const float* p = As + (32 + 16 * mi + gq) * kAStride + 16 * kk + 2 * cq;
-                const float2 y0 = *reinterpret_cast<const float2*>(p), y1 = *reinterpret_cast<const float2*>(p + 8 * kAStride);
-                const float2 y2 = *reinterpret_cast<const float2*>(p + 8), y3 = *reinterpret_cast<const float2*>(p + 8 * kAStride + 8);
-                split2(y0.x, y0.y, ah[0], al[0]);
-                split2(y1.x, y1.y, ah[1], al[1]);
-                split2(y2.x, y2.y, ah[2], al[2]);
-                split2(y3.x, y3.y, ah[3], al[3]);
+                load_split(E, 32 + 16 * mi, 16 * kk, ah, al);
                 ldsm4t(th, aTH + sw128_off(16 * kk + fr, 2 * ni + fc));
                 ldsm4t(tl, aTL + sw128_off(16 * kk + fr, 2 * ni + fc));
-                mma_16816(Mx[0], ah, th[0], th[1]);
-                mma_16816(Mx[1], ah, th[2], th[3]);
-                mma_16816(Mx[0], al, th[0], th[1]);
-                mma_16816(Mx[1], al, th[2], th[3]);
-                mma_16816(Mx[0], ah, tl[0], tl[1]);
-                mma_16816(Mx[1], ah, tl[2], tl[3]);
+                mma_split(Mx, ah, al, th, tl);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -368,31 +401,15 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
                     st_shared_b32(aM + 32 * kMStride + o, lo);
                 }
             named_sync(kBarPrep, kPrepThreads);
-            float N[2][4] = {};
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                uint32_t th[4], tl[4], mh[4], ml[4];
-                ldsm4(th, aTH + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
-                ldsm4(tl, aTL + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
-                ldsm4t(mh, aM + (16 * kk + fr) * kMStride + (2 * ni + fc) * 16);
-                ldsm4t(ml, aM + 32 * kMStride + (16 * kk + fr) * kMStride + (2 * ni + fc) * 16);
-                mma_16816(N[0], th, mh[0], mh[1]);
-                mma_16816(N[1], th, mh[2], mh[3]);
-                mma_16816(N[0], tl, mh[0], mh[1]);
-                mma_16816(N[1], tl, mh[2], mh[3]);
-                mma_16816(N[0], th, ml[0], ml[1]);
-                mma_16816(N[1], th, ml[2], ml[3]);
+                ldsm4(ah, aTH + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
+                ldsm4(al, aTL + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
+                ldsm4t(th, aM + (16 * kk + fr) * kMStride + (2 * ni + fc) * 16);
+                ldsm4t(tl, aM + 32 * kMStride + (16 * kk + fr) * kMStride + (2 * ni + fc) * 16);
+                mma_split(N, ah, al, th, tl);
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t hi, lo;
-                    split2(-N[i][2 * h], -N[i][2 * h + 1], hi, lo);
-                    const uint32_t o = sw128_off(32 + 16 * mi + 8 * h + gq, 2 * ni + i) + 4 * cq;
-                    st_shared_b32(aTH + o, hi);
-                    st_shared_b32(aTL + o, lo);
-                }
+            store_negated(aTH, aTL, 32 + 16 * mi, 16 * ni, N);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -431,8 +448,8 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             mbar_init(&B->tp_free[i], 1);
             mbar_init(&B->drain[i], 1);
         }
-        for (uint64_t* b : {&B->x, &B->r, &B->up, &B->uo}) mbar_init(b, kConvWarps);
-        for (uint64_t* b : {&B->g, &B->z, &B->o1, &B->u, &B->dx, &B->o}) mbar_init(b, 1);
+        for (uint64_t* b : {&B->xh, &B->xl, &B->rh, &B->rl, &B->dh, &B->dl, &B->uo}) mbar_init(b, kConvWarps);
+        for (uint64_t* b : {&B->g, &B->z, &B->u, &B->dx, &B->o}) mbar_init(b, 1);
         B->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmq);
@@ -476,17 +493,26 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             __syncwarp();
             if (lane == 0) mbar_arrive(b);
         };
-        auto store_split = [&](uint32_t hi_col, uint32_t lo_col, const float* x) {   // 32 values: 16 columns each
-            uint32_t h[16], l[16];
+        // 32 values: their high parts to 16 columns, kept in h for the low ones' turn
+        auto store_high = [&](uint32_t col, const float* x, uint32_t (&h)[16]) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) split2(x[2 * i], x[2 * i + 1], h[i], l[i]);
-            tmem_st16(hi_col, h);
-            tmem_st16(lo_col, l);
+            for (int i = 0; i < 16; ++i) h[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+            tmem_st16(col, h);
+        };
+        auto store_low = [&](uint32_t col, const float* x, const uint32_t (&h)[16]) {
+            uint32_t l[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) l[i] = low_parts(x[2 * i], x[2 * i + 1], h[i]);
+            tmem_st16(col, l);
         };
         auto publish_x = [&]() {
+            uint32_t h[XH / 32][16];
 #pragma unroll
-            for (int p = 0; p < XH / 32; ++p) store_split(colx + 16 * p, colx + XH / 2 + 16 * p, X + 32 * p);
-            signal(&B->x);
+            for (int p = 0; p < XH / 32; ++p) store_high(colx + 16 * p, X + 32 * p, h[p]);
+            signal(&B->xh);
+#pragma unroll
+            for (int p = 0; p < XH / 32; ++p) store_low(colx + XH / 2 + 16 * p, X + 32 * p, h[p]);
+            signal(&B->xl);
         };
         // warp-uniform before the warp-collective tensor-memory accesses
         auto wait_all = [&](uint64_t* b, uint32_t parity) {
@@ -496,27 +522,39 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         };
         publish_x();
         Ring3 at, last;
-        // outputs of block c: O through the tile over its V, [64 t][128], 16-byte
+        // outputs of block c, o = G O1 + O2, through the tile over its V, [64 t][128], 16-byte
         // chunks of odd tokens shifted by half a bank row
         auto outputs = [&](int c, int s) {
             wait_all(&B->o, c & 1);
             if (fail) return;
             const bool odd = lane & 1;
             const int ch = (r & ~1) / 8;
-            const uint32_t ot = sbase + L::V + s * L::V_BYTES + (r & 6) * 2;
-            float o[32];
-            tmem_ld32(tl + L::COL_O + 64 * (c & 1) + 32 * hh, o);
+            const uint32_t ot = sbase + L::V + s * L::V_BYTES + (r & 6) * 2 + 32 * hh * 256 + (odd ? 256 : 0) + ((ch ^ (odd ? 4 : 0)) << 4);
+            const float* G = reinterpret_cast<const float*>(sm + L::VEC) + s * kVec + 2 * C + 32 * hh;
+            float o[32], o2[32];
+            tmem_ld32(tl + L::COL_O1 + 32 * hh, o);
+            tmem_ld32(tl + L::COL_O2 + 32 * hh, o2);
             tmem_ld_wait();
 #pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const float send = odd ? o[2 * m] : o[2 * m + 1];
+            for (int i = 0; i < 32; i += 4) {
+                const float4 g4 = *reinterpret_cast<const float4*>(G + i);
+                o[i] = g4.x * o[i] + o2[i];
+                o[i + 1] = g4.y * o[i + 1] + o2[i + 1];
+                o[i + 2] = g4.z * o[i + 2] + o2[i + 2];
+                o[i + 3] = g4.w * o[i + 3] + o2[i + 3];
+            }
+#pragma unroll
+            for (int m = 0; m < 16; ++m) {   // lane pairs trade values: two adjacent rows of one token per lane
+                const float send = odd ? o[2 * m] : o[2 * m + 1], keep = odd ? o[2 * m + 1] : o[2 * m];
                 const float recv = __shfl_xor_sync(0xffffffffu, send, 1);
-                const int t = 32 * hh + 2 * m + (odd ? 1 : 0);
-                st_shared_b32(ot + t * 256 + ((ch ^ (odd ? 4 : 0)) << 4), odd ? pack_bf16(recv, o[2 * m + 1]) : pack_bf16(o[2 * m], recv));
+                st_shared_b32(ot + 512 * m, odd ? pack_bf16(recv, keep) : pack_bf16(keep, recv));
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&B->ot_full[s]);
+            if (lane == 0) {
+                mbar_arrive(&B->ot_full[s]);
+                mbar_arrive(&B->vec_free[s]);
+            }
         };
         for (int c = 0; c < w.blocks && !fail; ++c) {
             const int s = at.s;
@@ -524,67 +562,51 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             if (c > 0) outputs(c - 1, last.s);
             const float* vec = reinterpret_cast<const float*>(sm + L::VEC) + s * kVec;
             float y[32];
-            // ---- R = b V - b G Z, tokens 32 hh .. ------------------------------------
+            uint32_t h[16];
+            // ---- R = -G Z, tokens 32 hh .. --------------------------------------------
             wait_all(&B->ready[p], (c >> 1) & 1);
-            wait_all(&B->v_full[s], at.phase);
             wait_all(&B->z, p);
             if (fail) break;
-            tmem_ld32(tl + L::COL_Z + 32 * hh, y);
-            {
-                const uint32_t av = sbase + L::V + s * L::V_BYTES + (r / 64) * 8192 + (r % 8) * 2;
-                const uint32_t c8 = (r % 64) / 8;
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = ld_shared_bf16(av + sw128_off(32 * hh + i, c8));
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 b4 = *reinterpret_cast<const float4*>(vec + C + 32 * hh + i);
-                    const float4 g4 = *reinterpret_cast<const float4*>(vec + 2 * C + 32 * hh + i);
-                    y[i] = b4.x * v[i] - g4.x * y[i];
-                    y[i + 1] = b4.y * v[i + 1] - g4.y * y[i + 1];
-                    y[i + 2] = b4.z * v[i + 2] - g4.z * y[i + 2];
-                    y[i + 3] = b4.w * v[i + 3] - g4.w * y[i + 3];
-                }
-            }
-            store_split(tl + L::COL_R + 16 * hh, tl + L::COL_R + 32 + 16 * hh, y);
-            signal(&B->r);
-            // ---- O = G (Q X^T), in place, while U is computed ---------------------------
-            wait_all(&B->o1, p);
-            if (fail) break;
-            tmem_ld32(tl + L::COL_O + 64 * p + 32 * hh, y);
+            const uint32_t colz = tl + L::COL_Z + 32 * hh, colu = tl + L::COL_U + 32 * hh, cold = tl + L::COL_UD + 32 * hh;
+            tmem_ld32(colz, y);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(vec + 3 * C + 32 * hh + i);
-                y[i] *= g4.x;
-                y[i + 1] *= g4.y;
-                y[i + 2] *= g4.z;
-                y[i + 3] *= g4.w;
+                const float4 g4 = *reinterpret_cast<const float4*>(vec + 2 * C + 32 * hh + i);
+                y[i] *= -g4.x;
+                y[i + 1] *= -g4.y;
+                y[i + 2] *= -g4.z;
+                y[i + 3] *= -g4.w;
             }
-            tmem_st32(tl + L::COL_O + 64 * p + 32 * hh, reinterpret_cast<const uint32_t(&)[32]>(y));
+            store_high(colz, y, h);
+            signal(&B->rh);
+            store_low(colz + 16, y, h);
+            signal(&B->rl);
             // ---- U' = U D_63 for the state, then U for the outputs ------------------------
             wait_all(&B->u, p);
             if (fail) break;
-            tmem_ld32(tl + L::COL_Z + 32 * hh, y);
+            tmem_ld32(colu, y);
             tmem_ld_wait();
             {
                 float d[32];
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
-                    const float4 d4 = *reinterpret_cast<const float4*>(vec + 4 * C + 32 * hh + i);
+                    const float4 d4 = *reinterpret_cast<const float4*>(vec + 3 * C + 32 * hh + i);
                     d[i] = y[i] * d4.x;
                     d[i + 1] = y[i + 1] * d4.y;
                     d[i + 2] = y[i + 2] * d4.z;
                     d[i + 3] = y[i + 3] * d4.w;
                 }
-                store_split(tl + L::COL_UD + 16 * hh, tl + L::COL_UD + 32 + 16 * hh, d);
+                store_high(cold, d, h);
+                signal(&B->dh);
+                store_low(cold + 16, d, h);
+                signal(&B->dl);
             }
-            signal(&B->up);
-            store_split(tl + L::COL_R + 16 * hh, tl + L::COL_R + 32 + 16 * hh, y);
+            store_high(colu, y, h);
+            store_low(colu + 16, y, h);
             signal(&B->uo);
             // ---- X = G_63 X + dX ----------------------------------------------------------
-            const float gc = vec[3 * C + C - 1];
+            const float gc = vec[2 * C + C - 1];
             wait_all(&B->dx, p);
             if (fail) break;
 #pragma unroll
@@ -595,8 +617,6 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 for (int i = 0; i < 32; ++i) X[32 * q + i] = gc * X[32 * q + i] + y[i];
             }
             if (c + 1 < w.blocks) publish_x();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B->vec_free[s]);
             last = at;
             at.next();
         }
@@ -621,64 +641,95 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         // ======================= MMA issue ==========================================
         if (lane == 0) {
             constexpr uint32_t ID_64 = idesc_bf16(128, 64, false, false);
-            constexpr uint32_t ID_K = idesc_bf16(128, DK, false, true);
-            // the A operand of k-step kk: channels 16 kk ..
+            constexpr uint32_t ID_V = idesc_bf16(128, 64, true, false);    // V^T T'^T
+            constexpr uint32_t ID_K = idesc_bf16(128, DK, false, true);    // U' K
+            // the A operands of k-step kk: channels 16 kk .., tokens 16 kk ..
             auto colx = [&](int kk) { return tmem + L::COL_X + (kk / (XH / 16)) * XH + (kk % (XH / 16)) * 8; };
+            auto colt = [](uint32_t col, int kk) { return col + (kk / 2) * 32 + (kk % 2) * 8; };
+            // operand descriptors of stage 0; offsets in 16-byte units are added to them
+            const uint64_t dK0 = kmaj(sbase + L::KQ), dKm0 = mnmaj(sbase + L::KQ, 16384), dV0 = mnmaj(sbase + L::V, 8192);
+            const uint64_t dT0 = kmaj(sbase + L::TP);
+            const uint32_t cz = tmem + L::COL_Z, cu = tmem + L::COL_U, cd = tmem + L::COL_UD;
             Ring3 at;
             for (int c = 0; c < w.blocks && !fail; ++c, at.next()) {
                 const uint32_t p = c & 1;
-                const uint32_t kq = sbase + L::KQ + at.s * L::KQ_BYTES;
-                const uint32_t tp = sbase + L::TP + p * L::TP_BYTES;
-                wait(&B->kq_full[at.s], at.phase);
-                wait(&B->ready[p], (c >> 1) & 1);
-                wait(&B->x, p);
-                if (fail) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk)
-                    mma_bf16_ts(tmem + L::COL_Z, colx(kk), kmaj(kq + (kk / 4) * 16384 + (kk % 4) * 32), ID_64, kk > 0);
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk)
-                    mma_bf16_ts(tmem + L::COL_Z, colx(kk) + XH / 2, kmaj(kq + (kk / 4) * 16384 + (kk % 4) * 32), ID_64, true);
-                mma_commit(&B->z);
-                if (c >= 2) {   // the outputs of block c - 2 have left this buffer
-                    Ring3 two = at;   // c - 2 is the next stage's block before
-                    two.next();
-                    wait(&B->ot_full[two.s], two.phase ^ 1);
-                    if (fail) break;
+                const uint64_t dK = dK0 + at.s * (L::KQ_BYTES / 16), dKm = dKm0 + at.s * (L::KQ_BYTES / 16);
+                const uint64_t dV = dV0 + at.s * (L::V_BYTES / 16);
+                const uint64_t dT = dT0 + p * (L::TP_BYTES / 16);
+                auto kstep = [](int kk) { return static_cast<uint64_t>((kk / 4) * 1024 + (kk % 4) * 2); };
+                auto start_u = [&]() {   // U = V^T T'^T, both parts of T'; the parts of the U before are read by now
+                    wait(&B->v_full[at.s], at.phase);
+                    if (c >= 1) wait(&B->o, p ^ 1);
+                    if (fail) return;
                     tc_fence_after();
-                }
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk)
-                    mma_bf16_ts(tmem + L::COL_O + 64 * p, colx(kk), kmaj(kq + 8192 + (kk / 4) * 16384 + (kk % 4) * 32), ID_64,
-                                kk > 0);
-                mma_commit(&B->o1);
-                wait(&B->r, p);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        mma_bf16_ss(cu, dV + kk * 128, dT + kk * 2, ID_V, kk > 0);
+                        mma_bf16_ss(cu, dV + kk * 128, dT + 512 + kk * 2, ID_V, true);
+                    }
+                };
+                // before X is published if T' is there already
+                const bool u_early = mbar_try_wait(smem_u32(&B->ready[p]), (c >> 1) & 1);
+                if (u_early) start_u();
+                wait(&B->kq_full[at.s], at.phase);
+                if (c + 1 == w.blocks) wait(&B->ready[p], (c >> 1) & 1);   // K's rows past the end are zeroed
+                wait(&B->xh, p);
+                if (fail) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk), dK + kstep(kk), ID_64, kk > 0);
+                wait(&B->xl, p);
+                if (fail) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk) + XH / 2, dK + kstep(kk), ID_64, true);
+                mma_commit(&B->z);
+                if (!u_early) {
+                    wait(&B->ready[p], (c >> 1) & 1);
+                    start_u();
+                }
+                if (c >= 1) {   // the outputs of the block before are read
+                    Ring3 before = at;
+                    before.next();
+                    before.next();   // the stage of block c + 2, and of block c - 1 a round earlier
+                    wait(&B->ot_full[before.s], before.phase ^ 1);
+                }
+                if (fail) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(tmem + L::COL_O1, colx(kk), dK + 512 + kstep(kk), ID_64, kk > 0);
+                wait(&B->rh, p);
                 if (fail) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16_ts(tmem + L::COL_Z, tmem + L::COL_R + 8 * kk, kmaj(tp + kk * 32), ID_64, kk > 0);
-                    mma_bf16_ts(tmem + L::COL_Z, tmem + L::COL_R + 32 + 8 * kk, kmaj(tp + kk * 32), ID_64, true);
-                    mma_bf16_ts(tmem + L::COL_Z, tmem + L::COL_R + 8 * kk, kmaj(tp + 8192 + kk * 32), ID_64, true);
+                    mma_bf16_ts(cu, colt(cz, kk), dT + kk * 2, ID_64, true);
+                    mma_bf16_ts(cu, colt(cz, kk), dT + 512 + kk * 2, ID_64, true);
                 }
+                wait(&B->rl, p);
+                if (fail) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cu, colt(cz, kk) + 16, dT + kk * 2, ID_64, true);
                 mma_commit(&B->u);
-                wait(&B->up, p);
+                wait(&B->dh, p);
                 if (fail) break;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16_ts(tmem + L::COL_X, tmem + L::COL_UD + 8 * kk, mnmaj(kq + kk * 2048, 16384), ID_K, kk > 0);
-                    mma_bf16_ts(tmem + L::COL_X, tmem + L::COL_UD + 32 + 8 * kk, mnmaj(kq + kk * 2048, 16384), ID_K, true);
-                }
+                for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk), dKm + kk * 128, ID_K, kk > 0);
+                wait(&B->dl, p);
+                if (fail) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk) + 16, dKm + kk * 128, ID_K, true);
                 mma_commit(&B->dx);
                 wait(&B->uo, p);
                 if (fail) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16_ts(tmem + L::COL_O + 64 * p, tmem + L::COL_R + 8 * kk, kmaj(tp + 16384 + kk * 32), ID_64, true);
-                    mma_bf16_ts(tmem + L::COL_O + 64 * p, tmem + L::COL_R + 32 + 8 * kk, kmaj(tp + 16384 + kk * 32), ID_64, true);
+                    mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk), dT + 1024 + kk * 2, ID_64, kk > 0);
+                    mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk) + 16, dT + 1024 + kk * 2, ID_64, true);
                 }
                 mma_commit(&B->o);
                 // only where somebody will wait: an arrival after the CTA has left would hit another's memory
