@@ -21,7 +21,7 @@
 // their latency: three products (Z, R T'^T, dX) with a conversion after each.
 // High parts are published first, so that a product starts while the low ones
 // are still formed. V^T T'^T, Q X^T and the outputs run in the gaps: the
-// outputs of a block are read while the next one's Z runs.
+// outputs of a block are read while the next one's Z and U run.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -51,7 +51,7 @@ constexpr uint32_t kBarPrep = 1;      // named barrier of the prep warps
 constexpr int kTiles = 3;             // ring of K, Q and V tiles
 constexpr int kAStride = 68;          // floats per row of A
 constexpr int kMStride = 80;          // bytes per row of the 32x32 bf16 product between the two merges
-constexpr int kVec = 4 * C;           // floats of a block's gate vectors: g, b, G, D_63
+constexpr int kVec = 6 * C;           // floats of a block's gate vectors: g, b, G, D_63, and G inside 16 and 32 tokens
 
 template <int DK>
 struct TcLayout {
@@ -96,12 +96,21 @@ struct Bars {
     uint64_t ready[2], tp_free[2];               // prep warps: T, P and vectors (4); MMA: T and P are read
     uint64_t g;                                  // MMA: [K;Q] K^T
     uint64_t xh, xl, rh, rl, dh, dl, uo;         // converters: parts of X, R, U' and both of U published (8 each)
-    uint64_t z, u, dx, o;                        // MMA: Z, U, dX, O done
+    uint64_t z, u, o1, dx, o;                    // MMA: Z, U, Q X^T, dX, O done
     uint64_t drain[2];                           // after a failure: MMAs of either issuer are done
     uint32_t tmem;
     int abort;
 };
 static_assert(sizeof(Bars) <= 40 * 8, "barrier space");
+
+// One lane of a converged warp; MMAs issued under it keep their descriptors in
+// uniform registers (a single thread's branch takes 45 clocks per MMA to issue,
+// more than the 32 that an M = 128, N = 64 one runs).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
 
 struct Ring3 {
     int s = 0;
@@ -168,7 +177,8 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
     const int gq = lane >> 2, cq = lane & 3;
     const int fr = (lane & 7) + ((lane >> 3) & 1) * 8, fc = lane >> 4;
     const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * pw) << 16);
-    const bool issuer = ptid == 64;
+    const bool issuer = pw == 2;
+    const bool el = elect_one();
     volatile int* abort = &B->abort;
     float* E = reinterpret_cast<float*>(sm + L::A);
     const uint32_t aM = sbase + L::M;
@@ -198,6 +208,19 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
             if (lane >= o) pre *= y;
             if (lane + o < 32) suf *= z;
         }
+        float g16 = gn.x * gn.y;   // up to this pair's second token, from the start of its 16 (32) tokens
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, g16, o);
+            if ((lane & 7) >= o) g16 *= y;
+        }
+        const float first = __shfl_sync(0xffffffffu, g16, (lane & 16) + 7);   // all of the 32's first 16
+        const float g32 = lane & 8 ? first * g16 : g16;
+        float b16 = __shfl_up_sync(0xffffffffu, g16, 1), b32 = __shfl_up_sync(0xffffffffu, g32, 1);
+        if ((lane & 7) == 0) b16 = 1.f;
+        if ((lane & 15) == 0) b32 = 1.f;
+        reinterpret_cast<float2*>(vec + 4 * C)[lane] = make_float2(b16 * gn.x, g16);
+        reinterpret_cast<float2*>(vec + 5 * C)[lane] = make_float2(b32 * gn.x, g32);
         float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
         if (lane == 0) before = 1.f;
         if (lane == 31) after = 1.f;
@@ -209,12 +232,15 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
     auto issue_products = [&](int s) {   // [K;Q] K^T of the block in stage s
         constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
         const uint64_t d0 = kmaj(sbase + L::KQ + s * L::KQ_BYTES);
+        if (el) {
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) {
-            const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
-            mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
+            for (int kk = 0; kk < DK / 16; ++kk) {
+                const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
+                mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
+            }
+            mma_commit(&B->g);
         }
-        mma_commit(&B->g);
+        __syncwarp();
     };
     if (pw == 3) {
         load_gates(0);
@@ -252,40 +278,39 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
             if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
         }
         if (issuer && !early) {
-            ok = mbar_wait_or_abort(&B->kq_full[at.s], at.phase, abort);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(&B->kq_full[at.s], at.phase, abort));
             if (ok) issue_products(at.s);
         }
         early = false;
-        __syncwarp();
         ok = ok && mbar_wait_or_abort(&B->g, c & 1, abort);
         if (ok && c >= 2) ok = mbar_wait_or_abort(&B->tp_free[c & 1], ((c - 2) >> 1) & 1, abort);
         tc_fence_after();
         ok = __all_sync(0xffffffffu, ok);
-        // ---- E and P by rows; D is zero right of the diagonal --------------------------
+        // ---- E and P by rows, 16 columns at a time; D is zero right of the diagonal -----------
         if (ok) {
             const bool isP = pw >= 2;
             const int hd = pw & 1;   // the half of the columns with this warp's diagonal
             const int t = 32 * hd + lane;
-            float x[32], d = 0.f;
-            tmem_ld32(tlane + L::COL_G + 32 * hd, x);
-            tmem_ld_wait();
-            const float* g = vec + 32 * hd;
-            float carry = 0.f;   // gate of the column to the right
+            // x *= D over columns c0 .. c0 + 15 from the right, d being D right of them: a running product
+            // that starts on the diagonal (`diag`: lane of column c0's row, -1 without one) or at the column's edge
+            auto decay = [&](float (&x)[32], int c0, int xo, float d, int diag) {
+                float carry = c0 + 16 < C ? vec[c0 + 16] : 1.f;   // gate of the column to the right
 #pragma unroll
-            for (int q4 = 7; q4 >= 0; --q4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(g + 4 * q4);
-                const float gr[4] = {g4.y, g4.z, g4.w, carry};
-                carry = g4.x;
+                for (int q4 = 3; q4 >= 0; --q4) {
+                    const float4 g4 = *reinterpret_cast<const float4*>(vec + c0 + 4 * q4);
+                    const float gr[4] = {g4.y, g4.z, g4.w, carry};
+                    carry = g4.x;
 #pragma unroll
-                for (int i = 3; i >= 0; --i) {
-                    const int j = 4 * q4 + i;
-                    d *= gr[i];
-                    if (lane == j) d = 1.f;
-                    x[j] *= d;
-                    if (lane == j && !isP) x[j] = 0.f;
+                    for (int i = 3; i >= 0; --i) {
+                        const int j = 4 * q4 + i;
+                        if (j < 15) d *= gr[i];   // (column 15's is d itself: the caller's starts past its right edge)
+                        if (diag >= 0 && lane == diag + j) d = 1.f;
+                        x[xo + j] *= d;
+                        if (diag >= 0 && lane == diag + j && !isP) x[xo + j] = 0.f;
+                    }
                 }
-            }
-            auto store = [&](int h) {
+            };
+            auto store = [&](const float (&x)[32], int h) {
                 if (isP) {
                     chunk::store_row32_bf16(aP, t, 4 * h, x);
                 } else {
@@ -295,22 +320,21 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
                             make_float4(x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]);
                 }
             };
-            store(hd);
-            if (hd) {   // rows 32..63: columns 0..31 too
+            float x[32];
+            tmem_ld32(tlane + L::COL_G + 32 * hd, x);
+            const float g16 = vec[4 * C + t], g32 = vec[5 * C + t];
+            tmem_ld_wait();
+            // the diagonal's half: columns 16.. (rows 16.. of the half; zero for the others) and 0..15
+            // (rows 16..: all of the row's gates from 16 on, i.e. g16, are between)
+            decay(x, 32 * hd + 16, 16, 0.f, 16);
+            decay(x, 32 * hd, 0, lane >= 16 ? g16 : 0.f, 0);
+            store(x, hd);
+            if (hd) {   // rows 32..63: columns 16..31, then 0..15 with the gates of 16..31 besides
                 tmem_ld32(tlane + L::COL_G, x);
                 tmem_ld_wait();
-#pragma unroll
-                for (int q4 = 7; q4 >= 0; --q4) {
-                    const float4 g4 = *reinterpret_cast<const float4*>(vec + 4 * q4);
-                    const float gr[4] = {g4.y, g4.z, g4.w, carry};
-                    carry = g4.x;
-#pragma unroll
-                    for (int i = 3; i >= 0; --i) {
-                        d *= gr[i];
-                        x[4 * q4 + i] *= d;
-                    }
-                }
-                store(0);
+                decay(x, 16, 16, g32, -1);
+                decay(x, 0, 0, g32 * vec[4 * C + 31], -1);
+                store(x, 0);
             }
         }
         tc_fence_before();
@@ -371,10 +395,12 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
                 else
                     ok = false;
             }
-        } else if (issuer && w.rq.len - (c + 1) * C >= C && mbar_try_wait(smem_u32(&B->kq_full[nx.s]), nx.phase)) {
-            // the next block is whole and here: its products now (this one's are read)
+        } else if (issuer && w.rq.len - (c + 1) * C >= C) {
+            // the next block is whole: its products now (this one's are read). Its loads wait for the
+            // chain alone, which has all it needs for the blocks before.
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&B->kq_full[nx.s], nx.phase, abort));
             tc_fence_after();
-            issue_products(nx.s);
+            if (ok) issue_products(nx.s);
             early = true;
         }
         if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
@@ -449,7 +475,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             mbar_init(&B->drain[i], 1);
         }
         for (uint64_t* b : {&B->xh, &B->xl, &B->rh, &B->rl, &B->dh, &B->dl, &B->uo}) mbar_init(b, kConvWarps);
-        for (uint64_t* b : {&B->g, &B->z, &B->u, &B->dx, &B->o}) mbar_init(b, 1);
+        for (uint64_t* b : {&B->g, &B->z, &B->u, &B->o1, &B->dx, &B->o}) mbar_init(b, 1);
         B->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmq);
@@ -494,9 +520,12 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             if (lane == 0) mbar_arrive(b);
         };
         // 32 values: their high parts to 16 columns, kept in h for the low ones' turn
-        auto store_high = [&](uint32_t col, const float* x, uint32_t (&h)[16]) {
+        auto pack_high = [&](const float* x, uint32_t (&h)[16]) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) h[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        };
+        auto store_high = [&](uint32_t col, const float* x, uint32_t (&h)[16]) {
+            pack_high(x, h);
             tmem_st16(col, h);
         };
         auto store_low = [&](uint32_t col, const float* x, const uint32_t (&h)[16]) {
@@ -506,12 +535,15 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             tmem_st16(col, l);
         };
         auto publish_x = [&]() {
-            uint32_t h[XH / 32][16];
+            uint32_t h[16];
 #pragma unroll
-            for (int p = 0; p < XH / 32; ++p) store_high(colx + 16 * p, X + 32 * p, h[p]);
+            for (int p = 0; p < XH / 32; ++p) store_high(colx + 16 * p, X + 32 * p, h);
             signal(&B->xh);
 #pragma unroll
-            for (int p = 0; p < XH / 32; ++p) store_low(colx + XH / 2 + 16 * p, X + 32 * p, h[p]);
+            for (int p = 0; p < XH / 32; ++p) {   // (the high parts again: fewer registers than keeping them)
+                if (XH > 32) pack_high(X + 32 * p, h);
+                store_low(colx + XH / 2 + 16 * p, X + 32 * p, h);
+            }
             signal(&B->xl);
         };
         // warp-uniform before the warp-collective tensor-memory accesses
@@ -522,21 +554,21 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         };
         publish_x();
         Ring3 at, last;
-        // outputs of block c, o = G O1 + O2, through the tile over its V, [64 t][128], 16-byte
-        // chunks of odd tokens shifted by half a bank row
-        auto outputs = [&](int c, int s) {
-            wait_all(&B->o, c & 1);
+        // outputs of block c, o = G O1 + O2, 16 tokens a half (q) at a time, through the tile over its V,
+        // [64 t][128], 16-byte chunks of odd tokens shifted by half a bank row
+        auto outputs = [&](int c, int s, int q) {
+            if (q == 0) wait_all(&B->o, c & 1);
             if (fail) return;
             const bool odd = lane & 1;
-            const int ch = (r & ~1) / 8;
-            const uint32_t ot = sbase + L::V + s * L::V_BYTES + (r & 6) * 2 + 32 * hh * 256 + (odd ? 256 : 0) + ((ch ^ (odd ? 4 : 0)) << 4);
-            const float* G = reinterpret_cast<const float*>(sm + L::VEC) + s * kVec + 2 * C + 32 * hh;
-            float o[32], o2[32];
-            tmem_ld32(tl + L::COL_O1 + 32 * hh, o);
-            tmem_ld32(tl + L::COL_O2 + 32 * hh, o2);
+            const int ch = (r & ~1) / 8, t0 = 32 * hh + 16 * q;
+            const uint32_t ot = sbase + L::V + s * L::V_BYTES + (r & 6) * 2 + (t0 + (odd ? 1 : 0)) * 256 + ((ch ^ (odd ? 4 : 0)) << 4);
+            const float* G = reinterpret_cast<const float*>(sm + L::VEC) + s * kVec + 2 * C + t0;
+            float o[16], o2[16];
+            tmem_ld16(tl + L::COL_O1 + t0, o);
+            tmem_ld16(tl + L::COL_O2 + t0, o2);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
+            for (int i = 0; i < 16; i += 4) {
                 const float4 g4 = *reinterpret_cast<const float4*>(G + i);
                 o[i] = g4.x * o[i] + o2[i];
                 o[i + 1] = g4.y * o[i + 1] + o2[i + 1];
@@ -544,11 +576,12 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 o[i + 3] = g4.w * o[i + 3] + o2[i + 3];
             }
 #pragma unroll
-            for (int m = 0; m < 16; ++m) {   // lane pairs trade values: two adjacent rows of one token per lane
+            for (int m = 0; m < 8; ++m) {   // lane pairs trade values: two adjacent rows of one token per lane
                 const float send = odd ? o[2 * m] : o[2 * m + 1], keep = odd ? o[2 * m + 1] : o[2 * m];
                 const float recv = __shfl_xor_sync(0xffffffffu, send, 1);
                 st_shared_b32(ot + 512 * m, odd ? pack_bf16(recv, keep) : pack_bf16(keep, recv));
             }
+            if (q == 0) return;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -559,7 +592,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         for (int c = 0; c < w.blocks && !fail; ++c) {
             const int s = at.s;
             const uint32_t p = c & 1;
-            if (c > 0) outputs(c - 1, last.s);
+            if (c > 0) outputs(c - 1, last.s, 0);   // while Z is computed
             const float* vec = reinterpret_cast<const float*>(sm + L::VEC) + s * kVec;
             float y[32];
             uint32_t h[16];
@@ -582,26 +615,26 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             signal(&B->rh);
             store_low(colz + 16, y, h);
             signal(&B->rl);
+            if (c > 0) outputs(c - 1, last.s, 1);   // while U is computed
             // ---- U' = U D_63 for the state, then U for the outputs ------------------------
             wait_all(&B->u, p);
             if (fail) break;
             tmem_ld32(colu, y);
             tmem_ld_wait();
-            {
-                float d[32];
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 d4 = *reinterpret_cast<const float4*>(vec + 3 * C + 32 * hh + i);
-                    d[i] = y[i] * d4.x;
-                    d[i + 1] = y[i + 1] * d4.y;
-                    d[i + 2] = y[i + 2] * d4.z;
-                    d[i + 3] = y[i + 3] * d4.w;
-                }
-                store_high(cold, d, h);
-                signal(&B->dh);
-                store_low(cold + 16, d, h);
-                signal(&B->dl);
+            for (int i = 0; i < 32; i += 4) {
+                const float4 d4 = *reinterpret_cast<const float4*>(vec + 3 * C + 32 * hh + i);
+                y[i] *= d4.x;
+                y[i + 1] *= d4.y;
+                y[i + 2] *= d4.z;
+                y[i + 3] *= d4.w;
             }
+            store_high(cold, y, h);
+            signal(&B->dh);
+            store_low(cold + 16, y, h);
+            signal(&B->dl);
+            tmem_ld32(colu, y);
+            tmem_ld_wait();
             store_high(colu, y, h);
             store_low(colu + 16, y, h);
             signal(&B->uo);
@@ -624,122 +657,144 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
 #pragma unroll
             for (int i = 0; i < XH; i += 4)
                 *reinterpret_cast<float4*>(sp + i) = make_float4(X[i], X[i + 1], X[i + 2], X[i + 3]);
-            outputs(w.blocks - 1, last.s);
+            outputs(w.blocks - 1, last.s, 0);
+            outputs(w.blocks - 1, last.s, 1);
         }
         if (fail) status = kStatusMmaWait;
     } else if (warp < kConvWarps + kPrepWarps) {
         if (!prep_warps<DK>(a, w, sm, sbase, B, tmem)) {
             fail = true;
             status = kStatusMmaWait;
-            if (tid == 32 * kConvWarps) {
-                *abort = 1;
+            *abort = 1;
+            if (warp == kConvWarps + 2 && elect_one()) {   // the lane that issued this role's MMAs
                 mma_commit(&B->drain[1]);
                 mbar_wait(&B->drain[1], 0, 100000000ull);
             }
+            __syncwarp();
         }
     } else if (warp == kConvWarps + kPrepWarps) {
         // ======================= MMA issue ==========================================
-        if (lane == 0) {
+        {
+            const bool el = elect_one();
             constexpr uint32_t ID_64 = idesc_bf16(128, 64, false, false);
             constexpr uint32_t ID_V = idesc_bf16(128, 64, true, false);    // V^T T'^T
             constexpr uint32_t ID_K = idesc_bf16(128, DK, false, true);    // U' K
             // the A operands of k-step kk: channels 16 kk .., tokens 16 kk ..
             auto colx = [&](int kk) { return tmem + L::COL_X + (kk / (XH / 16)) * XH + (kk % (XH / 16)) * 8; };
             auto colt = [](uint32_t col, int kk) { return col + (kk / 2) * 32 + (kk % 2) * 8; };
+            auto kstep = [](int kk) { return static_cast<uint64_t>((kk / 4) * 1024 + (kk % 4) * 2); };
             // operand descriptors of stage 0; offsets in 16-byte units are added to them
             const uint64_t dK0 = kmaj(sbase + L::KQ), dKm0 = mnmaj(sbase + L::KQ, 16384), dV0 = mnmaj(sbase + L::V, 8192);
             const uint64_t dT0 = kmaj(sbase + L::TP);
             const uint32_t cz = tmem + L::COL_Z, cu = tmem + L::COL_U, cd = tmem + L::COL_UD;
+            auto wait_w = [&](uint64_t* b, uint32_t parity) {   // the whole warp goes on, or gives up, together
+                const bool ok = !fail && mbar_wait_or_abort(b, parity, abort);
+                fail = !__all_sync(0xffffffffu, ok);
+                tc_fence_after();
+            };
             Ring3 at;
             for (int c = 0; c < w.blocks && !fail; ++c, at.next()) {
                 const uint32_t p = c & 1;
                 const uint64_t dK = dK0 + at.s * (L::KQ_BYTES / 16), dKm = dKm0 + at.s * (L::KQ_BYTES / 16);
                 const uint64_t dV = dV0 + at.s * (L::V_BYTES / 16);
                 const uint64_t dT = dT0 + p * (L::TP_BYTES / 16);
-                auto kstep = [](int kk) { return static_cast<uint64_t>((kk / 4) * 1024 + (kk % 4) * 2); };
                 auto start_u = [&]() {   // U = V^T T'^T, both parts of T'; the parts of the U before are read by now
-                    wait(&B->v_full[at.s], at.phase);
-                    if (c >= 1) wait(&B->o, p ^ 1);
-                    if (fail) return;
-                    tc_fence_after();
+                    wait_w(&B->v_full[at.s], at.phase);
+                    if (c >= 1) wait_w(&B->o, p ^ 1);
+                    if (!fail && el) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        mma_bf16_ss(cu, dV + kk * 128, dT + kk * 2, ID_V, kk > 0);
-                        mma_bf16_ss(cu, dV + kk * 128, dT + 512 + kk * 2, ID_V, true);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            mma_bf16_ss(cu, dV + kk * 128, dT + kk * 2, ID_V, kk > 0);
+                            mma_bf16_ss(cu, dV + kk * 128, dT + 512 + kk * 2, ID_V, true);
+                        }
                     }
                 };
                 // before X is published if T' is there already
-                const bool u_early = mbar_try_wait(smem_u32(&B->ready[p]), (c >> 1) & 1);
+                const bool u_early = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&B->ready[p]), (c >> 1) & 1));
                 if (u_early) start_u();
-                wait(&B->kq_full[at.s], at.phase);
-                if (c + 1 == w.blocks) wait(&B->ready[p], (c >> 1) & 1);   // K's rows past the end are zeroed
-                wait(&B->xh, p);
+                wait_w(&B->kq_full[at.s], at.phase);
+                if (c + 1 == w.blocks) wait_w(&B->ready[p], (c >> 1) & 1);   // K's rows past the end are zeroed
+                wait_w(&B->xh, p);
                 if (fail) break;
-                tc_fence_after();
+                if (el) {
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk), dK + kstep(kk), ID_64, kk > 0);
-                wait(&B->xl, p);
+                    for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk), dK + kstep(kk), ID_64, kk > 0);
+                }
+                wait_w(&B->xl, p);
                 if (fail) break;
-                tc_fence_after();
+                if (el) {
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk) + XH / 2, dK + kstep(kk), ID_64, true);
-                mma_commit(&B->z);
+                    for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk) + XH / 2, dK + kstep(kk), ID_64, true);
+                    mma_commit(&B->z);
+                }
                 if (!u_early) {
-                    wait(&B->ready[p], (c >> 1) & 1);
+                    wait_w(&B->ready[p], (c >> 1) & 1);
                     start_u();
+                }
+                wait_w(&B->rh, p);
+                if (fail) break;
+                if (el) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        mma_bf16_ts(cu, colt(cz, kk), dT + kk * 2, ID_64, true);
+                        mma_bf16_ts(cu, colt(cz, kk), dT + 512 + kk * 2, ID_64, true);
+                    }
+                }
+                wait_w(&B->rl, p);
+                if (fail) break;
+                if (el) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cu, colt(cz, kk) + 16, dT + kk * 2, ID_64, true);
+                    mma_commit(&B->u);
                 }
                 if (c >= 1) {   // the outputs of the block before are read
                     Ring3 before = at;
                     before.next();
                     before.next();   // the stage of block c + 2, and of block c - 1 a round earlier
-                    wait(&B->ot_full[before.s], before.phase ^ 1);
+                    wait_w(&B->ot_full[before.s], before.phase ^ 1);
+                    if (fail) break;
                 }
-                if (fail) break;
-                tc_fence_after();
+                if (el) {
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(tmem + L::COL_O1, colx(kk), dK + 512 + kstep(kk), ID_64, kk > 0);
-                wait(&B->rh, p);
-                if (fail) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16_ts(cu, colt(cz, kk), dT + kk * 2, ID_64, true);
-                    mma_bf16_ts(cu, colt(cz, kk), dT + 512 + kk * 2, ID_64, true);
+                    for (int kk = 0; kk < DK / 16; ++kk)
+                        mma_bf16_ts(tmem + L::COL_O1, colx(kk), dK + 512 + kstep(kk), ID_64, kk > 0);
+                    mma_commit(&B->o1);
                 }
-                wait(&B->rl, p);
+                wait_w(&B->dh, p);
+                wait_w(&B->o1, p);   // X is read: dX may take its columns
                 if (fail) break;
-                tc_fence_after();
+                if (el) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cu, colt(cz, kk) + 16, dT + kk * 2, ID_64, true);
-                mma_commit(&B->u);
-                wait(&B->dh, p);
-                if (fail) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk), dKm + kk * 128, ID_K, kk > 0);
-                wait(&B->dl, p);
-                if (fail) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk) + 16, dKm + kk * 128, ID_K, true);
-                mma_commit(&B->dx);
-                wait(&B->uo, p);
-                if (fail) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk), dT + 1024 + kk * 2, ID_64, kk > 0);
-                    mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk) + 16, dT + 1024 + kk * 2, ID_64, true);
+                    for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk), dKm + kk * 128, ID_K, kk > 0);
                 }
-                mma_commit(&B->o);
-                // only where somebody will wait: an arrival after the CTA has left would hit another's memory
-                if (c + kTiles < w.blocks) mma_commit(&B->kq_free[at.s]);
-                if (c + 2 < w.blocks) mma_commit(&B->tp_free[p]);
+                wait_w(&B->dl, p);
+                if (fail) break;
+                if (el) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk) + 16, dKm + kk * 128, ID_K, true);
+                    mma_commit(&B->dx);
+                }
+                wait_w(&B->uo, p);
+                if (fail) break;
+                if (el) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk), dT + 1024 + kk * 2, ID_64, kk > 0);
+                        mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk) + 16, dT + 1024 + kk * 2, ID_64, true);
+                    }
+                    mma_commit(&B->o);
+                    // only where somebody will wait: an arrival after the CTA has left would hit another's memory
+                    if (c + kTiles < w.blocks) mma_commit(&B->kq_free[at.s]);
+                    if (c + 2 < w.blocks) mma_commit(&B->tp_free[p]);
+                }
             }
             if (fail) {   // every MMA issued completes before the CTA leaves (bounded)
                 status = kStatusMmaWait;
-                mma_commit(&B->drain[0]);
-                mbar_wait(&B->drain[0], 0, 100000000ull);
+                if (el) {
+                    mma_commit(&B->drain[0]);
+                    mbar_wait(&B->drain[0], 0, 100000000ull);
+                }
+                __syncwarp();
             }
         }
     } else if (warp == kConvWarps + kPrepWarps + 1) {
