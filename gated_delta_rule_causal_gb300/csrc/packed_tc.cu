@@ -6,8 +6,11 @@
 // and so is the precision: q, k, v exact; X, G Z, T' and U in two bf16 parts
 // wherever the state depends on them; X in Q X^T and P in one.
 //
-// Work split. One CTA per (request, value head), the state's 128 rows on the
-// 128 tensor-memory lanes, so that every product of the chain is an M = 128
+// Work split. A CTA takes one (request, value head) after another, longest
+// requests first: the grid has one CTA for each, and a running one takes over
+// the next that has not been started (cluster launch control), so that its
+// prep and load warps are already at the next request while the chain finishes
+// one. The state's 128 rows lie on the 128 tensor-memory lanes, so that every product of the chain is an M = 128
 // MMA with its A operand (X, R = -G Z, U: bf16 parts) in tensor memory and its
 // B operand (K, Q, T', P) in shared memory:
 //   Z = X K^T, O1 = X Q^T  [dv][token],  U = V^T T'^T + R T'^T,
@@ -15,7 +18,8 @@
 // Eight warps convert between them: thread (row r, half hh) holds half of row
 // r of X in fp32 registers and takes half the columns of each product. Four
 // prep warps compute T' and P of the next block meanwhile; of the others one
-// issues the chain's MMAs, one the loads, and one copies the outputs out.
+// issues the chain's MMAs, one the loads, one copies the outputs out, and one
+// fetches the work.
 //
 // The chain's steps depend on one another, so what bounds a long request is
 // their latency: three products (Z, R T'^T, dX) with a conversion after each.
@@ -45,10 +49,11 @@ using chunk::st_shared_v4;
 constexpr int C = 64;                 // tokens per block
 constexpr int DV = 128;
 constexpr int kConvWarps = 8, kPrepWarps = 4;
-constexpr int kThreads = 32 * (kConvWarps + kPrepWarps + 3);   // + MMA issue, loads, output copies
+constexpr int kThreads = 32 * (kConvWarps + kPrepWarps + 4);   // + MMA issue, loads, output copies, work
 constexpr int kPrepThreads = 32 * kPrepWarps;
 constexpr uint32_t kBarPrep = 1;      // named barrier of the prep warps
 constexpr int kTiles = 3;             // ring of K, Q and V tiles
+constexpr int kItems = 4;             // ring of work items (the loads run at most three blocks ahead)
 constexpr int kAStride = 68;          // floats per row of A
 constexpr int kMStride = 80;          // bytes per row of the 32x32 bf16 product between the two merges
 constexpr int kVec = 6 * C;           // floats of a block's gate vectors: g, b, G, D_63, and G inside 16 and 32 tokens
@@ -67,7 +72,7 @@ struct TcLayout {
     static constexpr uint32_t M = A + C * kAStride * 4;         // bf16 high, low [32][kMStride bytes]
     static constexpr uint32_t VEC = M + 2 * 32 * kMStride;      // [kTiles][kVec] fp32
     static constexpr uint32_t BAR = VEC + kTiles * kVec * 4;
-    static constexpr uint32_t BYTES = BAR + 40 * 8;
+    static constexpr uint32_t BYTES = BAR + 1024;
     // Tensor memory columns. X: per half hh of the channels DK/4 columns of
     // high parts, then DK/4 of low ones; dX (fp32, DK columns) takes the same
     // columns once Z and Q X^T are done, each half over its own.
@@ -82,9 +87,10 @@ struct TcLayout {
     static constexpr uint32_t TMEM_COLS = 512;
 };
 
-struct Work {
-    Request rq;
-    int head, khead, blocks;
+// A (request, value head); blocks 0: there is no more.
+struct __align__(16) Work {
+    int row0, len, slot, fresh;
+    int head, khead, blocks, pad;
 };
 
 // Barriers, in shared memory.
@@ -98,10 +104,13 @@ struct Bars {
     uint64_t xh, xl, rh, rl, dh, dl, uo;         // converters: parts of X, R, U' and both of U published (8 each)
     uint64_t z, u, o1, dx, o;                    // MMA: Z, U, Q X^T, dX, O done
     uint64_t drain[2];                           // after a failure: MMAs of either issuer are done
+    uint64_t item_full[kItems], item_free[kItems];   // work warp; every other warp has read the item (15)
+    uint64_t want, stolen;                       // loads: all of the item is issued; the answer to a request for more work
     uint32_t tmem;
     int abort;
+    uint4 answer;
+    Work item[kItems];
 };
-static_assert(sizeof(Bars) <= 40 * 8, "barrier space");
 
 // One lane of a converged warp; MMAs issued under it keep their descriptors in
 // uniform registers (a single thread's branch takes 45 clocks per MMA to issue,
@@ -111,6 +120,8 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
     return e != 0;
 }
+
+static_assert(sizeof(Bars) <= 1024, "barrier space");
 
 struct Ring3 {
     int s = 0;
@@ -122,6 +133,46 @@ struct Ring3 {
         }
     }
 };
+
+// The k-th item of this CTA, for a whole warp; false when there is none (blocks
+// 0) or after a failure.
+__device__ __forceinline__ bool next_item(Bars* B, int k, Work& w, bool& fail) {
+    const int i = k % kItems;
+    const bool ok = mbar_wait_or_abort(&B->item_full[i], (k / kItems) & 1, &B->abort);
+    if (!__all_sync(0xffffffffu, ok)) {
+        fail = true;
+        return false;
+    }
+    w = B->item[i];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&B->item_free[i]);
+    return w.blocks > 0;
+}
+
+// Ask for a CTA of this grid that has not been started to be taken over; the
+// answer (16 bytes) completes on `bar`.
+__device__ __forceinline__ void steal_request(uint4* answer, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(smem_u32(answer)), "r"(smem_u32(bar)) : "memory");
+}
+// The block index of the CTA taken over, or -1.
+__device__ __forceinline__ int stolen_index(const uint4* answer) {
+    int idx;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 x;\n\t"
+        "ld.shared.b128 r, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "mov.b32 x, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 x, r;\n\t"
+        "mov.b32 %0, x;\n\t}"
+        : "=r"(idx) : "r"(smem_u32(answer)) : "memory");
+    return idx;
+}
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z) : "memory");
+}
 
 // ---------------------------------------------------------------- prep warps
 
@@ -170,8 +221,7 @@ __device__ __forceinline__ void store_negated(uint32_t aTH, uint32_t aTL, int r0
 // Meanwhile warp 2 issues the next block's [K;Q] K^T and warp 3 computes its
 // gate vectors.
 template <int DK>
-__device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uint8_t* sm, uint32_t sbase, Bars* B,
-                                           uint32_t tmem) {
+__device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint32_t sbase, Bars* B, uint32_t tmem) {
     using L = TcLayout<DK>;
     const int lane = threadIdx.x & 31, pw = (threadIdx.x >> 5) - kConvWarps, ptid = threadIdx.x - 32 * kConvWarps;
     const int gq = lane >> 2, cq = lane & 3;
@@ -185,16 +235,16 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
 
     // gate vectors of block c from tokens 2 lane, 2 lane + 1 (past the end: gate 1, beta 0)
     float2 gn = make_float2(1.f, 1.f), bn = make_float2(0.f, 0.f);
-    auto load_gates = [&](int c) {
+    auto load_gates = [&](const Work& w, int c) {
         const int t = c * C + 2 * lane;
-        const size_t i = static_cast<size_t>(w.rq.row0 + t) * a.Hv + w.head;
+        const size_t i = static_cast<size_t>(w.row0 + t) * a.Hv + w.head;
         gn = make_float2(1.f, 1.f);
         bn = make_float2(0.f, 0.f);
-        if (t < w.rq.len) {
+        if (t < w.len) {
             gn.x = __ldg(a.gate + i);
             bn.x = __ldg(a.beta + i);
         }
-        if (t + 1 < w.rq.len) {
+        if (t + 1 < w.len) {
             gn.y = __ldg(a.gate + i + a.Hv);
             bn.y = __ldg(a.beta + i + a.Hv);
         }
@@ -242,8 +292,12 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
         }
         __syncwarp();
     };
+    Work w, wn;       // of the current and the next block
+    int items = 1;
+    bool lost = false;
+    if (!next_item(B, 0, w, lost)) return !lost;
     if (pw == 3) {
-        load_gates(0);
+        load_gates(w, 0);
         write_gates(0);
     }
     // T' and P above their diagonal blocks stay zero: the MMAs read whole tiles
@@ -253,17 +307,26 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
 
     bool early = false;   // (issuer) this block's products were issued during the block before
     Ring3 at;
-    for (int c = 0; c < w.blocks; ++c, at.next()) {
+    // block c of the item, block nb of the CTA
+    for (int c = 0, nb = 0; w.blocks > 0; ++nb, at.next()) {
         const uint32_t kq = sbase + L::KQ + at.s * L::KQ_BYTES;
-        const uint32_t aTH = sbase + L::TP + (c & 1) * L::TP_BYTES, aTL = aTH + 8192, aP = aTH + 16384;
+        const uint32_t aTH = sbase + L::TP + (nb & 1) * L::TP_BYTES, aTL = aTH + 8192, aP = aTH + 16384;
         const float* vec = reinterpret_cast<const float*>(sm + L::VEC) + at.s * kVec;
         Ring3 nx = at;
         nx.next();
-        if (pw == 3 && c + 1 < w.blocks) load_gates(c + 1);
-        bool ok = true;
-        const int n = w.rq.len - c * C;
+        int cn = c + 1;
+        wn = w;
+        if (cn == w.blocks) {
+            cn = 0;
+            next_item(B, items++, wn, lost);   // (blocks 0: this block is the last)
+            if (lost) wn.blocks = 0;
+        }
+        const bool more = wn.blocks > 0;
+        if (pw == 3 && more) load_gates(wn, cn);
+        bool ok = !lost;
+        const int n = w.len - c * C;
         if (n < C) {   // rows of the next request (or past the tensor): K and V zero, so that they leave the state alone
-            ok = mbar_wait_or_abort(&B->kq_full[at.s], at.phase, abort) && mbar_wait_or_abort(&B->v_full[at.s], at.phase, abort);
+            ok = ok && mbar_wait_or_abort(&B->kq_full[at.s], at.phase, abort) && mbar_wait_or_abort(&B->v_full[at.s], at.phase, abort);
             if (ok) {
                 const uint32_t v = sbase + L::V + at.s * L::V_BYTES;
                 for (int i = ptid; i < (C - n) * 8; i += kPrepThreads) {
@@ -282,8 +345,8 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
             if (ok) issue_products(at.s);
         }
         early = false;
-        ok = ok && mbar_wait_or_abort(&B->g, c & 1, abort);
-        if (ok && c >= 2) ok = mbar_wait_or_abort(&B->tp_free[c & 1], ((c - 2) >> 1) & 1, abort);
+        ok = ok && mbar_wait_or_abort(&B->g, nb & 1, abort);
+        if (ok && nb >= 2) ok = mbar_wait_or_abort(&B->tp_free[nb & 1], ((nb - 2) >> 1) & 1, abort);
         tc_fence_after();
         ok = __all_sync(0xffffffffu, ok);
         // ---- E and P by rows, 16 columns at a time; D is zero right of the diagonal -----------
@@ -388,14 +451,14 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
             mma_split(N, th, tl, mh, ml);
             store_negated(aTH, aTL, rb, cb, N);
         } else if (pw == 3) {
-            if (c + 1 < w.blocks) {
-                // the slot's vectors of block c - 2 are read (its phase is the one before block c + 1's)
-                if (c + 1 < kTiles || __all_sync(0xffffffffu, mbar_wait_or_abort(&B->vec_free[nx.s], nx.phase ^ 1, abort)))
+            if (more) {
+                // the slot's vectors of block nb - 2 are read (its phase is the one before block nb + 1's)
+                if (nb + 1 < kTiles || __all_sync(0xffffffffu, mbar_wait_or_abort(&B->vec_free[nx.s], nx.phase ^ 1, abort)))
                     write_gates(nx.s);
                 else
                     ok = false;
             }
-        } else if (issuer && w.rq.len - (c + 1) * C >= C) {
+        } else if (issuer && more && wn.len - cn * C >= C) {
             // the next block is whole: its products now (this one's are read). Its loads wait for the
             // chain alone, which has all it needs for the blocks before.
             ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&B->kq_full[nx.s], nx.phase, abort));
@@ -439,7 +502,9 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, const Work& w, uin
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B->ready[c & 1]);
+        if (lane == 0) mbar_arrive(&B->ready[nb & 1]);
+        w = wn;
+        c = cn;
     }
     return true;
 }
@@ -474,6 +539,12 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             mbar_init(&B->tp_free[i], 1);
             mbar_init(&B->drain[i], 1);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&B->item_full[i], 1);
+            mbar_init(&B->item_free[i], kThreads / 32 - 1);
+        }
+        mbar_init(&B->want, 1);
+        mbar_init(&B->stolen, 1);
         for (uint64_t* b : {&B->xh, &B->xl, &B->rh, &B->rl, &B->dh, &B->dl, &B->uo}) mbar_init(b, kConvWarps);
         for (uint64_t* b : {&B->g, &B->z, &B->u, &B->o1, &B->dx, &B->o}) mbar_init(b, 1);
         B->abort = 0;
@@ -483,11 +554,10 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         tma_prefetch_desc(&tmv);
     }
     griddep_wait();
-    Work w;
-    if (!read_request(a, blockIdx.x / a.Hv, w.rq)) return;
-    w.head = blockIdx.x % a.Hv;
-    w.khead = w.head / (a.Hv / a.Hk);
-    w.blocks = (w.rq.len + C - 1) / C;
+    {   // requests without a part come last: where this CTA's has none, nobody's after it has
+        Request rq;
+        if (!read_request(a, blockIdx.x / a.Hv, rq)) return;
+    }
     if (warp == 0) tmem_alloc(&B->tmem, L::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
@@ -502,17 +572,29 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         const int r = 32 * (warp & 3) + lane, hh = warp >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t colx = tl + L::COL_X + hh * XH;
-        float* sp = a.states + ((static_cast<size_t>(w.rq.slot) * a.Hv + w.head) * DV + r) * DK + hh * XH;
         float X[XH];
+        // The state in global memory, 8 lanes to 128 contiguous bytes of a row: this lane reads and writes
+        // chunk (lane & 7) of 32 floats' 16-byte chunks of the rows of its group of 8 lanes, and trades with the
+        // group for its own row's (an 8x8 transpose of 16-byte chunks).
+        auto state_row = [&](const Work& w) {
+            return a.states + ((static_cast<size_t>(w.slot) * a.Hv + w.head) * DV + (r & ~7)) * DK + hh * XH + 4 * (lane & 7);
+        };
+        auto trade = [&]() {
 #pragma unroll
-        for (int i = 0; i < XH; i += 4) {
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!w.rq.fresh) y = *reinterpret_cast<const float4*>(sp + i);
-            X[i] = y.x;
-            X[i + 1] = y.y;
-            X[i + 2] = y.z;
-            X[i + 3] = y.w;
-        }
+            for (int q = 0; q < XH; q += 32)
+#pragma unroll
+                for (int b = 1; b < 8; b <<= 1)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (!(j & b)) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float &lo = X[q + 4 * j + e], &hi = X[q + 4 * (j | b) + e];
+                                const float y = __shfl_xor_sync(0xffffffffu, lane & b ? lo : hi, b);
+                                if (lane & b) lo = y; else hi = y;
+                            }
+                        }
+        };
         auto signal = [&](uint64_t* b) {   // this warp's tensor-memory stores (and loads) are done
             tmem_st_wait();
             tc_fence_before();
@@ -552,12 +634,11 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             fail = !__all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
-        publish_x();
         Ring3 at, last;
-        // outputs of block c, o = G O1 + O2, 16 tokens a half (q) at a time, through the tile over its V,
+        // outputs of block nb, o = G O1 + O2, 16 tokens a half (q) at a time, through the tile over its V,
         // [64 t][128], 16-byte chunks of odd tokens shifted by half a bank row
-        auto outputs = [&](int c, int s, int q) {
-            if (q == 0) wait_all(&B->o, c & 1);
+        auto outputs = [&](int nb, int s, int q) {
+            if (q == 0) wait_all(&B->o, nb & 1);
             if (fail) return;
             const bool odd = lane & 1;
             const int ch = (r & ~1) / 8, t0 = 32 * hh + 16 * q;
@@ -589,15 +670,35 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 mbar_arrive(&B->vec_free[s]);
             }
         };
-        for (int c = 0; c < w.blocks && !fail; ++c) {
+        Work w;
+        int nb = 0;   // blocks of the CTA so far
+        for (int k = 0; !fail && next_item(B, k, w, fail); ++k) {
+        float* sp = state_row(w);
+        if (!w.fresh) {
+#pragma unroll
+            for (int i = 0; i < XH / 4; ++i) {
+                const float4 y = __ldcs(reinterpret_cast<const float4*>(sp + (i % 8) * DK + 32 * (i / 8)));
+                X[4 * i] = y.x;
+                X[4 * i + 1] = y.y;
+                X[4 * i + 2] = y.z;
+                X[4 * i + 3] = y.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < XH; ++i) X[i] = 0.f;
+        }
+        if (nb > 0) outputs(nb - 1, last.s, 0);   // while the state arrives
+        if (!w.fresh) trade();
+        publish_x();
+        for (int c = 0; c < w.blocks && !fail; ++c, ++nb) {
             const int s = at.s;
-            const uint32_t p = c & 1;
-            if (c > 0) outputs(c - 1, last.s, 0);   // while Z is computed
+            const uint32_t p = nb & 1;
+            if (c > 0) outputs(nb - 1, last.s, 0);   // while Z is computed
             const float* vec = reinterpret_cast<const float*>(sm + L::VEC) + s * kVec;
             float y[32];
             uint32_t h[16];
             // ---- R = -G Z, tokens 32 hh .. --------------------------------------------
-            wait_all(&B->ready[p], (c >> 1) & 1);
+            wait_all(&B->ready[p], (nb >> 1) & 1);
             wait_all(&B->z, p);
             if (fail) break;
             const uint32_t colz = tl + L::COL_Z + 32 * hh, colu = tl + L::COL_U + 32 * hh, cold = tl + L::COL_UD + 32 * hh;
@@ -615,7 +716,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             signal(&B->rh);
             store_low(colz + 16, y, h);
             signal(&B->rl);
-            if (c > 0) outputs(c - 1, last.s, 1);   // while U is computed
+            if (nb > 0) outputs(nb - 1, last.s, 1);   // while U is computed
             // ---- U' = U D_63 for the state, then U for the outputs ------------------------
             wait_all(&B->u, p);
             if (fail) break;
@@ -653,16 +754,20 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             last = at;
             at.next();
         }
-        if (!fail) {
+        if (fail) break;
+        trade();
 #pragma unroll
-            for (int i = 0; i < XH; i += 4)
-                *reinterpret_cast<float4*>(sp + i) = make_float4(X[i], X[i + 1], X[i + 2], X[i + 3]);
-            outputs(w.blocks - 1, last.s, 0);
-            outputs(w.blocks - 1, last.s, 1);
+        for (int i = 0; i < XH / 4; ++i)
+            __stcs(reinterpret_cast<float4*>(sp + (i % 8) * DK + 32 * (i / 8)),
+                   make_float4(X[4 * i], X[4 * i + 1], X[4 * i + 2], X[4 * i + 3]));
+        }
+        if (!fail && nb > 0) {
+            outputs(nb - 1, last.s, 0);
+            outputs(nb - 1, last.s, 1);
         }
         if (fail) status = kStatusMmaWait;
     } else if (warp < kConvWarps + kPrepWarps) {
-        if (!prep_warps<DK>(a, w, sm, sbase, B, tmem)) {
+        if (!prep_warps<DK>(a, sm, sbase, B, tmem)) {
             fail = true;
             status = kStatusMmaWait;
             *abort = 1;
@@ -693,14 +798,17 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 tc_fence_after();
             };
             Ring3 at;
-            for (int c = 0; c < w.blocks && !fail; ++c, at.next()) {
-                const uint32_t p = c & 1;
+            Work w;
+            int nb = 0;   // blocks of the CTA so far
+            for (int k = 0; !fail && next_item(B, k, w, fail); ++k)
+            for (int c = 0; c < w.blocks && !fail; ++c, ++nb, at.next()) {
+                const uint32_t p = nb & 1;
                 const uint64_t dK = dK0 + at.s * (L::KQ_BYTES / 16), dKm = dKm0 + at.s * (L::KQ_BYTES / 16);
                 const uint64_t dV = dV0 + at.s * (L::V_BYTES / 16);
                 const uint64_t dT = dT0 + p * (L::TP_BYTES / 16);
                 auto start_u = [&]() {   // U = V^T T'^T, both parts of T'; the parts of the U before are read by now
                     wait_w(&B->v_full[at.s], at.phase);
-                    if (c >= 1) wait_w(&B->o, p ^ 1);
+                    if (nb >= 1) wait_w(&B->o, p ^ 1);
                     if (!fail && el) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
@@ -710,10 +818,10 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     }
                 };
                 // before X is published if T' is there already
-                const bool u_early = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&B->ready[p]), (c >> 1) & 1));
+                const bool u_early = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&B->ready[p]), (nb >> 1) & 1));
                 if (u_early) start_u();
                 wait_w(&B->kq_full[at.s], at.phase);
-                if (c + 1 == w.blocks) wait_w(&B->ready[p], (c >> 1) & 1);   // K's rows past the end are zeroed
+                if (w.len - c * C < C) wait_w(&B->ready[p], (nb >> 1) & 1);   // K's rows past the end are zeroed
                 wait_w(&B->xh, p);
                 if (fail) break;
                 if (el) {
@@ -728,7 +836,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     mma_commit(&B->z);
                 }
                 if (!u_early) {
-                    wait_w(&B->ready[p], (c >> 1) & 1);
+                    wait_w(&B->ready[p], (nb >> 1) & 1);
                     start_u();
                 }
                 wait_w(&B->rh, p);
@@ -747,10 +855,10 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cu, colt(cz, kk) + 16, dT + kk * 2, ID_64, true);
                     mma_commit(&B->u);
                 }
-                if (c >= 1) {   // the outputs of the block before are read
+                if (nb >= 1) {   // the outputs of the block before are read
                     Ring3 before = at;
                     before.next();
-                    before.next();   // the stage of block c + 2, and of block c - 1 a round earlier
+                    before.next();   // the stage of block nb + 2, and of block nb - 1 a round earlier
                     wait_w(&B->ot_full[before.s], before.phase ^ 1);
                     if (fail) break;
                 }
@@ -783,11 +891,13 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                         mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk) + 16, dT + 1024 + kk * 2, ID_64, true);
                     }
                     mma_commit(&B->o);
-                    // only where somebody will wait: an arrival after the CTA has left would hit another's memory
-                    if (c + kTiles < w.blocks) mma_commit(&B->kq_free[at.s]);
-                    if (c + 2 < w.blocks) mma_commit(&B->tp_free[p]);
+                    mma_commit(&B->kq_free[at.s]);
+                    mma_commit(&B->tp_free[p]);
                 }
             }
+            // the last arrivals that nobody else waits for: after the CTA has left they would hit another's memory
+            for (int m = nb < kTiles ? 0 : nb - kTiles; m < nb && !fail; ++m) wait_w(&B->kq_free[m % kTiles], (m / kTiles) & 1);
+            for (int m = nb < 2 ? 0 : nb - 2; m < nb && !fail; ++m) wait_w(&B->tp_free[m & 1], (m >> 1) & 1);
             if (fail) {   // every MMA issued completes before the CTA leaves (bounded)
                 status = kStatusMmaWait;
                 if (el) {
@@ -799,27 +909,44 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         }
     } else if (warp == kConvWarps + kPrepWarps + 1) {
         // ======================= loads ===============================================
-        if (lane == 0) {
-            Ring3 at;
-            int c = 0;
-            for (; c < w.blocks; ++c, at.next()) {
-                const int s = at.s, row = w.rq.row0 + c * C;
-                if (c >= kTiles) wait(&B->kq_free[s], at.phase ^ 1);
-                if (fail) break;
-                uint8_t* kq = sm + L::KQ + s * L::KQ_BYTES;
-                mbar_arrive_expect_tx(&B->kq_full[s], L::KQ_BYTES);
+        Ring3 at;
+        Work w;
+        int nb = 0;
+        for (int k = 0; !fail && next_item(B, k, w, fail); ++k)
+            for (int c = 0; c < w.blocks && !fail; ++c, ++nb, at.next()) {
+                const int s = at.s, row = w.row0 + c * C;
+                if (lane == 0) {
+                    if (c + kTiles < w.blocks) {   // into L2, three blocks ahead
 #pragma unroll
-                for (int x = 0; x < KA; ++x) {
-                    tma_load_3d(&tmk, &B->kq_full[s], kq + x * 16384, x * 64, w.khead, row);
-                    tma_load_3d(&tmq, &B->kq_full[s], kq + x * 16384 + 8192, x * 64, w.khead, row);
+                        for (int x = 0; x < KA; ++x) {
+                            prefetch_3d(&tmk, x * 64, w.khead, row + kTiles * C);
+                            prefetch_3d(&tmq, x * 64, w.khead, row + kTiles * C);
+                        }
+#pragma unroll
+                        for (int x = 0; x < DV / 64; ++x) prefetch_3d(&tmv, x * 64, w.head, row + kTiles * C);
+                    }
+                    if (nb >= kTiles) wait(&B->kq_free[s], at.phase ^ 1);
+                    if (!fail) {
+                        uint8_t* kq = sm + L::KQ + s * L::KQ_BYTES;
+                        mbar_arrive_expect_tx(&B->kq_full[s], L::KQ_BYTES);
+#pragma unroll
+                        for (int x = 0; x < KA; ++x) {
+                            tma_load_3d(&tmk, &B->kq_full[s], kq + x * 16384, x * 64, w.khead, row);
+                            tma_load_3d(&tmq, &B->kq_full[s], kq + x * 16384 + 8192, x * 64, w.khead, row);
+                        }
+                    }
+                    if (nb >= kTiles) wait(&B->v_free[s], at.phase ^ 1);
+                    if (!fail) {
+                        uint8_t* v = sm + L::V + s * L::V_BYTES;
+                        mbar_arrive_expect_tx(&B->v_full[s], L::V_BYTES);
+#pragma unroll
+                        for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[s], v + x * 8192, x * 64, w.head, row);
+                        if (c + 1 == w.blocks) mbar_arrive(&B->want);
+                    }
                 }
-                if (c >= kTiles) wait(&B->v_free[s], at.phase ^ 1);
-                if (fail) break;
-                uint8_t* v = sm + L::V + s * L::V_BYTES;
-                mbar_arrive_expect_tx(&B->v_full[s], L::V_BYTES);
-#pragma unroll
-                for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[s], v + x * 8192, x * 64, w.head, row);
+                fail = __any_sync(0xffffffffu, fail);
             }
+        if (lane == 0) {
             // After a failure loads may be in flight: let them land (bounded; a
             // phase that no load began runs into the limit).
             if (fail || *abort) {
@@ -831,28 +958,84 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     }
             }
         }
-    } else {
+    } else if (warp == kConvWarps + kPrepWarps + 2) {
         // ======================= output copies =======================================
         Ring3 at;
-        __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(w.rq.row0) * a.Hv + w.head) * DV;
+        Work w;
         const size_t ostep = static_cast<size_t>(a.Hv) * DV;
-        for (int c = 0; c < w.blocks; ++c, at.next()) {
-            wait(&B->ot_full[at.s], at.phase);
-            fail = !__all_sync(0xffffffffu, !fail);
-            if (fail) break;
-            const uint32_t ot = sbase + L::V + at.s * L::V_BYTES;
-            const int n = min(C, w.rq.len - c * C);
-            const int ch = lane & 15;
+        for (int k = 0; !fail && next_item(B, k, w, fail); ++k) {
+            __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(w.row0) * a.Hv + w.head) * DV;
+            for (int c = 0; c < w.blocks; ++c, at.next()) {
+                wait(&B->ot_full[at.s], at.phase);
+                fail = !__all_sync(0xffffffffu, !fail);
+                if (fail) break;
+                const uint32_t ot = sbase + L::V + at.s * L::V_BYTES;
+                const int n = min(C, w.len - c * C);
+                const int ch = lane & 15;
 #pragma unroll 8
-            for (int t = lane >> 4; t < n; t += 2) {
-                const uint4 y = ld_shared_v4(ot + t * 256 + ((ch ^ ((t & 1) << 2)) << 4));
-                *reinterpret_cast<uint4*>(op + static_cast<size_t>(c * C + t) * ostep + ch * 8) = y;
+                for (int t = lane >> 4; t < n; t += 2) {
+                    const uint4 y = ld_shared_v4(ot + t * 256 + ((ch ^ ((t & 1) << 2)) << 4));
+                    *reinterpret_cast<uint4*>(op + static_cast<size_t>(c * C + t) * ostep + ch * 8) = y;
+                }
+                fence_proxy_async_smem();   // the tile's generic accesses come before the load that overwrites it
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->v_free[at.s]);
             }
-            fence_proxy_async_smem();   // the tile's generic accesses come before the load that overwrites it
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B->v_free[at.s]);
         }
         if (fail) status = kStatusMmaWait;
+    } else {
+        // ======================= work ================================================
+        int idx = blockIdx.x;
+        for (int k = 0;; ++k) {
+            Request rq;
+            const bool have = idx >= 0 && read_request(a, idx / a.Hv, rq);
+            const int i = k % kItems;
+            if (k >= kItems) wait(&B->item_free[i], ((k / kItems) & 1) ^ 1);
+            fail = __any_sync(0xffffffffu, fail);
+            if (fail) break;
+            Work w = {};
+            if (have) {
+                w.row0 = rq.row0;
+                w.len = rq.len;
+                w.slot = rq.slot;
+                w.fresh = rq.fresh;
+                w.head = idx % a.Hv;
+                w.khead = w.head / (a.Hv / a.Hk);
+                w.blocks = (rq.len + C - 1) / C;
+            }
+            if (lane == 0) {
+                B->item[i] = w;
+                mbar_arrive(&B->item_full[i]);
+            }
+            if (!have) break;
+            // what the item begins with, into L2
+            if (!w.fresh) {
+                const float* st = a.states + (static_cast<size_t>(w.slot) * a.Hv + w.head) * DV * DK;
+                for (int x = lane; x < DV * DK / 32; x += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(st + 32 * x));
+            }
+            if (lane < min(w.blocks, kTiles)) {
+                const int row = w.row0 + lane * C;
+#pragma unroll
+                for (int x = 0; x < KA; ++x) {
+                    prefetch_3d(&tmk, x * 64, w.khead, row);
+                    prefetch_3d(&tmq, x * 64, w.khead, row);
+                }
+#pragma unroll
+                for (int x = 0; x < DV / 64; ++x) prefetch_3d(&tmv, x * 64, w.head, row);
+            }
+            // more work only once this item's loads are under way: what waits here could run elsewhere
+            wait(&B->want, k & 1);
+            fail = __any_sync(0xffffffffu, fail);
+            if (fail) break;
+            if (lane == 0) steal_request(&B->answer, &B->stolen);
+            wait(&B->stolen, k & 1);
+            fail = __any_sync(0xffffffffu, fail);
+            if (fail) break;
+            idx = stolen_index(&B->answer);
+            fence_proxy_async_smem();   // this read comes before the next answer's write
+            __syncwarp();
+        }
+        if (fail) status = kStatusFlagWait;
     }
     if (fail) *abort = 1;
     if (status && lane == 0) atomicOr(a.status, status);
