@@ -134,11 +134,77 @@ struct Ring3 {
     }
 };
 
+// mbar_wait_or_abort with the loop out of line: the warps' code, dozens of waits
+// among it, has to stay in the instruction cache (148 KB with the loops inline
+// ran a third slower once every SM fetched it). One try waits for a while itself.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+    const uint32_t b = smem_u32(bar);
+    return mbar_try_wait(b, parity) || wait_on(b, parity, abort);
+}
+
+// 16 lanes x 64 (32) columns of tensor memory between a warp's registers, by quads: with g = lane / 4,
+// c = lane % 4, x[4 i], x[4 i + 1] are columns 8 i + 2 c, + 1 of lane g, x[4 i + 2], x[4 i + 3] of lane g + 8.
+template <int N>
+__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const float* x) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(x);
+    if constexpr (N == 32) {
+        asm volatile(
+            "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+            "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+            "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+            ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+              "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
+              "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]),
+              "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+            : "memory");
+    } else {
+        static_assert(N == 16, "64 or 32 columns");
+        asm volatile(
+            "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+            "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+            ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+              "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+            : "memory");
+    }
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float* x) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(x);
+    if constexpr (N == 32) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+            "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+            : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+              "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+              "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+              "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+              "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+            : "r"(taddr));
+    } else {
+        static_assert(N == 16, "64 or 32 columns");
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+              "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+              "=r"(u[14]), "=r"(u[15])
+            : "r"(taddr));
+    }
+}
+
 // The k-th item of this CTA, for a whole warp; false when there is none (blocks
 // 0) or after a failure.
 __device__ __forceinline__ bool next_item(Bars* B, int k, Work& w, bool& fail) {
     const int i = k % kItems;
-    const bool ok = mbar_wait_or_abort(&B->item_full[i], (k / kItems) & 1, &B->abort);
+    const bool ok = wait_bar(&B->item_full[i], (k / kItems) & 1, &B->abort);
     if (!__all_sync(0xffffffffu, ok)) {
         fail = true;
         return false;
@@ -175,6 +241,36 @@ __device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int x, int y
 }
 
 // ---------------------------------------------------------------- prep warps
+
+// Gate vectors of a block from the gates and betas of tokens 2 lane, 2 lane + 1: g, b, the product of
+// the gates up to a token, from behind it, and up to it inside its 16 and its 32 tokens.
+__device__ __noinline__ void write_gates(float* vec, float2 gn, float2 bn) {
+    const int lane = threadIdx.x & 31;
+    float pre = gn.x * gn.y, suf = pre, g16 = pre;   // up to / from this lane's pair
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, pre, o), z = __shfl_down_sync(0xffffffffu, suf, o);
+        const float x = __shfl_up_sync(0xffffffffu, g16, o);
+        if (lane >= o) pre *= y;
+        if (lane + o < 32) suf *= z;
+        if (o < 8 && (lane & 7) >= o) g16 *= x;
+    }
+    const float first = __shfl_sync(0xffffffffu, g16, (lane & 16) + 7);   // all of the 32's first 16
+    const float g32 = lane & 8 ? first * g16 : g16;
+    float b16 = __shfl_up_sync(0xffffffffu, g16, 1), b32 = __shfl_up_sync(0xffffffffu, g32, 1);
+    if ((lane & 7) == 0) b16 = 1.f;
+    if ((lane & 15) == 0) b32 = 1.f;
+    float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
+    if (lane == 0) before = 1.f;
+    if (lane == 31) after = 1.f;
+    float2* v = reinterpret_cast<float2*>(vec) + lane;
+    v[0] = gn;
+    v[C / 2] = bn;
+    v[2 * C / 2] = make_float2(before * gn.x, pre);
+    v[3 * C / 2] = make_float2(gn.y * after, after);
+    v[4 * C / 2] = make_float2(b16 * gn.x, g16);
+    v[5 * C / 2] = make_float2(b32 * gn.x, g32);
+}
 
 // A fragment of rows r0.., columns c0.. of an fp32 matrix in shared memory, in two bf16 parts.
 __device__ __forceinline__ void load_split(const float* m, int r0, int c0, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
@@ -249,41 +345,12 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             bn.y = __ldg(a.beta + i + a.Hv);
         }
     };
-    auto write_gates = [&](int s) {
-        float* vec = reinterpret_cast<float*>(sm + L::VEC) + s * kVec;
-        float pre = gn.x * gn.y, suf = pre;   // products up to / from this lane's pair
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, pre, o), z = __shfl_down_sync(0xffffffffu, suf, o);
-            if (lane >= o) pre *= y;
-            if (lane + o < 32) suf *= z;
-        }
-        float g16 = gn.x * gn.y;   // up to this pair's second token, from the start of its 16 (32) tokens
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, g16, o);
-            if ((lane & 7) >= o) g16 *= y;
-        }
-        const float first = __shfl_sync(0xffffffffu, g16, (lane & 16) + 7);   // all of the 32's first 16
-        const float g32 = lane & 8 ? first * g16 : g16;
-        float b16 = __shfl_up_sync(0xffffffffu, g16, 1), b32 = __shfl_up_sync(0xffffffffu, g32, 1);
-        if ((lane & 7) == 0) b16 = 1.f;
-        if ((lane & 15) == 0) b32 = 1.f;
-        reinterpret_cast<float2*>(vec + 4 * C)[lane] = make_float2(b16 * gn.x, g16);
-        reinterpret_cast<float2*>(vec + 5 * C)[lane] = make_float2(b32 * gn.x, g32);
-        float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
-        if (lane == 0) before = 1.f;
-        if (lane == 31) after = 1.f;
-        reinterpret_cast<float2*>(vec)[lane] = gn;
-        reinterpret_cast<float2*>(vec + C)[lane] = bn;
-        reinterpret_cast<float2*>(vec + 2 * C)[lane] = make_float2(before * gn.x, pre);
-        reinterpret_cast<float2*>(vec + 3 * C)[lane] = make_float2(gn.y * after, after);
-    };
+    auto vec_of = [&](int s) { return reinterpret_cast<float*>(sm + L::VEC) + s * kVec; };
     auto issue_products = [&](int s) {   // [K;Q] K^T of the block in stage s
         constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
         const uint64_t d0 = kmaj(sbase + L::KQ + s * L::KQ_BYTES);
         if (el) {
-#pragma unroll
+#pragma unroll 1
             for (int kk = 0; kk < DK / 16; ++kk) {
                 const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
                 mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
@@ -298,7 +365,7 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
     if (!next_item(B, 0, w, lost)) return !lost;
     if (pw == 3) {
         load_gates(w, 0);
-        write_gates(0);
+        write_gates(vec_of(0), gn, bn);
     }
     // T' and P above their diagonal blocks stay zero: the MMAs read whole tiles
     for (int i = ptid; i < 2 * static_cast<int>(L::TP_BYTES) / 16; i += kPrepThreads)
@@ -326,7 +393,7 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
         bool ok = !lost;
         const int n = w.len - c * C;
         if (n < C) {   // rows of the next request (or past the tensor): K and V zero, so that they leave the state alone
-            ok = ok && mbar_wait_or_abort(&B->kq_full[at.s], at.phase, abort) && mbar_wait_or_abort(&B->v_full[at.s], at.phase, abort);
+            ok = ok && wait_bar(&B->kq_full[at.s], at.phase, abort) && wait_bar(&B->v_full[at.s], at.phase, abort);
             if (ok) {
                 const uint32_t v = sbase + L::V + at.s * L::V_BYTES;
                 for (int i = ptid; i < (C - n) * 8; i += kPrepThreads) {
@@ -341,63 +408,52 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
         }
         if (issuer && !early) {
-            ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(&B->kq_full[at.s], at.phase, abort));
+            ok = __all_sync(0xffffffffu, ok && wait_bar(&B->kq_full[at.s], at.phase, abort));
             if (ok) issue_products(at.s);
         }
         early = false;
-        ok = ok && mbar_wait_or_abort(&B->g, nb & 1, abort);
-        if (ok && nb >= 2) ok = mbar_wait_or_abort(&B->tp_free[nb & 1], ((nb - 2) >> 1) & 1, abort);
+        ok = ok && wait_bar(&B->g, nb & 1, abort);
+        if (ok && nb >= 2) ok = wait_bar(&B->tp_free[nb & 1], ((nb - 2) >> 1) & 1, abort);
         tc_fence_after();
         ok = __all_sync(0xffffffffu, ok);
-        // ---- E and P by rows, 16 columns at a time; D is zero right of the diagonal -----------
+        // ---- E and P by rows, 16 columns at a time from the right. D at a group's right edge: zero in the
+        //      group of the diagonal and right of it, else the row's gates from the edge on -----------
         if (ok) {
             const bool isP = pw >= 2;
             const int hd = pw & 1;   // the half of the columns with this warp's diagonal
             const int t = 32 * hd + lane;
-            // x *= D over columns c0 .. c0 + 15 from the right, d being D right of them: a running product
-            // that starts on the diagonal (`diag`: lane of column c0's row, -1 without one) or at the column's edge
-            auto decay = [&](float (&x)[32], int c0, int xo, float d, int diag) {
-                float carry = c0 + 16 < C ? vec[c0 + 16] : 1.f;   // gate of the column to the right
+            const float g16 = vec[4 * C + t], g32 = vec[5 * C + t], mid = vec[4 * C + 31];
+#pragma unroll 1
+            for (int c16 = 2 * hd + 1; c16 >= 0; --c16) {
+                const int u = 2 * hd + 1 - c16;   // 0, 1: the half of the diagonal; 2, 3: columns 16..31, 0..15 of rows 32..
+                float d = u == 0 ? 0.f : u == 1 ? (lane >= 16 ? g16 : 0.f) : u == 2 ? g32 : g32 * mid;
+                const int diag = u < 2 ? lane - (16 - 16 * u) : -1;   // the column of the row's diagonal element
+                float x[16];
+                tmem_ld16(tlane + L::COL_G + 16 * c16, x);
+                tmem_ld_wait();
 #pragma unroll
                 for (int q4 = 3; q4 >= 0; --q4) {
-                    const float4 g4 = *reinterpret_cast<const float4*>(vec + c0 + 4 * q4);
-                    const float gr[4] = {g4.y, g4.z, g4.w, carry};
-                    carry = g4.x;
+                    const float4 g4 = *reinterpret_cast<const float4*>(vec + 16 * c16 + 4 * q4);
+                    const float gl[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
                     for (int i = 3; i >= 0; --i) {
                         const int j = 4 * q4 + i;
-                        if (j < 15) d *= gr[i];   // (column 15's is d itself: the caller's starts past its right edge)
-                        if (diag >= 0 && lane == diag + j) d = 1.f;
-                        x[xo + j] *= d;
-                        if (diag >= 0 && lane == diag + j && !isP) x[xo + j] = 0.f;
+                        if (j == diag) d = 1.f;
+                        x[j] *= (j == diag && !isP) ? 0.f : d;
+                        d *= gl[i];   // the gate of column j itself comes before the columns left of it
                     }
                 }
-            };
-            auto store = [&](const float (&x)[32], int h) {
                 if (isP) {
-                    chunk::store_row32_bf16(aP, t, 4 * h, x);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        st_shared_v4(aP + sw128_off(t, 2 * c16 + m), pack_bf16(x[8 * m], x[8 * m + 1]), pack_bf16(x[8 * m + 2], x[8 * m + 3]),
+                                     pack_bf16(x[8 * m + 4], x[8 * m + 5]), pack_bf16(x[8 * m + 6], x[8 * m + 7]));
                 } else {
 #pragma unroll
-                    for (int q4 = 0; q4 < 8; ++q4)
-                        *reinterpret_cast<float4*>(E + t * kAStride + 32 * h + 4 * q4) =
+                    for (int q4 = 0; q4 < 4; ++q4)
+                        *reinterpret_cast<float4*>(E + t * kAStride + 16 * c16 + 4 * q4) =
                             make_float4(x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]);
                 }
-            };
-            float x[32];
-            tmem_ld32(tlane + L::COL_G + 32 * hd, x);
-            const float g16 = vec[4 * C + t], g32 = vec[5 * C + t];
-            tmem_ld_wait();
-            // the diagonal's half: columns 16.. (rows 16.. of the half; zero for the others) and 0..15
-            // (rows 16..: all of the row's gates from 16 on, i.e. g16, are between)
-            decay(x, 32 * hd + 16, 16, 0.f, 16);
-            decay(x, 32 * hd, 0, lane >= 16 ? g16 : 0.f, 0);
-            store(x, hd);
-            if (hd) {   // rows 32..63: columns 16..31, then 0..15 with the gates of 16..31 besides
-                tmem_ld32(tlane + L::COL_G, x);
-                tmem_ld_wait();
-                decay(x, 16, 16, g32, -1);
-                decay(x, 0, 0, g32 * vec[4 * C + 31], -1);
-                store(x, 0);
             }
         }
         tc_fence_before();
@@ -453,15 +509,15 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
         } else if (pw == 3) {
             if (more) {
                 // the slot's vectors of block nb - 2 are read (its phase is the one before block nb + 1's)
-                if (nb + 1 < kTiles || __all_sync(0xffffffffu, mbar_wait_or_abort(&B->vec_free[nx.s], nx.phase ^ 1, abort)))
-                    write_gates(nx.s);
+                if (nb + 1 < kTiles || __all_sync(0xffffffffu, wait_bar(&B->vec_free[nx.s], nx.phase ^ 1, abort)))
+                    write_gates(vec_of(nx.s), gn, bn);
                 else
                     ok = false;
             }
         } else if (issuer && more && wn.len - cn * C >= C) {
             // the next block is whole: its products now (this one's are read). Its loads wait for the
             // chain alone, which has all it needs for the blocks before.
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&B->kq_full[nx.s], nx.phase, abort));
+            ok = __all_sync(0xffffffffu, wait_bar(&B->kq_full[nx.s], nx.phase, abort));
             tc_fence_after();
             if (ok) issue_products(nx.s);
             early = true;
@@ -472,7 +528,7 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             const int mi = pw >> 1, ni = pw & 1;
             float Mx[2][4] = {}, N[2][4] = {};
             uint32_t ah[4], al[4], th[4], tl[4];
-#pragma unroll
+#pragma unroll 1
             for (int kk = 0; kk < 2; ++kk) {
                 load_split(E, 32 + 16 * mi, 16 * kk, ah, al);
                 ldsm4t(th, aTH + sw128_off(16 * kk + fr, 2 * ni + fc));
@@ -490,7 +546,7 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
                     st_shared_b32(aM + 32 * kMStride + o, lo);
                 }
             named_sync(kBarPrep, kPrepThreads);
-#pragma unroll
+#pragma unroll 1
             for (int kk = 0; kk < 2; ++kk) {
                 ldsm4(ah, aTH + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
                 ldsm4(al, aTL + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
@@ -566,34 +622,17 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
 
     int status = 0;
     bool fail = false;
-    auto wait = [&](uint64_t* b, uint32_t parity) { fail = fail || !mbar_wait_or_abort(b, parity, abort); };
+    auto wait = [&](uint64_t* b, uint32_t parity) { fail = fail || !wait_bar(b, parity, abort); };
     if (warp < kConvWarps) {
         // ======================= converting warps ==================================
         const int r = 32 * (warp & 3) + lane, hh = warp >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t colx = tl + L::COL_X + hh * XH;
         float X[XH];
-        // The state in global memory, 8 lanes to 128 contiguous bytes of a row: this lane reads and writes
-        // chunk (lane & 7) of 32 floats' 16-byte chunks of the rows of its group of 8 lanes, and trades with the
-        // group for its own row's (an 8x8 transpose of 16-byte chunks).
+        // The state in global memory: a warp moves its 32 rows by quads of lanes, 32 contiguous bytes of a row
+        // each (rows lane / 4 + 8 i), and turns them to a row a lane through the columns of dX.
         auto state_row = [&](const Work& w) {
-            return a.states + ((static_cast<size_t>(w.slot) * a.Hv + w.head) * DV + (r & ~7)) * DK + hh * XH + 4 * (lane & 7);
-        };
-        auto trade = [&]() {
-#pragma unroll
-            for (int q = 0; q < XH; q += 32)
-#pragma unroll
-                for (int b = 1; b < 8; b <<= 1)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (!(j & b)) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float &lo = X[q + 4 * j + e], &hi = X[q + 4 * (j | b) + e];
-                                const float y = __shfl_xor_sync(0xffffffffu, lane & b ? lo : hi, b);
-                                if (lane & b) lo = y; else hi = y;
-                            }
-                        }
+            return a.states + ((static_cast<size_t>(w.slot) * a.Hv + w.head) * DV + 32 * (warp & 3) + (lane >> 2)) * DK + hh * XH + 2 * (lane & 3);
         };
         auto signal = [&](uint64_t* b) {   // this warp's tensor-memory stores (and loads) are done
             tmem_st_wait();
@@ -630,7 +669,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         };
         // warp-uniform before the warp-collective tensor-memory accesses
         auto wait_all = [&](uint64_t* b, uint32_t parity) {
-            const bool ok = !fail && mbar_wait_or_abort(b, parity, abort);
+            const bool ok = !fail && wait_bar(b, parity, abort);
             fail = !__all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
@@ -673,27 +712,31 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         Work w;
         int nb = 0;   // blocks of the CTA so far
         for (int k = 0; !fail && next_item(B, k, w, fail); ++k) {
-        float* sp = state_row(w);
-        if (!w.fresh) {
-#pragma unroll
-            for (int i = 0; i < XH / 4; ++i) {
-                const float4 y = __ldcs(reinterpret_cast<const float4*>(sp + (i % 8) * DK + 32 * (i / 8)));
-                X[4 * i] = y.x;
-                X[4 * i + 1] = y.y;
-                X[4 * i + 2] = y.z;
-                X[4 * i + 3] = y.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < XH; ++i) X[i] = 0.f;
-        }
-        if (nb > 0) outputs(nb - 1, last.s, 0);   // while the state arrives
-        if (!w.fresh) trade();
-        publish_x();
         for (int c = 0; c < w.blocks && !fail; ++c, ++nb) {
             const int s = at.s;
             const uint32_t p = nb & 1;
-            if (c > 0) outputs(nb - 1, last.s, 0);   // while Z is computed
+            if (c == 0) {
+                const float* sp = state_row(w);
+#pragma unroll
+                for (int i = 0; i < XH; i += 2) {   // 16 rows at a time: x[(column / 8) * 4 + ..]: rows lane / 4, then + 8
+                    const int h16 = i / (XH / 2), e = i % (XH / 2);
+                    float2 u = make_float2(0.f, 0.f);
+                    if (!w.fresh) u = __ldcs(reinterpret_cast<const float2*>(sp + (16 * h16 + 8 * ((e / 2) & 1)) * DK + 8 * (e / 4)));
+                    X[i] = u.x;
+                    X[i + 1] = u.y;
+                }
+            }
+            if (nb > 0) outputs(nb - 1, last.s, 0);   // while Z is computed, or the state arrives
+            if (c == 0) {
+                tmem_st_rows<XH / 2>(colx, X);
+                tmem_st_rows<XH / 2>(colx + (16u << 16), X + XH / 2);
+                tmem_st_wait();
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < XH / 32; ++q) tmem_ld32(colx + 32 * q, reinterpret_cast<float(&)[32]>(X[32 * q]));
+                tmem_ld_wait();
+                publish_x();
+            }
             const float* vec = reinterpret_cast<const float*>(sm + L::VEC) + s * kVec;
             float y[32];
             uint32_t h[16];
@@ -755,11 +798,19 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             at.next();
         }
         if (fail) break;
-        trade();
 #pragma unroll
-        for (int i = 0; i < XH / 4; ++i)
-            __stcs(reinterpret_cast<float4*>(sp + (i % 8) * DK + 32 * (i / 8)),
-                   make_float4(X[4 * i], X[4 * i + 1], X[4 * i + 2], X[4 * i + 3]));
+        for (int q = 0; q < XH / 32; ++q) tmem_st32(colx + 32 * q, reinterpret_cast<const uint32_t(&)[32]>(X[32 * q]));
+        tmem_st_wait();
+        __syncwarp();
+        tmem_ld_rows<XH / 2>(colx, X);
+        tmem_ld_rows<XH / 2>(colx + (16u << 16), X + XH / 2);
+        tmem_ld_wait();
+        float* sp = state_row(w);
+#pragma unroll
+        for (int i = 0; i < XH; i += 2) {
+            const int h16 = i / (XH / 2), e = i % (XH / 2);
+            __stcs(reinterpret_cast<float2*>(sp + (16 * h16 + 8 * ((e / 2) & 1)) * DK + 8 * (e / 4)), make_float2(X[i], X[i + 1]));
+        }
         }
         if (!fail && nb > 0) {
             outputs(nb - 1, last.s, 0);
@@ -793,7 +844,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             const uint64_t dT0 = kmaj(sbase + L::TP);
             const uint32_t cz = tmem + L::COL_Z, cu = tmem + L::COL_U, cd = tmem + L::COL_UD;
             auto wait_w = [&](uint64_t* b, uint32_t parity) {   // the whole warp goes on, or gives up, together
-                const bool ok = !fail && mbar_wait_or_abort(b, parity, abort);
+                const bool ok = !fail && wait_bar(b, parity, abort);
                 fail = !__all_sync(0xffffffffu, ok);
                 tc_fence_after();
             };
@@ -810,7 +861,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     wait_w(&B->v_full[at.s], at.phase);
                     if (nb >= 1) wait_w(&B->o, p ^ 1);
                     if (!fail && el) {
-#pragma unroll
+#pragma unroll 1
                         for (int kk = 0; kk < 4; ++kk) {
                             mma_bf16_ss(cu, dV + kk * 128, dT + kk * 2, ID_V, kk > 0);
                             mma_bf16_ss(cu, dV + kk * 128, dT + 512 + kk * 2, ID_V, true);
@@ -825,13 +876,13 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 wait_w(&B->xh, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk), dK + kstep(kk), ID_64, kk > 0);
                 }
                 wait_w(&B->xl, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk) + XH / 2, dK + kstep(kk), ID_64, true);
                     mma_commit(&B->z);
                 }
@@ -842,7 +893,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 wait_w(&B->rh, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < 4; ++kk) {
                         mma_bf16_ts(cu, colt(cz, kk), dT + kk * 2, ID_64, true);
                         mma_bf16_ts(cu, colt(cz, kk), dT + 512 + kk * 2, ID_64, true);
@@ -851,7 +902,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 wait_w(&B->rl, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cu, colt(cz, kk) + 16, dT + kk * 2, ID_64, true);
                     mma_commit(&B->u);
                 }
@@ -863,7 +914,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     if (fail) break;
                 }
                 if (el) {
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < DK / 16; ++kk)
                         mma_bf16_ts(tmem + L::COL_O1, colx(kk), dK + 512 + kstep(kk), ID_64, kk > 0);
                     mma_commit(&B->o1);
@@ -872,20 +923,20 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 wait_w(&B->o1, p);   // X is read: dX may take its columns
                 if (fail) break;
                 if (el) {
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk), dKm + kk * 128, ID_K, kk > 0);
                 }
                 wait_w(&B->dl, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk) + 16, dKm + kk * 128, ID_K, true);
                     mma_commit(&B->dx);
                 }
                 wait_w(&B->uo, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < 4; ++kk) {
                         mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk), dT + 1024 + kk * 2, ID_64, kk > 0);
                         mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk) + 16, dT + 1024 + kk * 2, ID_64, true);
