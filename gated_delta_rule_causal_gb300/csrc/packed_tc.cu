@@ -10,22 +10,23 @@
 // requests first: the grid has one CTA for each, and a running one takes over
 // the next that has not been started (cluster launch control), so that its
 // prep and load warps are already at the next request while the chain finishes
-// one. The state's 128 rows lie on the 128 tensor-memory lanes, so that every product of the chain is an M = 128
-// MMA with its A operand (X, R = -G Z, U: bf16 parts) in tensor memory and its
-// B operand (K, Q, T', P) in shared memory:
-//   Z = X K^T, O1 = X Q^T  [dv][token],  U = V^T T'^T + R T'^T,
-//   dX = U' K,  O2 = U P^T
-// Eight warps convert between them: thread (row r, half hh) holds half of row
-// r of X in fp32 registers and takes half the columns of each product. Four
-// prep warps compute T' and P of the next block meanwhile; of the others one
-// issues the chain's MMAs, one the loads, one copies the outputs out, and one
-// fetches the work.
+// one. The state's 128 rows lie on the 128 tensor-memory lanes, fp32, for the
+// whole request, so that every product of the chain is an M = 128 MMA with its
+// A operand (X, R = -G Z, U: bf16 parts) in tensor memory too and its B operand
+// (K, Q, T', P) in shared memory:
+//   Z = X K^T, O = X Q^T  [dv][token],  U = V^T T'^T + R T'^T,
+//   X += U' K,  O += U P^T
+// Sixteen warps convert between them: thread (row r, part cp) takes a quarter
+// of the columns of each product in row r. Two groups of four prep warps
+// compute T' and P of the blocks that follow; of the others one issues the
+// chain's MMAs, one the loads, one copies the outputs out, and one fetches the
+// work.
 //
-// The chain's steps depend on one another, so what bounds a long request is
-// their latency: three products (Z, R T'^T, dX) with a conversion after each.
-// High parts are published first, so that a product starts while the low ones
-// are still formed. V^T T'^T, Q X^T and the outputs run in the gaps: the
-// outputs of a block are read while the next one's Z and U run.
+// The chain's steps depend on one another, so what bounds a request is their
+// latency: three products (Z, R T'^T, U' K) with a conversion after each. High
+// parts are published first, so that a product starts while the low ones are
+// still formed. V^T T'^T, Q X^T, the scaling of X by G_63 and of O by G, and the
+// outputs run in the gaps.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -48,11 +49,12 @@ using chunk::st_shared_v4;
 
 constexpr int C = 64;                 // tokens per block
 constexpr int DV = 128;
-constexpr int kConvWarps = 8, kPrepWarps = 4;
-constexpr int kThreads = 32 * (kConvWarps + kPrepWarps + 4);   // + MMA issue, loads, output copies, work
+constexpr int kConvWarps = 16, kPrepWarps = 4, kGroups = 2;     // two groups of prep warps, every other block each
+constexpr int kThreads = 32 * (kConvWarps + kGroups * kPrepWarps + 4);   // + MMA issue, loads, output copies, work
 constexpr int kPrepThreads = 32 * kPrepWarps;
-constexpr uint32_t kBarPrep = 1;      // named barrier of the prep warps
-constexpr int kTiles = 3;             // ring of K, Q and V tiles
+constexpr int kOther = kConvWarps + kGroups * kPrepWarps;      // first of the four other warps
+constexpr uint32_t kBarPrep = 1;      // named barriers of the prep groups: 1, 2
+constexpr int kTiles = 3;             // ring of K and Q tiles (V's has two: its loads are awaited later)
 constexpr int kItems = 4;             // ring of work items (the loads run at most three blocks ahead)
 constexpr int kAStride = 68;          // floats per row of A
 constexpr int kMStride = 80;          // bytes per row of the 32x32 bf16 product between the two merges
@@ -65,24 +67,21 @@ struct TcLayout {
     static constexpr uint32_t KQ_BYTES = KA * 16384;
     static constexpr uint32_t V_BYTES = 16384;                  // two atoms [64 t][64]; later the output tile [64 t][128]
     static constexpr uint32_t KQ = 0;                           // [kTiles]
-    static constexpr uint32_t V = kTiles * KQ_BYTES;            // [kTiles]
-    static constexpr uint32_t TP = V + kTiles * V_BYTES;        // [2]: T high, T low, P, each [64 t][64 j]
+    static constexpr uint32_t V = kTiles * KQ_BYTES;            // [2]
+    static constexpr uint32_t TP = V + 2 * V_BYTES;        // [2]: T high, T low, P, each [64 t][64 j]
     static constexpr uint32_t TP_BYTES = 3 * 8192;
-    static constexpr uint32_t A = TP + 2 * TP_BYTES;            // fp32 [64][kAStride]
-    static constexpr uint32_t M = A + C * kAStride * 4;         // bf16 high, low [32][kMStride bytes]
-    static constexpr uint32_t VEC = M + 2 * 32 * kMStride;      // [kTiles][kVec] fp32
+    static constexpr uint32_t A = TP + 2 * TP_BYTES;            // per prep group: fp32 [64][kAStride]
+    static constexpr uint32_t M = A + kGroups * C * kAStride * 4;   // per prep group: bf16 high, low [32][kMStride bytes]
+    static constexpr uint32_t VEC = M + kGroups * 2 * 32 * kMStride;      // [kTiles][kVec] fp32
     static constexpr uint32_t BAR = VEC + kTiles * kVec * 4;
     static constexpr uint32_t BYTES = BAR + 1024;
-    // Tensor memory columns. X: per half hh of the channels DK/4 columns of
-    // high parts, then DK/4 of low ones; dX (fp32, DK columns) takes the same
-    // columns once Z and Q X^T are done, each half over its own.
-    static constexpr uint32_t COL_X = 0;
-    // Z; R over it, per half of the tokens 16 columns of high parts, then 16 of low ones
-    static constexpr uint32_t COL_Z = 128;
-    static constexpr uint32_t COL_U = 192;     // U; its parts over it, like R
-    static constexpr uint32_t COL_UD = 256;    // parts of U'
-    static constexpr uint32_t COL_O1 = 320;
-    static constexpr uint32_t COL_O2 = 384;
+    // Tensor memory columns. Operands in two bf16 parts lie by steps of 16 along their columns: 8 columns
+    // of high parts, then 8 of low ones.
+    static constexpr uint32_t COL_X = 0;       // X, fp32 [DK]
+    static constexpr uint32_t COL_XP = 128;    // parts of X; of U' once Z and Q X^T are done
+    static constexpr uint32_t COL_Z = 256;     // Z; parts of R over it
+    static constexpr uint32_t COL_U = 320;     // U; its parts over it
+    static constexpr uint32_t COL_O = 384;
     static constexpr uint32_t COL_G = 448;     // [K;Q] K^T
     static constexpr uint32_t TMEM_COLS = 512;
 };
@@ -95,16 +94,18 @@ struct __align__(16) Work {
 
 // Barriers, in shared memory.
 struct Bars {
-    uint64_t kq_full[kTiles], kq_free[kTiles];   // TMA; MMA: every product of the block is done
-    uint64_t v_full[kTiles], v_free[kTiles];     // TMA; copier: the output tile over V has left
-    uint64_t vec_free[kTiles];                   // converters: the block's vectors are read (8)
-    uint64_t ot_full[kTiles];                    // converters: the output tile is written (8)
+    // (six of those that a prep group waits for, block nb's at nb % 6: with three it would see every other
+    // turn of a barrier, always of the same parity, and take the turn before for its own)
+    uint64_t kq_full[6], kq_free[kTiles];        // TMA; MMA: every product of the block is done
+    uint64_t v_full[2], v_free[2];               // TMA; copier: the output tile over V has left
+    uint64_t vec_free[6];                        // converters: the block's vectors are read (16)
+    uint64_t ot_full[2];                         // converters: the output tile is written (16)
     uint64_t ready[2], tp_free[2];               // prep warps: T, P and vectors (4); MMA: T and P are read
-    uint64_t g;                                  // MMA: [K;Q] K^T
-    uint64_t xh, xl, rh, rl, dh, dl, uo;         // converters: parts of X, R, U' and both of U published (8 each)
+    uint64_t g[2], g_free;                       // MMA: [K;Q] K^T, per prep group; prep warps: it is read (4)
+    uint64_t xh, xl, rh, rl, dh, dl, uo;         // converters: parts of X, R, U' and both of U published (16 each)
     uint64_t z, u, o1, dx, o;                    // MMA: Z, U, Q X^T, dX, O done
-    uint64_t drain[2];                           // after a failure: MMAs of either issuer are done
-    uint64_t item_full[kItems], item_free[kItems];   // work warp; every other warp has read the item (15)
+    uint64_t drain[3];                           // after a failure: MMAs of either issuer are done
+    uint64_t item_full[kItems], item_free[kItems];   // work warp; every other warp has read the item (27)
     uint64_t want, stolen;                       // loads: all of the item is issued; the answer to a request for more work
     uint32_t tmem;
     int abort;
@@ -123,88 +124,54 @@ __device__ __forceinline__ bool elect_one() {
 
 static_assert(sizeof(Bars) <= 1024, "barrier space");
 
-struct Ring3 {
+// A block's place among N, stepped instead of divided, and the parity of its turn.
+template <int N>
+struct Ring {
     int s = 0;
     uint32_t phase = 0;
     __device__ __forceinline__ void next() {
-        if (++s == kTiles) {
+        if (++s == N) {
             s = 0;
             phase ^= 1;
         }
     }
 };
 
-// mbar_wait_or_abort with the loop out of line: the warps' code, dozens of waits
-// among it, has to stay in the instruction cache (148 KB with the loops inline
-// ran a third slower once every SM fetched it). One try waits for a while itself.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, const volatile int* abort) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) return false;
-    }
-    return true;
-}
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const volatile int* abort) {
-    const uint32_t b = smem_u32(bar);
-    return mbar_try_wait(b, parity) || wait_on(b, parity, abort);
-}
-
-// 16 lanes x 64 (32) columns of tensor memory between a warp's registers, by quads: with g = lane / 4,
+// 16 lanes x 2 N columns of tensor memory between a warp's registers, by quads: with g = lane / 4,
 // c = lane % 4, x[4 i], x[4 i + 1] are columns 8 i + 2 c, + 1 of lane g, x[4 i + 2], x[4 i + 3] of lane g + 8.
 template <int N>
 __device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const float* x) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(x);
-    if constexpr (N == 32) {
-        asm volatile(
-            "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
-            "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-            "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-            ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
-              "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
-              "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]),
-              "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
-            : "memory");
-    } else {
-        static_assert(N == 16, "64 or 32 columns");
-        asm volatile(
-            "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
-            "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-            ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
-              "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-            : "memory");
-    }
+    static_assert(N == 16 || N == 8, "32 or 16 columns");
+    if constexpr (N == 16)
+        asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                     ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]) : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float* x) {
     uint32_t* u = reinterpret_cast<uint32_t*>(x);
-    if constexpr (N == 32) {
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-            "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-            : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
-              "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
-              "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
-              "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
-              "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
-            : "r"(taddr));
-    } else {
-        static_assert(N == 16, "64 or 32 columns");
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
-              "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
-              "=r"(u[14]), "=r"(u[15])
-            : "r"(taddr));
-    }
+    static_assert(N == 16 || N == 8, "32 or 16 columns");
+    if constexpr (N == 16)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]) : "r"(taddr));
+    else
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]) : "r"(taddr));
+}
+// Each thread of the warp writes 8 consecutive columns of its lane.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&u)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
 }
 
 // The k-th item of this CTA, for a whole warp; false when there is none (blocks
 // 0) or after a failure.
 __device__ __forceinline__ bool next_item(Bars* B, int k, Work& w, bool& fail) {
     const int i = k % kItems;
-    const bool ok = wait_bar(&B->item_full[i], (k / kItems) & 1, &B->abort);
+    const bool ok = mbar_wait_or_abort(&B->item_full[i], (k / kItems) & 1, &B->abort);
     if (!__all_sync(0xffffffffu, ok)) {
         fail = true;
         return false;
@@ -308,28 +275,30 @@ __device__ __forceinline__ void store_negated(uint32_t aTH, uint32_t aTL, int r0
         }
 }
 
-// Four warps, block by block: [K;Q] K^T on the tensor cores; E_tj = D_tj
-// k_t.k_j (j < t; warps 0, 1) and P_tj = D_tj q_t.k_j (j <= t; warps 2, 3) row
-// by row (lane = tensor-memory lane = row; D_tj is a running product from the
-// diagonal leftwards); then T' (A = diag(b) E): 16x16 diagonal blocks by
-// forward substitution in fp32 (warps 0 and 1, a half-warp each), merged twice
-// by T'_21 = -T'_22 (E_21 T'_11) on warp-level MMAs with two bf16 parts.
-// Meanwhile warp 2 issues the next block's [K;Q] K^T and warp 3 computes its
-// gate vectors.
+// A group of four warps takes every other block: [K;Q] K^T on the tensor cores;
+// E_tj = D_tj k_t.k_j (j < t; warps 0, 1) and P_tj = D_tj q_t.k_j (j <= t;
+// warps 2, 3) row by row (lane = tensor-memory lane = row; D_tj is a running
+// product from the diagonal leftwards); then T' (A = diag(b) E): 16x16 diagonal
+// blocks by forward substitution in fp32 (warps 0 and 1, a half-warp each),
+// merged twice by T'_21 = -T'_22 (E_21 T'_11) on warp-level MMAs with two bf16
+// parts. Two groups because a block's steps wait for one another longer than
+// the chain takes for a block.
 template <int DK>
 __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint32_t sbase, Bars* B, uint32_t tmem) {
     using L = TcLayout<DK>;
-    const int lane = threadIdx.x & 31, pw = (threadIdx.x >> 5) - kConvWarps, ptid = threadIdx.x - 32 * kConvWarps;
+    const int lane = threadIdx.x & 31, group = ((threadIdx.x >> 5) - kConvWarps) / kPrepWarps;
+    const int pw = (threadIdx.x >> 5) & 3, ptid = threadIdx.x & (kPrepThreads - 1);
     const int gq = lane >> 2, cq = lane & 3;
     const int fr = (lane & 7) + ((lane >> 3) & 1) * 8, fc = lane >> 4;
     const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * pw) << 16);
-    const bool issuer = pw == 2;
+    const uint32_t bar = kBarPrep + group;
     const bool el = elect_one();
     volatile int* abort = &B->abort;
-    float* E = reinterpret_cast<float*>(sm + L::A);
-    const uint32_t aM = sbase + L::M;
+    float* E = reinterpret_cast<float*>(sm + L::A) + group * C * kAStride;
+    const uint32_t aM = sbase + L::M + group * 2 * 32 * kMStride;
+    const uint32_t aTH = sbase + L::TP + group * L::TP_BYTES, aTL = aTH + 8192, aP = aTH + 16384;
 
-    // gate vectors of block c from tokens 2 lane, 2 lane + 1 (past the end: gate 1, beta 0)
+    // gates and betas of tokens 2 lane, 2 lane + 1 of block c (past the end: gate 1, beta 0)
     float2 gn = make_float2(1.f, 1.f), bn = make_float2(0.f, 0.f);
     auto load_gates = [&](const Work& w, int c) {
         const int t = c * C + 2 * lane;
@@ -345,57 +314,43 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             bn.y = __ldg(a.beta + i + a.Hv);
         }
     };
-    auto vec_of = [&](int s) { return reinterpret_cast<float*>(sm + L::VEC) + s * kVec; };
-    auto issue_products = [&](int s) {   // [K;Q] K^T of the block in stage s
-        constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
-        const uint64_t d0 = kmaj(sbase + L::KQ + s * L::KQ_BYTES);
-        if (el) {
-#pragma unroll 1
-            for (int kk = 0; kk < DK / 16; ++kk) {
-                const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
-                mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
-            }
-            mma_commit(&B->g);
-        }
-        __syncwarp();
-    };
-    Work w, wn;       // of the current and the next block
-    int items = 1;
-    bool lost = false;
-    if (!next_item(B, 0, w, lost)) return !lost;
-    if (pw == 3) {
-        load_gates(w, 0);
-        write_gates(vec_of(0), gn, bn);
-    }
     // T' and P above their diagonal blocks stay zero: the MMAs read whole tiles
-    for (int i = ptid; i < 2 * static_cast<int>(L::TP_BYTES) / 16; i += kPrepThreads)
-        st_shared_v4(sbase + L::TP + i * 16, 0, 0, 0, 0);
-    named_sync(kBarPrep, kPrepThreads);
+    for (int i = ptid; i < static_cast<int>(L::TP_BYTES) / 16; i += kPrepThreads) st_shared_v4(aTH + i * 16, 0, 0, 0, 0);
+    named_sync(bar, kPrepThreads);
 
-    bool early = false;   // (issuer) this block's products were issued during the block before
-    Ring3 at;
-    // block c of the item, block nb of the CTA
-    for (int c = 0, nb = 0; w.blocks > 0; ++nb, at.next()) {
+    Work w = {};
+    int items = 0, c = -1;
+    bool lost = false;
+    auto step = [&]() {   // on to the next block; false when there is none
+        if (++c < w.blocks) return true;
+        c = 0;
+        return next_item(B, items++, w, lost);
+    };
+    Ring<kTiles> at;   // of block nb of the CTA
+    Ring<6> six;
+    int nb = 0;
+    bool more = step();
+    if (group == 1 && more) {
+        more = step();
+        at.next();
+        six.next();
+        ++nb;
+    }
+    if (more && pw == 3) load_gates(w, c);
+    while (more) {
         const uint32_t kq = sbase + L::KQ + at.s * L::KQ_BYTES;
-        const uint32_t aTH = sbase + L::TP + (nb & 1) * L::TP_BYTES, aTL = aTH + 8192, aP = aTH + 16384;
-        const float* vec = reinterpret_cast<const float*>(sm + L::VEC) + at.s * kVec;
-        Ring3 nx = at;
-        nx.next();
-        int cn = c + 1;
-        wn = w;
-        if (cn == w.blocks) {
-            cn = 0;
-            next_item(B, items++, wn, lost);   // (blocks 0: this block is the last)
-            if (lost) wn.blocks = 0;
+        float* vec = reinterpret_cast<float*>(sm + L::VEC) + at.s * kVec;
+        const int n = w.len - c * C;   // tokens of the block
+        bool ok = true;
+        if (pw == 3) {   // the slot's vectors of block nb - 3 are read
+            const int b3 = six.s < 3 ? six.s + 3 : six.s - 3;   // block nb - 3's place; its turn is the one before from 0 .. 2
+            ok = nb < kTiles || __all_sync(0xffffffffu, mbar_wait_or_abort(&B->vec_free[b3], six.phase ^ (six.s < 3 ? 1 : 0), abort));
+            if (ok) write_gates(vec, gn, bn);
         }
-        const bool more = wn.blocks > 0;
-        if (pw == 3 && more) load_gates(wn, cn);
-        bool ok = !lost;
-        const int n = w.len - c * C;
         if (n < C) {   // rows of the next request (or past the tensor): K and V zero, so that they leave the state alone
-            ok = ok && wait_bar(&B->kq_full[at.s], at.phase, abort) && wait_bar(&B->v_full[at.s], at.phase, abort);
+            ok = ok && mbar_wait_or_abort(&B->kq_full[six.s], six.phase, abort) && mbar_wait_or_abort(&B->v_full[group], (nb >> 1) & 1, abort);
             if (ok) {
-                const uint32_t v = sbase + L::V + at.s * L::V_BYTES;
+                const uint32_t v = sbase + L::V + group * L::V_BYTES;
                 for (int i = ptid; i < (C - n) * 8; i += kPrepThreads) {
                     const uint32_t o = sw128_off(n + i / 8, i % 8);
 #pragma unroll
@@ -405,15 +360,34 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
                 }
             }
             fence_proxy_async_smem();
-            if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
         }
-        if (issuer && !early) {
-            ok = __all_sync(0xffffffffu, ok && wait_bar(&B->kq_full[at.s], at.phase, abort));
-            if (ok) issue_products(at.s);
+        if (named_sync_or(bar, kPrepThreads, !ok)) return false;
+        if (pw == 2) {   // [K;Q] K^T, once the other group has read its own
+            ok = mbar_wait_or_abort(&B->kq_full[six.s], six.phase, abort) && (nb == 0 || mbar_wait_or_abort(&B->g_free, (nb - 1) & 1, abort));
+            tc_fence_after();
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && el) {
+                constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
+                const uint64_t d0 = kmaj(kq);
+#pragma unroll 1
+                for (int kk = 0; kk < DK / 16; ++kk) {
+                    const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
+                    mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
+                }
+                mma_commit(&B->g[group]);
+            }
+            __syncwarp();
         }
-        early = false;
-        ok = ok && wait_bar(&B->g, nb & 1, abort);
-        if (ok && nb >= 2) ok = wait_bar(&B->tp_free[nb & 1], ((nb - 2) >> 1) & 1, abort);
+        // The block after next, its gates loaded meanwhile. (Only within the request: the next one may wait for
+        // this one's loads, and those for this very block.)
+        const bool same = c + 2 < w.blocks;
+        if (same) {
+            c += 2;
+            if (pw == 3) load_gates(w, c);
+        }
+        ok = ok && mbar_wait_or_abort(&B->g[group], (nb >> 1) & 1, abort);
+        // P, and T' below, are written over those of block nb - 2
+        if (pw >= 2 && ok && nb >= 2) ok = mbar_wait_or_abort(&B->tp_free[group], ((nb - 2) >> 1) & 1, abort);
         tc_fence_after();
         ok = __all_sync(0xffffffffu, ok);
         // ---- E and P by rows, 16 columns at a time from the right. D at a group's right edge: zero in the
@@ -455,80 +429,66 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
                             make_float4(x[4 * q4], x[4 * q4 + 1], x[4 * q4 + 2], x[4 * q4 + 3]);
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B->g_free);
         }
-        tc_fence_before();
-        if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
-        if (pw < 2) {
-            // ---- diagonal blocks 2 pw and 2 pw + 1, lane = (block, column): x_i = b_i (1_ij - sum E_is x_s),
-            //      column by column of E, four at a time ----------------------------------------
+        if (pw < 2 && ok) {
+            // ---- diagonal blocks 2 pw and 2 pw + 1 (rows of this warp), lane = (block, column):
+            //      x_i = b_i (1_ij - sum E_is x_s), column by column of E, two at a time -------------
             const int blk = 2 * pw + (lane >> 4), col = lane & 15;
             const float* eb = E + 16 * blk * kAStride + 16 * blk;
             float x[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
 #pragma unroll
-            for (int s4 = 0; s4 < 16; s4 += 4) {
-                const float4 b4 = *reinterpret_cast<const float4*>(vec + C + 16 * blk + s4);
-                float4 e[16];
+            for (int s2 = 0; s2 < 16; s2 += 2) {
+                const float2 b2 = *reinterpret_cast<const float2*>(vec + C + 16 * blk + s2);
+                float2 e[16];
 #pragma unroll
-                for (int i = s4 + 1; i < 16; ++i) e[i] = *reinterpret_cast<const float4*>(eb + i * kAStride + s4);
-                x[s4] *= b4.x;
-                x[s4 + 1] = b4.y * (x[s4 + 1] - e[s4 + 1].x * x[s4]);
-                x[s4 + 2] = b4.z * (x[s4 + 2] - e[s4 + 2].x * x[s4] - e[s4 + 2].y * x[s4 + 1]);
-                x[s4 + 3] = b4.w * (x[s4 + 3] - e[s4 + 3].x * x[s4] - e[s4 + 3].y * x[s4 + 1] - e[s4 + 3].z * x[s4 + 2]);
+                for (int i = s2 + 1; i < 16; ++i) e[i] = *reinterpret_cast<const float2*>(eb + i * kAStride + s2);
+                x[s2] *= b2.x;
+                x[s2 + 1] = b2.y * (x[s2 + 1] - e[s2 + 1].x * x[s2]);
 #pragma unroll
-                for (int i = s4 + 4; i < 16; ++i)
-                    x[i] = x[i] - e[i].x * x[s4] - e[i].y * x[s4 + 1] - e[i].z * x[s4 + 2] - e[i].w * x[s4 + 3];
+                for (int i = s2 + 2; i < 16; ++i) x[i] = x[i] - e[i].x * x[s2] - e[i].y * x[s2 + 1];
             }
+            if (nb >= 2) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&B->tp_free[group], ((nb - 2) >> 1) & 1, abort));
+            if (ok) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t o = sw128_off(16 * blk + i, 2 * blk + (col >> 3)) + 2 * (col & 7);
-                const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
-                st_shared_u16(aTH + o, hi);
-                st_shared_u16(aTL + o, __float2bfloat16_rn(x[i] - __bfloat162float(hi)));
-            }
-            __syncwarp();
-            // ---- the 16x16 block below: -T'_22 (E_21 T'_11) ----------------------------------
-            const int rb = 32 * pw + 16, cb = 32 * pw;   // its first row and column
-            uint32_t ah[4], al[4], th[4], tl[4], mh[4], ml[4];
-            load_split(E, rb, cb, ah, al);
-            ldsm4t(th, aTH + sw128_off(cb + fr, cb / 8 + fc));
-            ldsm4t(tl, aTL + sw128_off(cb + fr, cb / 8 + fc));
-            float Mx[2][4] = {}, N[2][4] = {};
-            mma_split(Mx, ah, al, th, tl);
-            split_tiles(Mx[0], Mx[1], mh, ml);
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t o = sw128_off(16 * blk + i, 2 * blk + (col >> 3)) + 2 * (col & 7);
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
+                    st_shared_u16(aTH + o, hi);
+                    st_shared_u16(aTL + o, __float2bfloat16_rn(x[i] - __bfloat162float(hi)));
+                }
+                __syncwarp();
+                // ---- the 16x16 block below: -T'_22 (E_21 T'_11) ----------------------------------
+                const int rb = 32 * pw + 16, cb = 32 * pw;   // its first row and column
+                uint32_t ah[4], al[4], th[4], tl[4], mh[4], ml[4];
+                load_split(E, rb, cb, ah, al);
+                ldsm4t(th, aTH + sw128_off(cb + fr, cb / 8 + fc));
+                ldsm4t(tl, aTL + sw128_off(cb + fr, cb / 8 + fc));
+                float Mx[2][4] = {}, N[2][4] = {};
+                mma_split(Mx, ah, al, th, tl);
+                split_tiles(Mx[0], Mx[1], mh, ml);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mh[i] = transpose8x8(mh[i]);
-                ml[i] = transpose8x8(ml[i]);
+                for (int i = 0; i < 4; ++i) {
+                    mh[i] = transpose8x8(mh[i]);
+                    ml[i] = transpose8x8(ml[i]);
+                }
+                ldsm4(th, aTH + sw128_off(rb + fr, rb / 8 + fc));
+                ldsm4(tl, aTL + sw128_off(rb + fr, rb / 8 + fc));
+                mma_split(N, th, tl, mh, ml);
+                store_negated(aTH, aTL, rb, cb, N);
             }
-            ldsm4(th, aTH + sw128_off(rb + fr, rb / 8 + fc));
-            ldsm4(tl, aTL + sw128_off(rb + fr, rb / 8 + fc));
-            mma_split(N, th, tl, mh, ml);
-            store_negated(aTH, aTL, rb, cb, N);
-        } else if (pw == 3) {
-            if (more) {
-                // the slot's vectors of block nb - 2 are read (its phase is the one before block nb + 1's)
-                if (nb + 1 < kTiles || __all_sync(0xffffffffu, wait_bar(&B->vec_free[nx.s], nx.phase ^ 1, abort)))
-                    write_gates(vec_of(nx.s), gn, bn);
-                else
-                    ok = false;
-            }
-        } else if (issuer && more && wn.len - cn * C >= C) {
-            // the next block is whole: its products now (this one's are read). Its loads wait for the
-            // chain alone, which has all it needs for the blocks before.
-            ok = __all_sync(0xffffffffu, wait_bar(&B->kq_full[nx.s], nx.phase, abort));
-            tc_fence_after();
-            if (ok) issue_products(nx.s);
-            early = true;
         }
-        if (named_sync_or(kBarPrep, kPrepThreads, !ok)) return false;
+        if (named_sync_or(bar, kPrepThreads, !ok)) return false;
         // ---- rows 32..63, columns 0..31: -T'_B (E_BA T'_A), a 16x16 tile per warp -----------
         {
             const int mi = pw >> 1, ni = pw & 1;
             float Mx[2][4] = {}, N[2][4] = {};
             uint32_t ah[4], al[4], th[4], tl[4];
-#pragma unroll 1
+#pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 load_split(E, 32 + 16 * mi, 16 * kk, ah, al);
                 ldsm4t(th, aTH + sw128_off(16 * kk + fr, 2 * ni + fc));
@@ -545,8 +505,8 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
                     st_shared_b32(aM + o, hi);
                     st_shared_b32(aM + 32 * kMStride + o, lo);
                 }
-            named_sync(kBarPrep, kPrepThreads);
-#pragma unroll 1
+            named_sync(bar, kPrepThreads);
+#pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 ldsm4(ah, aTH + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
                 ldsm4(al, aTL + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
@@ -558,11 +518,18 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B->ready[nb & 1]);
-        w = wn;
-        c = cn;
+        if (lane == 0) mbar_arrive(&B->ready[group]);
+        if (!same) {
+            more = step() && step();
+            if (more && pw == 3) load_gates(w, c);
+        }
+        nb += 2;
+        at.next();
+        at.next();
+        six.next();
+        six.next();
     }
-    return true;
+    return !lost;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -572,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
           const __grid_constant__ CUtensorMap tmv, const StepArgs a) {
     using L = TcLayout<DK>;
-    constexpr int KA = L::KA, XH = DK / 2;   // channels of X a converting thread holds
+    constexpr int KA = L::KA, XC = DK / 4;   // channels of X of a converting thread
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -583,18 +550,23 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
 
     if (tid == 0) {
         for (int i = 0; i < kTiles; ++i) {
-            mbar_init(&B->kq_full[i], 1);
             mbar_init(&B->kq_free[i], 1);
-            mbar_init(&B->v_full[i], 1);
-            mbar_init(&B->v_free[i], 1);
+        }
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&B->kq_full[i], 1);
             mbar_init(&B->vec_free[i], kConvWarps);
-            mbar_init(&B->ot_full[i], kConvWarps);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&B->g[i], 1);
+            mbar_init(&B->v_full[i], 1);
+            mbar_init(&B->v_free[i], 1);
+            mbar_init(&B->ot_full[i], kConvWarps);
             mbar_init(&B->ready[i], kPrepWarps);
             mbar_init(&B->tp_free[i], 1);
             mbar_init(&B->drain[i], 1);
         }
+        mbar_init(&B->drain[2], 1);
+        mbar_init(&B->g_free, kPrepWarps);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&B->item_full[i], 1);
             mbar_init(&B->item_free[i], kThreads / 32 - 1);
@@ -602,7 +574,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         mbar_init(&B->want, 1);
         mbar_init(&B->stolen, 1);
         for (uint64_t* b : {&B->xh, &B->xl, &B->rh, &B->rl, &B->dh, &B->dl, &B->uo}) mbar_init(b, kConvWarps);
-        for (uint64_t* b : {&B->g, &B->z, &B->u, &B->o1, &B->dx, &B->o}) mbar_init(b, 1);
+        for (uint64_t* b : {&B->z, &B->u, &B->o1, &B->dx, &B->o}) mbar_init(b, 1);
         B->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmq);
@@ -622,243 +594,219 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
 
     int status = 0;
     bool fail = false;
-    auto wait = [&](uint64_t* b, uint32_t parity) { fail = fail || !wait_bar(b, parity, abort); };
+    auto wait = [&](uint64_t* b, uint32_t parity) { fail = fail || !mbar_wait_or_abort(b, parity, abort); };
     if (warp < kConvWarps) {
         // ======================= converting warps ==================================
-        const int r = 32 * (warp & 3) + lane, hh = warp >> 2;
+        const int r = 32 * (warp & 3) + lane, cp = warp >> 2, t0 = 16 * cp;   // row; part: tokens t0 .., channels XC cp ..
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-        const uint32_t colx = tl + L::COL_X + hh * XH;
-        float X[XH];
-        // The state in global memory: a warp moves its 32 rows by quads of lanes, 32 contiguous bytes of a row
-        // each (rows lane / 4 + 8 i), and turns them to a row a lane through the columns of dX.
-        auto state_row = [&](const Work& w) {
-            return a.states + ((static_cast<size_t>(w.slot) * a.Hv + w.head) * DV + 32 * (warp & 3) + (lane >> 2)) * DK + hh * XH + 2 * (lane & 3);
-        };
+        const uint32_t colx = tl + L::COL_X + cp * XC, colxp = tl + L::COL_XP + cp * XC;
+        const uint32_t colz = tl + L::COL_Z + t0, colu = tl + L::COL_U + t0, colo = tl + L::COL_O + t0, cold = tl + L::COL_XP + t0;
         auto signal = [&](uint64_t* b) {   // this warp's tensor-memory stores (and loads) are done
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(b);
         };
-        // 32 values: their high parts to 16 columns, kept in h for the low ones' turn
-        auto pack_high = [&](const float* x, uint32_t (&h)[16]) {
+        // 16 values: their high parts to 8 columns, kept in h for the low ones' turn
+        auto store_high = [&](uint32_t col, const float* x, uint32_t (&h)[8]) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) h[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+            for (int i = 0; i < 8; ++i) h[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+            tmem_st8(col, h);
         };
-        auto store_high = [&](uint32_t col, const float* x, uint32_t (&h)[16]) {
-            pack_high(x, h);
-            tmem_st16(col, h);
-        };
-        auto store_low = [&](uint32_t col, const float* x, const uint32_t (&h)[16]) {
-            uint32_t l[16];
+        auto store_low = [&](uint32_t col, const float* x, const uint32_t (&h)[8]) {
+            uint32_t l[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) l[i] = low_parts(x[2 * i], x[2 * i + 1], h[i]);
-            tmem_st16(col, l);
+            for (int i = 0; i < 8; ++i) l[i] = low_parts(x[2 * i], x[2 * i + 1], h[i]);
+            tmem_st8(col, l);
+        };
+        auto load_x = [&](float (&x)[XC]) {
+            if constexpr (XC == 32) tmem_ld32(colx, x);
+            else tmem_ld16(colx, x);
+            tmem_ld_wait();
         };
         auto publish_x = [&]() {
-            uint32_t h[16];
+            float x[XC];
+            uint32_t h[XC / 16][8];
+            load_x(x);
 #pragma unroll
-            for (int p = 0; p < XH / 32; ++p) store_high(colx + 16 * p, X + 32 * p, h);
+            for (int p = 0; p < XC / 16; ++p) store_high(colxp + 16 * p, x + 16 * p, h[p]);
             signal(&B->xh);
 #pragma unroll
-            for (int p = 0; p < XH / 32; ++p) {   // (the high parts again: fewer registers than keeping them)
-                if (XH > 32) pack_high(X + 32 * p, h);
-                store_low(colx + XH / 2 + 16 * p, X + 32 * p, h);
-            }
+            for (int p = 0; p < XC / 16; ++p) store_low(colxp + 16 * p + 8, x + 16 * p, h[p]);
             signal(&B->xl);
         };
         // warp-uniform before the warp-collective tensor-memory accesses
         auto wait_all = [&](uint64_t* b, uint32_t parity) {
-            const bool ok = !fail && wait_bar(b, parity, abort);
+            const bool ok = !fail && mbar_wait_or_abort(b, parity, abort);
             fail = !__all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
-        Ring3 at, last;
-        // outputs of block nb, o = G O1 + O2, 16 tokens a half (q) at a time, through the tile over its V,
-        // [64 t][128], 16-byte chunks of odd tokens shifted by half a bank row
-        auto outputs = [&](int nb, int s, int q) {
-            if (q == 0) wait_all(&B->o, nb & 1);
+        Ring<kTiles> at;
+        Ring<6> six;
+        // outputs of block nb through the tile over its V, [64 t][128], 16-byte chunks of odd tokens
+        // shifted by half a bank row
+        auto outputs = [&](int nb) {
+            wait_all(&B->o, nb & 1);
             if (fail) return;
             const bool odd = lane & 1;
-            const int ch = (r & ~1) / 8, t0 = 32 * hh + 16 * q;
-            const uint32_t ot = sbase + L::V + s * L::V_BYTES + (r & 6) * 2 + (t0 + (odd ? 1 : 0)) * 256 + ((ch ^ (odd ? 4 : 0)) << 4);
-            const float* G = reinterpret_cast<const float*>(sm + L::VEC) + s * kVec + 2 * C + t0;
-            float o[16], o2[16];
-            tmem_ld16(tl + L::COL_O1 + t0, o);
-            tmem_ld16(tl + L::COL_O2 + t0, o2);
+            const int ch = (r & ~1) / 8;
+            const uint32_t ot = sbase + L::V + (nb & 1) * L::V_BYTES + (r & 6) * 2 + (t0 + (odd ? 1 : 0)) * 256 + ((ch ^ (odd ? 4 : 0)) << 4);
+            float o[16];
+            tmem_ld16(colo, o);
             tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(G + i);
-                o[i] = g4.x * o[i] + o2[i];
-                o[i + 1] = g4.y * o[i + 1] + o2[i + 1];
-                o[i + 2] = g4.z * o[i + 2] + o2[i + 2];
-                o[i + 3] = g4.w * o[i + 3] + o2[i + 3];
-            }
 #pragma unroll
             for (int m = 0; m < 8; ++m) {   // lane pairs trade values: two adjacent rows of one token per lane
                 const float send = odd ? o[2 * m] : o[2 * m + 1], keep = odd ? o[2 * m + 1] : o[2 * m];
                 const float recv = __shfl_xor_sync(0xffffffffu, send, 1);
                 st_shared_b32(ot + 512 * m, odd ? pack_bf16(recv, keep) : pack_bf16(keep, recv));
             }
-            if (q == 0) return;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&B->ot_full[s]);
-                mbar_arrive(&B->vec_free[s]);
-            }
+            if (lane == 0) mbar_arrive(&B->ot_full[nb & 1]);
+        };
+        // The state in global memory: a warp moves its 32 rows by quads of lanes, 32 contiguous bytes of a row
+        // each (rows lane / 4 + 8 i of its 32).
+        auto state_row = [&](const Work& w) {
+            return a.states + ((static_cast<size_t>(w.slot) * a.Hv + w.head) * DV + 32 * (warp & 3) + (lane >> 2)) * DK + cp * XC + 2 * (lane & 3);
         };
         Work w;
         int nb = 0;   // blocks of the CTA so far
         for (int k = 0; !fail && next_item(B, k, w, fail); ++k) {
-        for (int c = 0; c < w.blocks && !fail; ++c, ++nb) {
-            const int s = at.s;
-            const uint32_t p = nb & 1;
-            if (c == 0) {
+            {
+                float x[XC];
                 const float* sp = state_row(w);
 #pragma unroll
-                for (int i = 0; i < XH; i += 2) {   // 16 rows at a time: x[(column / 8) * 4 + ..]: rows lane / 4, then + 8
-                    const int h16 = i / (XH / 2), e = i % (XH / 2);
+                for (int i = 0; i < XC; i += 2) {   // 16 rows at a time: rows lane / 4, then + 8, of 8 columns
+                    const int h16 = i / (XC / 2), e = i % (XC / 2);
                     float2 u = make_float2(0.f, 0.f);
                     if (!w.fresh) u = __ldcs(reinterpret_cast<const float2*>(sp + (16 * h16 + 8 * ((e / 2) & 1)) * DK + 8 * (e / 4)));
-                    X[i] = u.x;
-                    X[i + 1] = u.y;
+                    x[i] = u.x;
+                    x[i + 1] = u.y;
                 }
-            }
-            if (nb > 0) outputs(nb - 1, last.s, 0);   // while Z is computed, or the state arrives
-            if (c == 0) {
-                tmem_st_rows<XH / 2>(colx, X);
-                tmem_st_rows<XH / 2>(colx + (16u << 16), X + XH / 2);
+                tmem_st_rows<XC / 2>(colx, x);
+                tmem_st_rows<XC / 2>(colx + (16u << 16), x + XC / 2);
                 tmem_st_wait();
                 __syncwarp();
-#pragma unroll
-                for (int q = 0; q < XH / 32; ++q) tmem_ld32(colx + 32 * q, reinterpret_cast<float(&)[32]>(X[32 * q]));
-                tmem_ld_wait();
+            }
+            for (int c = 0; c < w.blocks && !fail; ++c, ++nb) {
+                const uint32_t p = nb & 1;
+                const float* vec = reinterpret_cast<const float*>(sm + L::VEC) + at.s * kVec;
+                uint32_t h[8];
                 publish_x();
-            }
-            const float* vec = reinterpret_cast<const float*>(sm + L::VEC) + s * kVec;
-            float y[32];
-            uint32_t h[16];
-            // ---- R = -G Z, tokens 32 hh .. --------------------------------------------
-            wait_all(&B->ready[p], (nb >> 1) & 1);
-            wait_all(&B->z, p);
-            if (fail) break;
-            const uint32_t colz = tl + L::COL_Z + 32 * hh, colu = tl + L::COL_U + 32 * hh, cold = tl + L::COL_UD + 32 * hh;
-            tmem_ld32(colz, y);
-            tmem_ld_wait();
+                // ---- while Z is computed: the outputs of the block before; X scaled by G_63 --------------
+                if (nb > 0) outputs(nb - 1);
+                wait_all(&B->ready[p], (nb >> 1) & 1);
+                if (fail) break;
+                {
+                    float x[XC];
+                    const float gc = vec[2 * C + C - 1];
+                    load_x(x);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(vec + 2 * C + 32 * hh + i);
-                y[i] *= -g4.x;
-                y[i + 1] *= -g4.y;
-                y[i + 2] *= -g4.z;
-                y[i + 3] *= -g4.w;
-            }
-            store_high(colz, y, h);
-            signal(&B->rh);
-            store_low(colz + 16, y, h);
-            signal(&B->rl);
-            if (nb > 0) outputs(nb - 1, last.s, 1);   // while U is computed
-            // ---- U' = U D_63 for the state, then U for the outputs ------------------------
-            wait_all(&B->u, p);
-            if (fail) break;
-            tmem_ld32(colu, y);
-            tmem_ld_wait();
+                    for (int i = 0; i < XC; ++i) x[i] *= gc;
+                    if constexpr (XC == 32) tmem_st32(colx, reinterpret_cast<const uint32_t(&)[32]>(x));
+                    else tmem_st16(colx, reinterpret_cast<const uint32_t(&)[16]>(x));
+                }
+                // ---- R = -G Z, tokens t0 .. ----------------------------------------------------------
+                wait_all(&B->z, p);
+                if (fail) break;
+                float y[16], g[16];
+                tmem_ld16(colz, y);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 d4 = *reinterpret_cast<const float4*>(vec + 3 * C + 32 * hh + i);
-                y[i] *= d4.x;
-                y[i + 1] *= d4.y;
-                y[i + 2] *= d4.z;
-                y[i + 3] *= d4.w;
-            }
-            store_high(cold, y, h);
-            signal(&B->dh);
-            store_low(cold + 16, y, h);
-            signal(&B->dl);
-            tmem_ld32(colu, y);
-            tmem_ld_wait();
-            store_high(colu, y, h);
-            store_low(colu + 16, y, h);
-            signal(&B->uo);
-            // ---- X = G_63 X + dX ----------------------------------------------------------
-            const float gc = vec[2 * C + C - 1];
-            wait_all(&B->dx, p);
-            if (fail) break;
-#pragma unroll
-            for (int q = 0; q < XH / 32; ++q) {
-                tmem_ld32(colx + 32 * q, y);
+                for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(&g[i]) = *reinterpret_cast<const float4*>(vec + 2 * C + t0 + i);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) X[32 * q + i] = gc * X[32 * q + i] + y[i];
+                for (int i = 0; i < 16; ++i) y[i] *= -g[i];
+                store_high(colz, y, h);
+                signal(&B->rh);
+                store_low(colz + 8, y, h);
+                signal(&B->rl);
+                // ---- O = G (Q X^T), in place, while U is computed ---------------------------------------
+                wait_all(&B->o1, p);
+                if (fail) break;
+                tmem_ld16(colo, y);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] *= g[i];
+                tmem_st16(colo, reinterpret_cast<const uint32_t(&)[16]>(y));
+                // ---- U' = U D_63 for the state, then U for the outputs -----------------------------------
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(&g[i]) = *reinterpret_cast<const float4*>(vec + 3 * C + t0 + i);
+                wait_all(&B->u, p);
+                if (fail) break;
+                tmem_ld16(colu, y);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) g[i] *= y[i];
+                store_high(cold, g, h);
+                signal(&B->dh);
+                store_low(cold + 8, g, h);
+                signal(&B->dl);
+                store_high(colu, y, h);
+                store_low(colu + 8, y, h);
+                signal(&B->uo);
+                if (lane == 0) mbar_arrive(&B->vec_free[six.s]);
+                // ---- X is whole ----------------------------------------------------------------------------
+                wait_all(&B->dx, p);
+                at.next();
+                six.next();
             }
-            if (c + 1 < w.blocks) publish_x();
-            last = at;
-            at.next();
-        }
-        if (fail) break;
+            if (fail) break;
+            float x[XC];
+            tmem_ld_rows<XC / 2>(colx, x);
+            tmem_ld_rows<XC / 2>(colx + (16u << 16), x + XC / 2);
+            tmem_ld_wait();
+            float* sp = state_row(w);
 #pragma unroll
-        for (int q = 0; q < XH / 32; ++q) tmem_st32(colx + 32 * q, reinterpret_cast<const uint32_t(&)[32]>(X[32 * q]));
-        tmem_st_wait();
-        __syncwarp();
-        tmem_ld_rows<XH / 2>(colx, X);
-        tmem_ld_rows<XH / 2>(colx + (16u << 16), X + XH / 2);
-        tmem_ld_wait();
-        float* sp = state_row(w);
-#pragma unroll
-        for (int i = 0; i < XH; i += 2) {
-            const int h16 = i / (XH / 2), e = i % (XH / 2);
-            __stcs(reinterpret_cast<float2*>(sp + (16 * h16 + 8 * ((e / 2) & 1)) * DK + 8 * (e / 4)), make_float2(X[i], X[i + 1]));
+            for (int i = 0; i < XC; i += 2) {
+                const int h16 = i / (XC / 2), e = i % (XC / 2);
+                __stcs(reinterpret_cast<float2*>(sp + (16 * h16 + 8 * ((e / 2) & 1)) * DK + 8 * (e / 4)), make_float2(x[i], x[i + 1]));
+            }
+            __syncwarp();
         }
-        }
-        if (!fail && nb > 0) {
-            outputs(nb - 1, last.s, 0);
-            outputs(nb - 1, last.s, 1);
-        }
+        if (!fail && nb > 0) outputs(nb - 1);
         if (fail) status = kStatusMmaWait;
-    } else if (warp < kConvWarps + kPrepWarps) {
+    } else if (warp < kConvWarps + kGroups * kPrepWarps) {
         if (!prep_warps<DK>(a, sm, sbase, B, tmem)) {
             fail = true;
             status = kStatusMmaWait;
             *abort = 1;
-            if (warp == kConvWarps + 2 && elect_one()) {   // the lane that issued this role's MMAs
-                mma_commit(&B->drain[1]);
-                mbar_wait(&B->drain[1], 0, 100000000ull);
+            if ((warp & 3) == 2 && elect_one()) {   // the lane that issued this group's MMAs
+                uint64_t* d = &B->drain[1 + (warp - kConvWarps) / kPrepWarps];
+                mma_commit(d);
+                mbar_wait(d, 0, 100000000ull);
             }
             __syncwarp();
         }
-    } else if (warp == kConvWarps + kPrepWarps) {
+    } else if (warp == kOther) {
         // ======================= MMA issue ==========================================
         {
             const bool el = elect_one();
             constexpr uint32_t ID_64 = idesc_bf16(128, 64, false, false);
             constexpr uint32_t ID_V = idesc_bf16(128, 64, true, false);    // V^T T'^T
             constexpr uint32_t ID_K = idesc_bf16(128, DK, false, true);    // U' K
-            // the A operands of k-step kk: channels 16 kk .., tokens 16 kk ..
-            auto colx = [&](int kk) { return tmem + L::COL_X + (kk / (XH / 16)) * XH + (kk % (XH / 16)) * 8; };
-            auto colt = [](uint32_t col, int kk) { return col + (kk / 2) * 32 + (kk % 2) * 8; };
+            // the A operand of k-step kk: 16 kk columns on, 8 more for the low parts
             auto kstep = [](int kk) { return static_cast<uint64_t>((kk / 4) * 1024 + (kk % 4) * 2); };
             // operand descriptors of stage 0; offsets in 16-byte units are added to them
             const uint64_t dK0 = kmaj(sbase + L::KQ), dKm0 = mnmaj(sbase + L::KQ, 16384), dV0 = mnmaj(sbase + L::V, 8192);
             const uint64_t dT0 = kmaj(sbase + L::TP);
-            const uint32_t cz = tmem + L::COL_Z, cu = tmem + L::COL_U, cd = tmem + L::COL_UD;
+            const uint32_t cx = tmem + L::COL_X, cxp = tmem + L::COL_XP, cz = tmem + L::COL_Z, cu = tmem + L::COL_U, co = tmem + L::COL_O;
             auto wait_w = [&](uint64_t* b, uint32_t parity) {   // the whole warp goes on, or gives up, together
-                const bool ok = !fail && wait_bar(b, parity, abort);
+                const bool ok = !fail && mbar_wait_or_abort(b, parity, abort);
                 fail = !__all_sync(0xffffffffu, ok);
                 tc_fence_after();
             };
-            Ring3 at;
+            Ring<kTiles> at;
+            Ring<6> six;
             Work w;
             int nb = 0;   // blocks of the CTA so far
             for (int k = 0; !fail && next_item(B, k, w, fail); ++k)
-            for (int c = 0; c < w.blocks && !fail; ++c, ++nb, at.next()) {
+            for (int c = 0; c < w.blocks && !fail; ++c, ++nb, at.next(), six.next()) {
                 const uint32_t p = nb & 1;
                 const uint64_t dK = dK0 + at.s * (L::KQ_BYTES / 16), dKm = dKm0 + at.s * (L::KQ_BYTES / 16);
-                const uint64_t dV = dV0 + at.s * (L::V_BYTES / 16);
+                const uint64_t dV = dV0 + p * (L::V_BYTES / 16);
                 const uint64_t dT = dT0 + p * (L::TP_BYTES / 16);
                 auto start_u = [&]() {   // U = V^T T'^T, both parts of T'; the parts of the U before are read by now
-                    wait_w(&B->v_full[at.s], at.phase);
+                    wait_w(&B->v_full[p], (nb >> 1) & 1);
                     if (nb >= 1) wait_w(&B->o, p ^ 1);
                     if (!fail && el) {
 #pragma unroll 1
@@ -871,66 +819,59 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 // before X is published if T' is there already
                 const bool u_early = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&B->ready[p]), (nb >> 1) & 1));
                 if (u_early) start_u();
-                wait_w(&B->kq_full[at.s], at.phase);
+                wait_w(&B->kq_full[six.s], six.phase);
                 if (w.len - c * C < C) wait_w(&B->ready[p], (nb >> 1) & 1);   // K's rows past the end are zeroed
                 wait_w(&B->xh, p);
                 if (fail) break;
                 if (el) {
 #pragma unroll 1
-                    for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk), dK + kstep(kk), ID_64, kk > 0);
+                    for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, cxp + 16 * kk, dK + kstep(kk), ID_64, kk > 0);
                 }
                 wait_w(&B->xl, p);
                 if (fail) break;
                 if (el) {
 #pragma unroll 1
-                    for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, colx(kk) + XH / 2, dK + kstep(kk), ID_64, true);
+                    for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, cxp + 16 * kk + 8, dK + kstep(kk), ID_64, true);
                     mma_commit(&B->z);
                 }
                 if (!u_early) {
                     wait_w(&B->ready[p], (nb >> 1) & 1);
                     start_u();
                 }
+                if (nb >= 1) wait_w(&B->ot_full[p ^ 1], ((nb - 1) >> 1) & 1);   // the outputs of the block before are read
+                if (fail) break;
+                if (el) {
+#pragma unroll 1
+                    for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(co, cxp + 16 * kk, dK + 512 + kstep(kk), ID_64, kk > 0);
+                    mma_commit(&B->o1);
+                }
                 wait_w(&B->rh, p);
                 if (fail) break;
                 if (el) {
 #pragma unroll 1
                     for (int kk = 0; kk < 4; ++kk) {
-                        mma_bf16_ts(cu, colt(cz, kk), dT + kk * 2, ID_64, true);
-                        mma_bf16_ts(cu, colt(cz, kk), dT + 512 + kk * 2, ID_64, true);
+                        mma_bf16_ts(cu, cz + 16 * kk, dT + kk * 2, ID_64, true);
+                        mma_bf16_ts(cu, cz + 16 * kk, dT + 512 + kk * 2, ID_64, true);
                     }
                 }
                 wait_w(&B->rl, p);
                 if (fail) break;
                 if (el) {
 #pragma unroll 1
-                    for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cu, colt(cz, kk) + 16, dT + kk * 2, ID_64, true);
+                    for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cu, cz + 16 * kk + 8, dT + kk * 2, ID_64, true);
                     mma_commit(&B->u);
                 }
-                if (nb >= 1) {   // the outputs of the block before are read
-                    Ring3 before = at;
-                    before.next();
-                    before.next();   // the stage of block nb + 2, and of block nb - 1 a round earlier
-                    wait_w(&B->ot_full[before.s], before.phase ^ 1);
-                    if (fail) break;
-                }
-                if (el) {
-#pragma unroll 1
-                    for (int kk = 0; kk < DK / 16; ++kk)
-                        mma_bf16_ts(tmem + L::COL_O1, colx(kk), dK + 512 + kstep(kk), ID_64, kk > 0);
-                    mma_commit(&B->o1);
-                }
-                wait_w(&B->dh, p);
-                wait_w(&B->o1, p);   // X is read: dX may take its columns
+                wait_w(&B->dh, p);   // (after Q X^T was waited for: U' lies where the parts of X were)
                 if (fail) break;
                 if (el) {
 #pragma unroll 1
-                    for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk), dKm + kk * 128, ID_K, kk > 0);
+                    for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cx, cxp + 16 * kk, dKm + kk * 128, ID_K, true);
                 }
                 wait_w(&B->dl, p);
                 if (fail) break;
                 if (el) {
 #pragma unroll 1
-                    for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + L::COL_X, colt(cd, kk) + 16, dKm + kk * 128, ID_K, true);
+                    for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cx, cxp + 16 * kk + 8, dKm + kk * 128, ID_K, true);
                     mma_commit(&B->dx);
                 }
                 wait_w(&B->uo, p);
@@ -938,8 +879,8 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 if (el) {
 #pragma unroll 1
                     for (int kk = 0; kk < 4; ++kk) {
-                        mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk), dT + 1024 + kk * 2, ID_64, kk > 0);
-                        mma_bf16_ts(tmem + L::COL_O2, colt(cu, kk) + 16, dT + 1024 + kk * 2, ID_64, true);
+                        mma_bf16_ts(co, cu + 16 * kk, dT + 1024 + kk * 2, ID_64, true);
+                        mma_bf16_ts(co, cu + 16 * kk + 8, dT + 1024 + kk * 2, ID_64, true);
                     }
                     mma_commit(&B->o);
                     mma_commit(&B->kq_free[at.s]);
@@ -958,13 +899,14 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 __syncwarp();
             }
         }
-    } else if (warp == kConvWarps + kPrepWarps + 1) {
+    } else if (warp == kOther + 1) {
         // ======================= loads ===============================================
-        Ring3 at;
+        Ring<kTiles> at;
+        Ring<6> six;
         Work w;
         int nb = 0;
         for (int k = 0; !fail && next_item(B, k, w, fail); ++k)
-            for (int c = 0; c < w.blocks && !fail; ++c, ++nb, at.next()) {
+            for (int c = 0; c < w.blocks && !fail; ++c, ++nb, at.next(), six.next()) {
                 const int s = at.s, row = w.row0 + c * C;
                 if (lane == 0) {
                     if (c + kTiles < w.blocks) {   // into L2, three blocks ahead
@@ -979,19 +921,20 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     if (nb >= kTiles) wait(&B->kq_free[s], at.phase ^ 1);
                     if (!fail) {
                         uint8_t* kq = sm + L::KQ + s * L::KQ_BYTES;
-                        mbar_arrive_expect_tx(&B->kq_full[s], L::KQ_BYTES);
+                        mbar_arrive_expect_tx(&B->kq_full[six.s], L::KQ_BYTES);
 #pragma unroll
                         for (int x = 0; x < KA; ++x) {
-                            tma_load_3d(&tmk, &B->kq_full[s], kq + x * 16384, x * 64, w.khead, row);
-                            tma_load_3d(&tmq, &B->kq_full[s], kq + x * 16384 + 8192, x * 64, w.khead, row);
+                            tma_load_3d(&tmk, &B->kq_full[six.s], kq + x * 16384, x * 64, w.khead, row);
+                            tma_load_3d(&tmq, &B->kq_full[six.s], kq + x * 16384 + 8192, x * 64, w.khead, row);
                         }
                     }
-                    if (nb >= kTiles) wait(&B->v_free[s], at.phase ^ 1);
+                    const int vs = nb & 1;
+                    if (nb >= 2) wait(&B->v_free[vs], ((nb - 2) >> 1) & 1);
                     if (!fail) {
-                        uint8_t* v = sm + L::V + s * L::V_BYTES;
-                        mbar_arrive_expect_tx(&B->v_full[s], L::V_BYTES);
+                        uint8_t* v = sm + L::V + vs * L::V_BYTES;
+                        mbar_arrive_expect_tx(&B->v_full[vs], L::V_BYTES);
 #pragma unroll
-                        for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[s], v + x * 8192, x * 64, w.head, row);
+                        for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[vs], v + x * 8192, x * 64, w.head, row);
                         if (c + 1 == w.blocks) mbar_arrive(&B->want);
                     }
                 }
@@ -1002,35 +945,36 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             // phase that no load began runs into the limit).
             if (fail || *abort) {
                 status = kStatusTmaWait;
-                for (int i = 0; i < kTiles; ++i)
+                for (int i = 0; i < 6; ++i)
                     for (uint32_t ph = 0; ph < 2; ++ph) {
                         mbar_wait(&B->kq_full[i], ph, 10000000ull);
-                        mbar_wait(&B->v_full[i], ph, 10000000ull);
+                        if (i < 2) mbar_wait(&B->v_full[i], ph, 10000000ull);
                     }
             }
         }
-    } else if (warp == kConvWarps + kPrepWarps + 2) {
+    } else if (warp == kOther + 2) {
         // ======================= output copies =======================================
-        Ring3 at;
         Work w;
+        int nb = 0;
         const size_t ostep = static_cast<size_t>(a.Hv) * DV;
         for (int k = 0; !fail && next_item(B, k, w, fail); ++k) {
             __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(w.row0) * a.Hv + w.head) * DV;
-            for (int c = 0; c < w.blocks; ++c, at.next()) {
-                wait(&B->ot_full[at.s], at.phase);
+            for (int c = 0; c < w.blocks; ++c, ++nb) {
+                const int vs = nb & 1;
+                wait(&B->ot_full[vs], (nb >> 1) & 1);
                 fail = !__all_sync(0xffffffffu, !fail);
                 if (fail) break;
-                const uint32_t ot = sbase + L::V + at.s * L::V_BYTES;
+                const uint32_t ot = sbase + L::V + vs * L::V_BYTES;
                 const int n = min(C, w.len - c * C);
                 const int ch = lane & 15;
-#pragma unroll 8
+#pragma unroll 4
                 for (int t = lane >> 4; t < n; t += 2) {
                     const uint4 y = ld_shared_v4(ot + t * 256 + ((ch ^ ((t & 1) << 2)) << 4));
                     *reinterpret_cast<uint4*>(op + static_cast<size_t>(c * C + t) * ostep + ch * 8) = y;
                 }
                 fence_proxy_async_smem();   // the tile's generic accesses come before the load that overwrites it
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&B->v_free[at.s]);
+                if (lane == 0) mbar_arrive(&B->v_free[vs]);
             }
         }
         if (fail) status = kStatusMmaWait;
