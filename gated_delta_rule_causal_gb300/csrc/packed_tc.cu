@@ -19,8 +19,8 @@
 // Sixteen warps convert between them: thread (row r, part cp) takes a quarter
 // of the columns of each product in row r. Two groups of four prep warps
 // compute T' and P of the blocks that follow; of the others one issues the
-// chain's MMAs, one the loads, one copies the outputs out, and one fetches the
-// work.
+// chain's MMAs, one loads K and Q, one copies the outputs out, and one fetches
+// the work and loads V.
 //
 // The chain's steps depend on one another, so what bounds a request is their
 // latency: three products (Z, R T'^T, U' K) with a conversion after each. High
@@ -106,7 +106,7 @@ struct Bars {
     uint64_t z, u, o1, dx, o;                    // MMA: Z, U, Q X^T, dX, O done
     uint64_t drain[3];                           // after a failure: MMAs of either issuer are done
     uint64_t item_full[kItems], item_free[kItems];   // work warp; every other warp has read the item (27)
-    uint64_t want, stolen;                       // loads: all of the item is issued; the answer to a request for more work
+    uint64_t stolen;                             // the answer to a request for more work is here
     uint32_t tmem;
     int abort;
     uint4 answer;
@@ -167,12 +167,30 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&u)[8])
                  ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
 }
 
+// Bounded wait of a whole warp on phase `parity` of `bar`: the same answer in every
+// lane; false after a failure here or elsewhere (*abort). One try (which waits a while
+// itself) in line, the loop out of line: the warps' code, dozens of waits among it,
+// has to stay in the instruction cache.
+__device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    const uint64_t t0 = globaltimer_ns();
+    bool ok;
+    do {
+        ok = mbar_try_wait(bar, parity);
+    } while (!ok && !*abort && globaltimer_ns() - t0 <= kWaitLimitNs);
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+    if (!ok) ok = warp_wait_on(bar, parity, abort);
+    tc_fence_after();
+    return ok;
+}
+
 // The k-th item of this CTA, for a whole warp; false when there is none (blocks
 // 0) or after a failure.
 __device__ __forceinline__ bool next_item(Bars* B, int k, Work& w, bool& fail) {
     const int i = k % kItems;
-    const bool ok = mbar_wait_or_abort(&B->item_full[i], (k / kItems) & 1, &B->abort);
-    if (!__all_sync(0xffffffffu, ok)) {
+    if (!warp_wait(smem_u32(&B->item_full[i]), (k / kItems) & 1, &B->abort)) {
         fail = true;
         return false;
     }
@@ -294,6 +312,7 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
     const uint32_t bar = kBarPrep + group;
     const bool el = elect_one();
     volatile int* abort = &B->abort;
+    auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(smem_u32(b), parity, abort); };
     float* E = reinterpret_cast<float*>(sm + L::A) + group * C * kAStride;
     const uint32_t aM = sbase + L::M + group * 2 * 32 * kMStride;
     const uint32_t aTH = sbase + L::TP + group * L::TP_BYTES, aTL = aTH + 8192, aP = aTH + 16384;
@@ -344,11 +363,11 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
         bool ok = true;
         if (pw == 3) {   // the slot's vectors of block nb - 3 are read
             const int b3 = six.s < 3 ? six.s + 3 : six.s - 3;   // block nb - 3's place; its turn is the one before from 0 .. 2
-            ok = nb < kTiles || __all_sync(0xffffffffu, mbar_wait_or_abort(&B->vec_free[b3], six.phase ^ (six.s < 3 ? 1 : 0), abort));
+            ok = nb < kTiles || wait(&B->vec_free[b3], six.phase ^ (six.s < 3 ? 1 : 0));
             if (ok) write_gates(vec, gn, bn);
         }
         if (n < C) {   // rows of the next request (or past the tensor): K and V zero, so that they leave the state alone
-            ok = ok && mbar_wait_or_abort(&B->kq_full[six.s], six.phase, abort) && mbar_wait_or_abort(&B->v_full[group], (nb >> 1) & 1, abort);
+            ok = ok && wait(&B->kq_full[six.s], six.phase) && wait(&B->v_full[group], (nb >> 1) & 1);
             if (ok) {
                 const uint32_t v = sbase + L::V + group * L::V_BYTES;
                 for (int i = ptid; i < (C - n) * 8; i += kPrepThreads) {
@@ -363,9 +382,7 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
         }
         if (named_sync_or(bar, kPrepThreads, !ok)) return false;
         if (pw == 2) {   // [K;Q] K^T, once the other group has read its own
-            ok = mbar_wait_or_abort(&B->kq_full[six.s], six.phase, abort) && (nb == 0 || mbar_wait_or_abort(&B->g_free, (nb - 1) & 1, abort));
-            tc_fence_after();
-            ok = __all_sync(0xffffffffu, ok);
+            ok = wait(&B->kq_full[six.s], six.phase) && (nb == 0 || wait(&B->g_free, (nb - 1) & 1));
             if (ok && el) {
                 constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
                 const uint64_t d0 = kmaj(kq);
@@ -385,11 +402,9 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             c += 2;
             if (pw == 3) load_gates(w, c);
         }
-        ok = ok && mbar_wait_or_abort(&B->g[group], (nb >> 1) & 1, abort);
+        ok = ok && wait(&B->g[group], (nb >> 1) & 1);
         // P, and T' below, are written over those of block nb - 2
-        if (pw >= 2 && ok && nb >= 2) ok = mbar_wait_or_abort(&B->tp_free[group], ((nb - 2) >> 1) & 1, abort);
-        tc_fence_after();
-        ok = __all_sync(0xffffffffu, ok);
+        if (pw >= 2 && ok && nb >= 2) ok = wait(&B->tp_free[group], ((nb - 2) >> 1) & 1);
         // ---- E and P by rows, 16 columns at a time from the right. D at a group's right edge: zero in the
         //      group of the diagonal and right of it, else the row's gates from the edge on -----------
         if (ok) {
@@ -452,7 +467,7 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
 #pragma unroll
                 for (int i = s2 + 2; i < 16; ++i) x[i] = x[i] - e[i].x * x[s2] - e[i].y * x[s2 + 1];
             }
-            if (nb >= 2) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&B->tp_free[group], ((nb - 2) >> 1) & 1, abort));
+            if (nb >= 2) ok = wait(&B->tp_free[group], ((nb - 2) >> 1) & 1);
             if (ok) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -461,60 +476,54 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
                     st_shared_u16(aTH + o, hi);
                     st_shared_u16(aTL + o, __float2bfloat16_rn(x[i] - __bfloat162float(hi)));
                 }
-                __syncwarp();
-                // ---- the 16x16 block below: -T'_22 (E_21 T'_11) ----------------------------------
-                const int rb = 32 * pw + 16, cb = 32 * pw;   // its first row and column
-                uint32_t ah[4], al[4], th[4], tl[4], mh[4], ml[4];
-                load_split(E, rb, cb, ah, al);
-                ldsm4t(th, aTH + sw128_off(cb + fr, cb / 8 + fc));
-                ldsm4t(tl, aTL + sw128_off(cb + fr, cb / 8 + fc));
-                float Mx[2][4] = {}, N[2][4] = {};
-                mma_split(Mx, ah, al, th, tl);
-                split_tiles(Mx[0], Mx[1], mh, ml);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mh[i] = transpose8x8(mh[i]);
-                    ml[i] = transpose8x8(ml[i]);
-                }
-                ldsm4(th, aTH + sw128_off(rb + fr, rb / 8 + fc));
-                ldsm4(tl, aTL + sw128_off(rb + fr, rb / 8 + fc));
-                mma_split(N, th, tl, mh, ml);
-                store_negated(aTH, aTL, rb, cb, N);
             }
         }
         if (named_sync_or(bar, kPrepThreads, !ok)) return false;
-        // ---- rows 32..63, columns 0..31: -T'_B (E_BA T'_A), a 16x16 tile per warp -----------
-        {
-            const int mi = pw >> 1, ni = pw & 1;
-            float Mx[2][4] = {}, N[2][4] = {};
+        // ---- the blocks below: 16x16 ones (warps 0, 1), then the 32x32 one, a 16x16 tile per warp:
+        //      -T'(r0.., tk..) (E(r0.., ck..) T'(ck.., c0..)), the product in brackets through shared memory
+#pragma unroll 1
+        for (int level = 0; level < 2; ++level) {
+            const bool on = level == 1 || pw < 2;
+            const int r0 = level ? 32 + 16 * (pw >> 1) : 32 * pw + 16, c0 = level ? 16 * (pw & 1) : 32 * pw;
+            const int ck = level ? 0 : 32 * pw, tk = level ? 32 : r0;
+            const int mr = level ? 16 * (pw >> 1) : 16 * pw, mc = level ? 16 * (pw & 1) : 0, mk = level ? 0 : mr;
             uint32_t ah[4], al[4], th[4], tl[4];
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                load_split(E, 32 + 16 * mi, 16 * kk, ah, al);
-                ldsm4t(th, aTH + sw128_off(16 * kk + fr, 2 * ni + fc));
-                ldsm4t(tl, aTL + sw128_off(16 * kk + fr, 2 * ni + fc));
-                mma_split(Mx, ah, al, th, tl);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t hi, lo;
-                    split2(Mx[i][2 * h], Mx[i][2 * h + 1], hi, lo);
-                    const uint32_t o = (16 * mi + 8 * h + gq) * kMStride + (16 * ni + 8 * i) * 2 + 4 * cq;
-                    st_shared_b32(aM + o, hi);
-                    st_shared_b32(aM + 32 * kMStride + o, lo);
+            if (on) {
+                float Mx[2][4] = {};
+#pragma unroll 1
+                for (int kk = 0; kk <= 16 * level; kk += 16) {
+                    load_split(E, r0, ck + kk, ah, al);
+                    const uint32_t o = sw128_off(ck + kk + fr, c0 / 8 + fc);
+                    ldsm4t(th, aTH + o);
+                    ldsm4t(tl, aTL + o);
+                    mma_split(Mx, ah, al, th, tl);
                 }
-            named_sync(bar, kPrepThreads);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                ldsm4(ah, aTH + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
-                ldsm4(al, aTL + sw128_off(32 + 16 * mi + fr, 4 + 2 * kk + fc));
-                ldsm4t(th, aM + (16 * kk + fr) * kMStride + (2 * ni + fc) * 16);
-                ldsm4t(tl, aM + 32 * kMStride + (16 * kk + fr) * kMStride + (2 * ni + fc) * 16);
-                mma_split(N, ah, al, th, tl);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t hi, lo;
+                        split2(Mx[i][2 * h], Mx[i][2 * h + 1], hi, lo);
+                        const uint32_t o = (mr + 8 * h + gq) * kMStride + (mc + 8 * i) * 2 + 4 * cq;
+                        st_shared_b32(aM + o, hi);
+                        st_shared_b32(aM + 32 * kMStride + o, lo);
+                    }
             }
-            store_negated(aTH, aTL, 32 + 16 * mi, 16 * ni, N);
+            named_sync(bar, kPrepThreads);
+            if (on) {
+                float N[2][4] = {};
+#pragma unroll 1
+                for (int kk = 0; kk <= 16 * level; kk += 16) {
+                    const uint32_t o = sw128_off(r0 + fr, (tk + kk) / 8 + fc), m = (mk + kk + fr) * kMStride + mc * 2 + fc * 16;
+                    ldsm4(ah, aTH + o);
+                    ldsm4(al, aTL + o);
+                    ldsm4t(th, aM + m);
+                    ldsm4t(tl, aM + 32 * kMStride + m);
+                    mma_split(N, ah, al, th, tl);
+                }
+                store_negated(aTH, aTL, r0, c0, N);
+            }
+            if (level == 0) named_sync(bar, kPrepThreads);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -571,7 +580,6 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             mbar_init(&B->item_full[i], 1);
             mbar_init(&B->item_free[i], kThreads / 32 - 1);
         }
-        mbar_init(&B->want, 1);
         mbar_init(&B->stolen, 1);
         for (uint64_t* b : {&B->xh, &B->xl, &B->rh, &B->rl, &B->dh, &B->dl, &B->uo}) mbar_init(b, kConvWarps);
         for (uint64_t* b : {&B->z, &B->u, &B->o1, &B->dx, &B->o}) mbar_init(b, 1);
@@ -594,7 +602,6 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
 
     int status = 0;
     bool fail = false;
-    auto wait = [&](uint64_t* b, uint32_t parity) { fail = fail || !mbar_wait_or_abort(b, parity, abort); };
     if (warp < kConvWarps) {
         // ======================= converting warps ==================================
         const int r = 32 * (warp & 3) + lane, cp = warp >> 2, t0 = 16 * cp;   // row; part: tokens t0 .., channels XC cp ..
@@ -637,9 +644,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         };
         // warp-uniform before the warp-collective tensor-memory accesses
         auto wait_all = [&](uint64_t* b, uint32_t parity) {
-            const bool ok = !fail && mbar_wait_or_abort(b, parity, abort);
-            fail = !__all_sync(0xffffffffu, ok);
-            tc_fence_after();
+            fail = fail || !warp_wait(smem_u32(b), parity, abort);
         };
         Ring<kTiles> at;
         Ring<6> six;
@@ -791,9 +796,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             const uint64_t dT0 = kmaj(sbase + L::TP);
             const uint32_t cx = tmem + L::COL_X, cxp = tmem + L::COL_XP, cz = tmem + L::COL_Z, cu = tmem + L::COL_U, co = tmem + L::COL_O;
             auto wait_w = [&](uint64_t* b, uint32_t parity) {   // the whole warp goes on, or gives up, together
-                const bool ok = !fail && mbar_wait_or_abort(b, parity, abort);
-                fail = !__all_sync(0xffffffffu, ok);
-                tc_fence_after();
+                fail = fail || !warp_wait(smem_u32(b), parity, abort);
             };
             Ring<kTiles> at;
             Ring<6> six;
@@ -900,7 +903,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             }
         }
     } else if (warp == kOther + 1) {
-        // ======================= loads ===============================================
+        // ======================= K and Q loads =======================================
         Ring<kTiles> at;
         Ring<6> six;
         Work w;
@@ -908,37 +911,17 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         for (int k = 0; !fail && next_item(B, k, w, fail); ++k)
             for (int c = 0; c < w.blocks && !fail; ++c, ++nb, at.next(), six.next()) {
                 const int s = at.s, row = w.row0 + c * C;
-                if (lane == 0) {
-                    if (c + kTiles < w.blocks) {   // into L2, three blocks ahead
-#pragma unroll
-                        for (int x = 0; x < KA; ++x) {
-                            prefetch_3d(&tmk, x * 64, w.khead, row + kTiles * C);
-                            prefetch_3d(&tmq, x * 64, w.khead, row + kTiles * C);
-                        }
-#pragma unroll
-                        for (int x = 0; x < DV / 64; ++x) prefetch_3d(&tmv, x * 64, w.head, row + kTiles * C);
-                    }
-                    if (nb >= kTiles) wait(&B->kq_free[s], at.phase ^ 1);
-                    if (!fail) {
-                        uint8_t* kq = sm + L::KQ + s * L::KQ_BYTES;
-                        mbar_arrive_expect_tx(&B->kq_full[six.s], L::KQ_BYTES);
-#pragma unroll
-                        for (int x = 0; x < KA; ++x) {
-                            tma_load_3d(&tmk, &B->kq_full[six.s], kq + x * 16384, x * 64, w.khead, row);
-                            tma_load_3d(&tmq, &B->kq_full[six.s], kq + x * 16384 + 8192, x * 64, w.khead, row);
-                        }
-                    }
-                    const int vs = nb & 1;
-                    if (nb >= 2) wait(&B->v_free[vs], ((nb - 2) >> 1) & 1);
-                    if (!fail) {
-                        uint8_t* v = sm + L::V + vs * L::V_BYTES;
-                        mbar_arrive_expect_tx(&B->v_full[vs], L::V_BYTES);
-#pragma unroll
-                        for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[vs], v + x * 8192, x * 64, w.head, row);
-                        if (c + 1 == w.blocks) mbar_arrive(&B->want);
+                if (nb >= kTiles) fail = !warp_wait(smem_u32(&B->kq_free[s]), at.phase ^ 1, abort);
+                if (lane == 0 && !fail) {
+                    uint8_t* kq = sm + L::KQ + s * L::KQ_BYTES;
+                    mbar_arrive_expect_tx(&B->kq_full[six.s], L::KQ_BYTES);
+#pragma unroll 1
+                    for (int x = 0; x < KA; ++x) {
+                        tma_load_3d(&tmk, &B->kq_full[six.s], kq + x * 16384, x * 64, w.khead, row);
+                        tma_load_3d(&tmq, &B->kq_full[six.s], kq + x * 16384 + 8192, x * 64, w.khead, row);
                     }
                 }
-                fail = __any_sync(0xffffffffu, fail);
+                __syncwarp();
             }
         if (lane == 0) {
             // After a failure loads may be in flight: let them land (bounded; a
@@ -946,10 +929,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             if (fail || *abort) {
                 status = kStatusTmaWait;
                 for (int i = 0; i < 6; ++i)
-                    for (uint32_t ph = 0; ph < 2; ++ph) {
-                        mbar_wait(&B->kq_full[i], ph, 10000000ull);
-                        if (i < 2) mbar_wait(&B->v_full[i], ph, 10000000ull);
-                    }
+                    for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(&B->kq_full[i], ph, 10000000ull);
             }
         }
     } else if (warp == kOther + 2) {
@@ -961,8 +941,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(w.row0) * a.Hv + w.head) * DV;
             for (int c = 0; c < w.blocks; ++c, ++nb) {
                 const int vs = nb & 1;
-                wait(&B->ot_full[vs], (nb >> 1) & 1);
-                fail = !__all_sync(0xffffffffu, !fail);
+                fail = !warp_wait(smem_u32(&B->ot_full[vs]), (nb >> 1) & 1, abort);
                 if (fail) break;
                 const uint32_t ot = sbase + L::V + vs * L::V_BYTES;
                 const int n = min(C, w.len - c * C);
@@ -979,14 +958,13 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         }
         if (fail) status = kStatusMmaWait;
     } else {
-        // ======================= work ================================================
-        int idx = blockIdx.x;
+        // ======================= work and V loads ====================================
+        int idx = blockIdx.x, nb = 0;
         for (int k = 0;; ++k) {
             Request rq;
             const bool have = idx >= 0 && read_request(a, idx / a.Hv, rq);
             const int i = k % kItems;
-            if (k >= kItems) wait(&B->item_free[i], ((k / kItems) & 1) ^ 1);
-            fail = __any_sync(0xffffffffu, fail);
+            if (k >= kItems) fail = !warp_wait(smem_u32(&B->item_free[i]), ((k / kItems) & 1) ^ 1, abort);
             if (fail) break;
             Work w = {};
             if (have) {
@@ -1003,34 +981,42 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 mbar_arrive(&B->item_full[i]);
             }
             if (!have) break;
-            // what the item begins with, into L2
-            if (!w.fresh) {
+            if (!w.fresh) {   // the state, into L2
                 const float* st = a.states + (static_cast<size_t>(w.slot) * a.Hv + w.head) * DV * DK;
                 for (int x = lane; x < DV * DK / 32; x += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(st + 32 * x));
             }
-            if (lane < min(w.blocks, kTiles)) {
-                const int row = w.row0 + lane * C;
-#pragma unroll
-                for (int x = 0; x < KA; ++x) {
-                    prefetch_3d(&tmk, x * 64, w.khead, row);
-                    prefetch_3d(&tmq, x * 64, w.khead, row);
+            for (int c = 0; c < w.blocks && !fail; ++c, ++nb) {
+                const int vs = nb & 1, row = w.row0 + c * C;
+                // more work only once this item's last loads are at hand: what waits here could run elsewhere
+                if (c + 1 == w.blocks && lane == 0) steal_request(&B->answer, &B->stolen);
+                if (nb >= 2) fail = !warp_wait(smem_u32(&B->v_free[vs]), ((nb - 2) >> 1) & 1, abort);
+                if (lane == 0 && !fail) {
+                    uint8_t* v = sm + L::V + vs * L::V_BYTES;
+                    mbar_arrive_expect_tx(&B->v_full[vs], L::V_BYTES);
+#pragma unroll 1
+                    for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[vs], v + x * 8192, x * 64, w.head, row);
                 }
-#pragma unroll
-                for (int x = 0; x < DV / 64; ++x) prefetch_3d(&tmv, x * 64, w.head, row);
+                // the block after next, into L2 (K, Q and V; lanes 0 ..)
+                if (c + kTiles < w.blocks && lane < 2 * KA + DV / 64) {
+                    const CUtensorMap* m = lane < KA ? &tmk : lane < 2 * KA ? &tmq : &tmv;
+                    const int x = lane < KA ? lane : lane < 2 * KA ? lane - KA : lane - 2 * KA;
+                    prefetch_3d(m, x * 64, lane < 2 * KA ? w.khead : w.head, row + kTiles * C);
+                }
+                __syncwarp();
             }
-            // more work only once this item's loads are under way: what waits here could run elsewhere
-            wait(&B->want, k & 1);
-            fail = __any_sync(0xffffffffu, fail);
-            if (fail) break;
-            if (lane == 0) steal_request(&B->answer, &B->stolen);
-            wait(&B->stolen, k & 1);
-            fail = __any_sync(0xffffffffu, fail);
+            if (!fail) fail = !warp_wait(smem_u32(&B->stolen), k & 1, abort);
             if (fail) break;
             idx = stolen_index(&B->answer);
             fence_proxy_async_smem();   // this read comes before the next answer's write
             __syncwarp();
         }
-        if (fail) status = kStatusFlagWait;
+        if (fail) {
+            status = kStatusFlagWait;
+            if (lane == 0)
+                for (int i = 0; i < 2; ++i)
+                    for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(&B->v_full[i], ph, 10000000ull);
+            __syncwarp();
+        }
     }
     if (fail) *abort = 1;
     if (status && lane == 0) atomicOr(a.status, status);
