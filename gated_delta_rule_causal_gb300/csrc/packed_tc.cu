@@ -20,7 +20,7 @@
 // of the columns of each product in row r. Two groups of four prep warps
 // compute T' and P of the blocks that follow; of the others one issues the
 // chain's MMAs, one loads K and Q, one copies the outputs out, and one fetches
-// the work and loads V.
+// the work, loads V and issues the prep warps' [K;Q] K^T.
 //
 // The chain's steps depend on one another, so what bounds a request is their
 // latency: three products (Z, R T'^T, U' K) with a conversion after each. High
@@ -100,11 +100,11 @@ struct Bars {
     uint64_t v_full[2], v_free[2];               // TMA; copier: the output tile over V has left
     uint64_t vec_free[6];                        // converters: the block's vectors are read (16)
     uint64_t ot_full[2];                         // converters: the output tile is written (16)
-    uint64_t ready[2], tp_free[2];               // prep warps: T, P and vectors (4); MMA: T and P are read
+    uint64_t ready[2], t_free[2], p_free[2];     // prep warps: T', P and vectors (4); MMA: T', P is read
     uint64_t g[2], g_free;                       // MMA: [K;Q] K^T, per prep group; prep warps: it is read (4)
     uint64_t xh, xl, rh, rl, dh, dl, uo;         // converters: parts of X, R, U' and both of U published (16 each)
     uint64_t z, u, o1, dx, o;                    // MMA: Z, U, Q X^T, dX, O done
-    uint64_t drain[3];                           // after a failure: MMAs of either issuer are done
+    uint64_t drain[2];                           // after a failure: MMAs of either issuer are done
     uint64_t item_full[kItems], item_free[kItems];   // work warp; every other warp has read the item (27)
     uint64_t stolen;                             // the answer to a request for more work is here
     uint32_t tmem;
@@ -184,6 +184,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
     if (!ok) ok = warp_wait_on(bar, parity, abort);
     tc_fence_after();
     return ok;
+}
+
+// Whether phase `parity` of `bar` is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
 }
 
 // The k-th item of this CTA, for a whole warp; false when there is none (blocks
@@ -310,7 +321,6 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
     const int fr = (lane & 7) + ((lane >> 3) & 1) * 8, fc = lane >> 4;
     const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * pw) << 16);
     const uint32_t bar = kBarPrep + group;
-    const bool el = elect_one();
     volatile int* abort = &B->abort;
     auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(smem_u32(b), parity, abort); };
     float* E = reinterpret_cast<float*>(sm + L::A) + group * C * kAStride;
@@ -356,17 +366,18 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
         ++nb;
     }
     if (more && pw == 3) load_gates(w, c);
-    while (more) {
+    // Warps that fail say so at the next barrier of the group and all leave together: a barrier has no limit.
+    bool ok = true;
+    while (true) {
         const uint32_t kq = sbase + L::KQ + at.s * L::KQ_BYTES;
         float* vec = reinterpret_cast<float*>(sm + L::VEC) + at.s * kVec;
         const int n = w.len - c * C;   // tokens of the block
-        bool ok = true;
-        if (pw == 3) {   // the slot's vectors of block nb - 3 are read
+        if (pw == 3 && more && ok) {   // the slot's vectors of block nb - 3 are read
             const int b3 = six.s < 3 ? six.s + 3 : six.s - 3;   // block nb - 3's place; its turn is the one before from 0 .. 2
             ok = nb < kTiles || wait(&B->vec_free[b3], six.phase ^ (six.s < 3 ? 1 : 0));
             if (ok) write_gates(vec, gn, bn);
         }
-        if (n < C) {   // rows of the next request (or past the tensor): K and V zero, so that they leave the state alone
+        if (more && n < C) {   // rows of the next request (or past the tensor): K and V zero, so that they leave the state alone
             ok = ok && wait(&B->kq_full[six.s], six.phase) && wait(&B->v_full[group], (nb >> 1) & 1);
             if (ok) {
                 const uint32_t v = sbase + L::V + group * L::V_BYTES;
@@ -380,21 +391,8 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             }
             fence_proxy_async_smem();
         }
-        if (named_sync_or(bar, kPrepThreads, !ok)) return false;
-        if (pw == 2) {   // [K;Q] K^T, once the other group has read its own
-            ok = wait(&B->kq_full[six.s], six.phase) && (nb == 0 || wait(&B->g_free, (nb - 1) & 1));
-            if (ok && el) {
-                constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
-                const uint64_t d0 = kmaj(kq);
-#pragma unroll 1
-                for (int kk = 0; kk < DK / 16; ++kk) {
-                    const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
-                    mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
-                }
-                mma_commit(&B->g[group]);
-            }
-            __syncwarp();
-        }
+        if (named_sync_or(bar, kPrepThreads, !ok || lost)) return false;
+        if (!more) return true;
         // The block after next, its gates loaded meanwhile. (Only within the request: the next one may wait for
         // this one's loads, and those for this very block.)
         const bool same = c + 2 < w.blocks;
@@ -403,8 +401,6 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             if (pw == 3) load_gates(w, c);
         }
         ok = ok && wait(&B->g[group], (nb >> 1) & 1);
-        // P, and T' below, are written over those of block nb - 2
-        if (pw >= 2 && ok && nb >= 2) ok = wait(&B->tp_free[group], ((nb - 2) >> 1) & 1);
         // ---- E and P by rows, 16 columns at a time from the right. D at a group's right edge: zero in the
         //      group of the diagonal and right of it, else the row's gates from the edge on -----------
         if (ok) {
@@ -412,11 +408,16 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             const int hd = pw & 1;   // the half of the columns with this warp's diagonal
             const int t = 32 * hd + lane;
             const float g16 = vec[4 * C + t], g32 = vec[5 * C + t], mid = vec[4 * C + 31];
+            // P waits in scratch until the one of block nb - 2 is read: rows 0..31 where the merges' product
+            // comes later, rows 32..63 in E's columns 32.. of rows 0..31, which nothing else uses
+            const uint32_t ps = hd ? smem_u32(E) + lane * (kAStride * 4) + 128 : aM + lane * 64;
 #pragma unroll 1
             for (int c16 = 2 * hd + 1; c16 >= 0; --c16) {
                 const int u = 2 * hd + 1 - c16;   // 0, 1: the half of the diagonal; 2, 3: columns 16..31, 0..15 of rows 32..
                 float d = u == 0 ? 0.f : u == 1 ? (lane >= 16 ? g16 : 0.f) : u == 2 ? g32 : g32 * mid;
-                const int diag = u < 2 ? lane - (16 - 16 * u) : -1;   // the column of the row's diagonal element
+                const int diag = u < 2 ? lane - (16 - 16 * u) : 99;   // the column of the row's diagonal element
+                // the last column that counts: what lies right of it, or in rows past the request's end, may be anything
+                const int lim = isP ? diag : t < n ? diag - 1 : -1;
                 float x[16];
                 tmem_ld16(tlane + L::COL_G + 16 * c16, x);
                 tmem_ld_wait();
@@ -427,15 +428,15 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
 #pragma unroll
                     for (int i = 3; i >= 0; --i) {
                         const int j = 4 * q4 + i;
-                        if (j == diag) d = 1.f;
-                        x[j] *= (j == diag && !isP) ? 0.f : d;
+                        d = j == diag ? 1.f : d;
+                        x[j] = j <= lim ? d * x[j] : 0.f;
                         d *= gl[i];   // the gate of column j itself comes before the columns left of it
                     }
                 }
                 if (isP) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
-                        st_shared_v4(aP + sw128_off(t, 2 * c16 + m), pack_bf16(x[8 * m], x[8 * m + 1]), pack_bf16(x[8 * m + 2], x[8 * m + 3]),
+                        st_shared_v4(ps + (2 * c16 + m) * 16, pack_bf16(x[8 * m], x[8 * m + 1]), pack_bf16(x[8 * m + 2], x[8 * m + 3]),
                                      pack_bf16(x[8 * m + 4], x[8 * m + 5]), pack_bf16(x[8 * m + 6], x[8 * m + 7]));
                 } else {
 #pragma unroll
@@ -447,6 +448,15 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&B->g_free);
+            if (isP) {
+                if (nb >= 2) ok = wait(&B->p_free[group], ((nb - 2) >> 1) & 1);
+#pragma unroll 1
+                for (int i = lane; i < 128 << hd && ok; i += 32) {   // this warp's 32 rows of 4 (8) chunks
+                    const int row = i >> (2 + hd), ch = i & (3 + 4 * hd);
+                    const uint4 y = ld_shared_v4((hd ? smem_u32(E) + row * (kAStride * 4) + 128 : aM + row * 64) + ch * 16);
+                    st_shared_v4(aP + sw128_off(32 * hd + row, ch), y.x, y.y, y.z, y.w);
+                }
+            }
         }
         if (pw < 2 && ok) {
             // ---- diagonal blocks 2 pw and 2 pw + 1 (rows of this warp), lane = (block, column):
@@ -467,7 +477,7 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
 #pragma unroll
                 for (int i = s2 + 2; i < 16; ++i) x[i] = x[i] - e[i].x * x[s2] - e[i].y * x[s2 + 1];
             }
-            if (nb >= 2) ok = wait(&B->tp_free[group], ((nb - 2) >> 1) & 1);
+            if (nb >= 2) ok = wait(&B->t_free[group], ((nb - 2) >> 1) & 1);
             if (ok) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -478,7 +488,10 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
                 }
             }
         }
-        if (named_sync_or(bar, kPrepThreads, !ok)) return false;
+        if (named_sync_or(bar, kPrepThreads, !ok)) {
+            *abort = 1;
+            return false;
+        }
         // ---- the blocks below: 16x16 ones (warps 0, 1), then the 32x32 one, a 16x16 tile per warp:
         //      -T'(r0.., tk..) (E(r0.., ck..) T'(ck.., c0..)), the product in brackets through shared memory
 #pragma unroll 1
@@ -538,7 +551,6 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
         six.next();
         six.next();
     }
-    return !lost;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -571,10 +583,10 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             mbar_init(&B->v_free[i], 1);
             mbar_init(&B->ot_full[i], kConvWarps);
             mbar_init(&B->ready[i], kPrepWarps);
-            mbar_init(&B->tp_free[i], 1);
+            mbar_init(&B->t_free[i], 1);
+            mbar_init(&B->p_free[i], 1);
             mbar_init(&B->drain[i], 1);
         }
-        mbar_init(&B->drain[2], 1);
         mbar_init(&B->g_free, kPrepWarps);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&B->item_full[i], 1);
@@ -774,13 +786,6 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         if (!prep_warps<DK>(a, sm, sbase, B, tmem)) {
             fail = true;
             status = kStatusMmaWait;
-            *abort = 1;
-            if ((warp & 3) == 2 && elect_one()) {   // the lane that issued this group's MMAs
-                uint64_t* d = &B->drain[1 + (warp - kConvWarps) / kPrepWarps];
-                mma_commit(d);
-                mbar_wait(d, 0, 100000000ull);
-            }
-            __syncwarp();
         }
     } else if (warp == kOther) {
         // ======================= MMA issue ==========================================
@@ -812,28 +817,30 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     wait_w(&B->v_full[p], (nb >> 1) & 1);
                     if (nb >= 1) wait_w(&B->o, p ^ 1);
                     if (!fail && el) {
-#pragma unroll 1
+#pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             mma_bf16_ss(cu, dV + kk * 128, dT + kk * 2, ID_V, kk > 0);
                             mma_bf16_ss(cu, dV + kk * 128, dT + 512 + kk * 2, ID_V, true);
                         }
                     }
                 };
-                // before X is published if T' is there already
-                const bool u_early = __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&B->ready[p]), (nb >> 1) & 1));
+                // before X is published if T' and V are there already and the block before's products are done
+                const bool u_early = __all_sync(0xffffffffu, mbar_test(smem_u32(&B->ready[p]), (nb >> 1) & 1) &&
+                                                                 mbar_test(smem_u32(&B->v_full[p]), (nb >> 1) & 1) &&
+                                                                 (nb == 0 || mbar_test(smem_u32(&B->o), p ^ 1)));
                 if (u_early) start_u();
                 wait_w(&B->kq_full[six.s], six.phase);
                 if (w.len - c * C < C) wait_w(&B->ready[p], (nb >> 1) & 1);   // K's rows past the end are zeroed
                 wait_w(&B->xh, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, cxp + 16 * kk, dK + kstep(kk), ID_64, kk > 0);
                 }
                 wait_w(&B->xl, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(cz, cxp + 16 * kk + 8, dK + kstep(kk), ID_64, true);
                     mma_commit(&B->z);
                 }
@@ -844,14 +851,14 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 if (nb >= 1) wait_w(&B->ot_full[p ^ 1], ((nb - 1) >> 1) & 1);   // the outputs of the block before are read
                 if (fail) break;
                 if (el) {
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < DK / 16; ++kk) mma_bf16_ts(co, cxp + 16 * kk, dK + 512 + kstep(kk), ID_64, kk > 0);
                     mma_commit(&B->o1);
                 }
                 wait_w(&B->rh, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         mma_bf16_ts(cu, cz + 16 * kk, dT + kk * 2, ID_64, true);
                         mma_bf16_ts(cu, cz + 16 * kk, dT + 512 + kk * 2, ID_64, true);
@@ -860,39 +867,43 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 wait_w(&B->rl, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cu, cz + 16 * kk + 8, dT + kk * 2, ID_64, true);
                     mma_commit(&B->u);
+                    mma_commit(&B->t_free[p]);
                 }
                 wait_w(&B->dh, p);   // (after Q X^T was waited for: U' lies where the parts of X were)
                 if (fail) break;
                 if (el) {
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cx, cxp + 16 * kk, dKm + kk * 128, ID_K, true);
                 }
                 wait_w(&B->dl, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(cx, cxp + 16 * kk + 8, dKm + kk * 128, ID_K, true);
                     mma_commit(&B->dx);
                 }
                 wait_w(&B->uo, p);
                 if (fail) break;
                 if (el) {
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         mma_bf16_ts(co, cu + 16 * kk, dT + 1024 + kk * 2, ID_64, true);
                         mma_bf16_ts(co, cu + 16 * kk + 8, dT + 1024 + kk * 2, ID_64, true);
                     }
                     mma_commit(&B->o);
                     mma_commit(&B->kq_free[at.s]);
-                    mma_commit(&B->tp_free[p]);
+                    mma_commit(&B->p_free[p]);
                 }
             }
             // the last arrivals that nobody else waits for: after the CTA has left they would hit another's memory
             for (int m = nb < kTiles ? 0 : nb - kTiles; m < nb && !fail; ++m) wait_w(&B->kq_free[m % kTiles], (m / kTiles) & 1);
-            for (int m = nb < 2 ? 0 : nb - 2; m < nb && !fail; ++m) wait_w(&B->tp_free[m & 1], (m >> 1) & 1);
+            for (int m = nb < 2 ? 0 : nb - 2; m < nb && !fail; ++m) {
+                wait_w(&B->t_free[m & 1], (m >> 1) & 1);
+                wait_w(&B->p_free[m & 1], (m >> 1) & 1);
+            }
             if (fail) {   // every MMA issued completes before the CTA leaves (bounded)
                 status = kStatusMmaWait;
                 if (el) {
@@ -958,8 +969,12 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         }
         if (fail) status = kStatusMmaWait;
     } else {
-        // ======================= work and V loads ====================================
-        int idx = blockIdx.x, nb = 0;
+        // ======================= work, V loads, [K;Q] K^T ============================
+        int idx = blockIdx.x, nb = 0, np = 0;   // block of V; of the products
+        Ring<kTiles> pt;                        // of block np
+        Ring<6> psix;
+        const bool el = elect_one();
+        const uint64_t dK0 = kmaj(sbase + L::KQ);
         for (int k = 0;; ++k) {
             Request rq;
             const bool have = idx >= 0 && read_request(a, idx / a.Hv, rq);
@@ -996,6 +1011,22 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
 #pragma unroll 1
                     for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[vs], v + x * 8192, x * 64, w.head, row);
                 }
+                // this request's products up to the next block's, each once its tile is here and the one before is read
+                for (const int last = nb + min(1, w.blocks - 1 - c); np <= last && !fail; ++np, pt.next(), psix.next()) {
+                    fail = !warp_wait(smem_u32(&B->kq_full[psix.s]), psix.phase, abort) ||
+                           (np > 0 && !warp_wait(smem_u32(&B->g_free), (np - 1) & 1, abort));
+                    if (el && !fail) {
+                        constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
+                        const uint64_t d0 = dK0 + pt.s * (L::KQ_BYTES / 16);
+#pragma unroll 1
+                        for (int kk = 0; kk < DK / 16; ++kk) {
+                            const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
+                            mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
+                        }
+                        mma_commit(&B->g[np & 1]);
+                    }
+                    __syncwarp();
+                }
                 // the block after next, into L2 (K, Q and V; lanes 0 ..)
                 if (c + kTiles < w.blocks && lane < 2 * KA + DV / 64) {
                     const CUtensorMap* m = lane < KA ? &tmk : lane < 2 * KA ? &tmq : &tmv;
@@ -1012,6 +1043,10 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         }
         if (fail) {
             status = kStatusFlagWait;
+            if (el) {   // the products in flight
+                mma_commit(&B->drain[1]);
+                mbar_wait(&B->drain[1], 0, 100000000ull);
+            }
             if (lane == 0)
                 for (int i = 0; i < 2; ++i)
                     for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(&B->v_full[i], ph, 10000000ull);
