@@ -914,34 +914,73 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             }
         }
     } else if (warp == kOther + 1) {
-        // ======================= K and Q loads =======================================
-        Ring<kTiles> at;
-        Ring<6> six;
+        // ======================= K and Q loads, [K;Q] K^T ============================
+        Ring<kTiles> at, pt;   // of the loads; of the products
+        Ring<6> six, psix;
+        const bool el = elect_one();
+        const uint64_t dK0 = kmaj(sbase + L::KQ);
         Work w;
-        int nb = 0;
-        for (int k = 0; !fail && next_item(B, k, w, fail); ++k)
-            for (int c = 0; c < w.blocks && !fail; ++c, ++nb, at.next(), six.next()) {
-                const int s = at.s, row = w.row0 + c * C;
-                if (nb >= kTiles) fail = !warp_wait(smem_u32(&B->kq_free[s]), at.phase ^ 1, abort);
-                if (lane == 0 && !fail) {
-                    uint8_t* kq = sm + L::KQ + s * L::KQ_BYTES;
-                    mbar_arrive_expect_tx(&B->kq_full[six.s], L::KQ_BYTES);
-#pragma unroll 1
-                    for (int x = 0; x < KA; ++x) {
-                        tma_load_3d(&tmk, &B->kq_full[six.s], kq + x * 16384, x * 64, w.khead, row);
-                        tma_load_3d(&tmq, &B->kq_full[six.s], kq + x * 16384 + 8192, x * 64, w.khead, row);
+        int nb = 0, np = 0;
+        for (int k = 0; !fail && next_item(B, k, w, fail); ++k) {
+            const int first = nb;
+            while (!fail && np < first + w.blocks) {
+                // the loads of block np, and of those after it whose slots are free already
+                while (nb < first + w.blocks && nb < np + kTiles) {
+                    const uint32_t slot = smem_u32(&B->kq_free[at.s]);
+                    if (nb >= kTiles) {
+                        if (nb == np)
+                            fail = !warp_wait(slot, at.phase ^ 1, abort);
+                        else if (!__all_sync(0xffffffffu, mbar_test(slot, at.phase ^ 1)))
+                            break;
+                        if (fail) break;
                     }
+                    if (lane == 0) {
+                        uint8_t* kq = sm + L::KQ + at.s * L::KQ_BYTES;
+                        const int row = w.row0 + (nb - first) * C;
+                        mbar_arrive_expect_tx(&B->kq_full[six.s], L::KQ_BYTES);
+#pragma unroll 1
+                        for (int x = 0; x < KA; ++x) {
+                            tma_load_3d(&tmk, &B->kq_full[six.s], kq + x * 16384, x * 64, w.khead, row);
+                            tma_load_3d(&tmq, &B->kq_full[six.s], kq + x * 16384 + 8192, x * 64, w.khead, row);
+                        }
+                    }
+                    __syncwarp();
+                    ++nb;
+                    at.next();
+                    six.next();
+                }
+                if (fail) break;
+                // its product, once the tile is here and the product before is read
+                fail = !warp_wait(smem_u32(&B->kq_full[psix.s]), psix.phase, abort) ||
+                       (np > 0 && !warp_wait(smem_u32(&B->g_free), (np - 1) & 1, abort));
+                if (el && !fail) {
+                    constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
+                    const uint64_t d0 = dK0 + pt.s * (L::KQ_BYTES / 16);
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk) {
+                        const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
+                        mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
+                    }
+                    mma_commit(&B->g[np & 1]);
                 }
                 __syncwarp();
+                ++np;
+                pt.next();
+                psix.next();
             }
-        if (lane == 0) {
+        }
+        if (fail || *abort) {
+            status = kStatusTmaWait;
+            if (el) {   // the products in flight
+                mma_commit(&B->drain[1]);
+                mbar_wait(&B->drain[1], 0, 100000000ull);
+            }
             // After a failure loads may be in flight: let them land (bounded; a
             // phase that no load began runs into the limit).
-            if (fail || *abort) {
-                status = kStatusTmaWait;
+            if (lane == 0)
                 for (int i = 0; i < 6; ++i)
                     for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(&B->kq_full[i], ph, 10000000ull);
-            }
+            __syncwarp();
         }
     } else if (warp == kOther + 2) {
         // ======================= output copies =======================================
@@ -969,12 +1008,8 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         }
         if (fail) status = kStatusMmaWait;
     } else {
-        // ======================= work, V loads, [K;Q] K^T ============================
-        int idx = blockIdx.x, nb = 0, np = 0;   // block of V; of the products
-        Ring<kTiles> pt;                        // of block np
-        Ring<6> psix;
-        const bool el = elect_one();
-        const uint64_t dK0 = kmaj(sbase + L::KQ);
+        // ======================= work, V loads =======================================
+        int idx = blockIdx.x, nb = 0;
         for (int k = 0;; ++k) {
             Request rq;
             const bool have = idx >= 0 && read_request(a, idx / a.Hv, rq);
@@ -1011,22 +1046,6 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
 #pragma unroll 1
                     for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[vs], v + x * 8192, x * 64, w.head, row);
                 }
-                // this request's products up to the next block's, each once its tile is here and the one before is read
-                for (const int last = nb + min(1, w.blocks - 1 - c); np <= last && !fail; ++np, pt.next(), psix.next()) {
-                    fail = !warp_wait(smem_u32(&B->kq_full[psix.s]), psix.phase, abort) ||
-                           (np > 0 && !warp_wait(smem_u32(&B->g_free), (np - 1) & 1, abort));
-                    if (el && !fail) {
-                        constexpr uint32_t ID_G = idesc_bf16(128, 64, false, false);
-                        const uint64_t d0 = dK0 + pt.s * (L::KQ_BYTES / 16);
-#pragma unroll 1
-                        for (int kk = 0; kk < DK / 16; ++kk) {
-                            const uint64_t d = d0 + (kk / 4) * 1024 + (kk % 4) * 2;
-                            mma_bf16_ss(tmem + L::COL_G, d, d, ID_G, kk > 0);
-                        }
-                        mma_commit(&B->g[np & 1]);
-                    }
-                    __syncwarp();
-                }
                 // the block after next, into L2 (K, Q and V; lanes 0 ..)
                 if (c + kTiles < w.blocks && lane < 2 * KA + DV / 64) {
                     const CUtensorMap* m = lane < KA ? &tmk : lane < 2 * KA ? &tmq : &tmv;
@@ -1043,10 +1062,6 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         }
         if (fail) {
             status = kStatusFlagWait;
-            if (el) {   // the products in flight
-                mma_commit(&B->drain[1]);
-                mbar_wait(&B->drain[1], 0, 100000000ull);
-            }
             if (lane == 0)
                 for (int i = 0; i < 2; ++i)
                     for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(&B->v_full[i], ph, 10000000ull);
