@@ -16,8 +16,9 @@
 // [dv][token], a warp's accumulators (X, Z = X K^T, R, U) turn into the next
 // product's A operand inside its own registers, so from the state's load to
 // its store the chain exchanges nothing between warps. K, Q, V tiles come by
-// TMA into a ring of three stages; ahead of the chain one prep warp computes T
-// of every block, another P, which also issues the loads.
+// TMA into a ring of three stages; two prep warps compute T and P of a block
+// each, ahead of the chain. The last chain warp to leave a stage issues the
+// loads that reuse it.
 //
 // Precision. q, k, v are bf16 and enter the MMAs as they are. What the state
 // depends on (X in K X^T, R and T in T R, U in U^T K) is split into two bf16
@@ -27,9 +28,9 @@
 // keeps one part where the other factor is exact: X in Q X^T, P in P U.
 // Accumulators, gates, A and the inverse are fp32.
 //
-// Rows past a request's end belong to the next request: K and V are zeroed there
-// before the chain reads them, with gate 1 and beta 0, so that they leave the
-// state alone; Q's reach only outputs that are not written.
+// Rows past a request's end belong to the next request: they are zeroed in the
+// tiles before anything reads them, with gate 1 and beta 0, and are not
+// written.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -46,15 +47,15 @@ namespace {
 constexpr int C = kBlock;
 constexpr int kChain = 4;                  // chain warps: 16 state rows each
 constexpr int kRows = 16 * kChain;         // state rows of a CTA
-constexpr int kPrep = 2;                   // prep warps: T, and P with the loads
+constexpr int kPrep = 2;                   // prep warps
 constexpr int kThreads = 32 * (kChain + kPrep);
 constexpr int kStages = 3;
 constexpr int kTStride = 80;               // bytes per row of a 32x32 bf16 tile: 16-byte chunks of 8 rows hit all banks
-// a prep warp's fp32 scratch: two 16x16 sub-blocks of K K^T or Q K^T, rows and blocks so far apart that the MMA
+// prep warps' fp32 scratch: two 16x16 sub-blocks each of K K^T and Q K^T, rows and blocks so far apart that the MMA
 // fragments' stores and the column reads of both halves of the warp hit all banks; then the gates
 constexpr int kSStride = 24;
 constexpr int kSBlock = 16 * kSStride + 16;
-constexpr int kScratch = 2 * kSBlock + C;
+constexpr int kScratch = 4 * kSBlock + C;
 
 template <int DK>
 struct Layout {
@@ -84,85 +85,21 @@ struct Item {
 };
 
 // ---------------------------------------------------------------- prep warps
-
-// Ring position of a block, stepped instead of divided.
-struct Ring {
-    int s = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++s == kStages) {
-            s = 0;
-            phase ^= 1;
-        }
-    }
-};
-
-// Loads of the request's next block into stage s (one thread); rows past the
-// tensor read as zeros.
-template <int DK>
-__device__ __forceinline__ void issue_loads(const CUtensorMap* tmq, const CUtensorMap* tmk, const CUtensorMap* tmv,
-                                            const Item& it, uint8_t* sm, uint64_t* full, int c, int s) {
-    using L = Layout<DK>;
-    const int row = it.rq.row0 + c * C;
-    uint8_t* st = sm + s * L::STAGE;
-    mbar_arrive_expect_tx(&full[s], L::TX);
-#pragma unroll
-    for (int x = 0; x < L::KA; ++x) {
-        tma_load_3d(tmk, &full[s], st + L::K + x * 4096, x * 64, it.khead, row);
-        tma_load_3d(tmq, &full[s], st + L::Q + x * 4096, x * 64, it.khead, row);
-    }
-    tma_load_3d(tmv, &full[s], st + L::V, it.split * kRows, it.head, row);
-}
-
-// The lower 16x16 tiles of M K^T, M = K or Q: tiles (m, n) of 16x8
-// (0,0) (0,1) (1,0) (1,1) (1,2) (1,3). Fragments are loaded a step ahead; a
-// key fragment serves as A and as B.
-template <int DK, bool QK>
-__device__ __forceinline__ void lower_products(uint32_t aM, uint32_t aK, int fr, int fc, float (&d)[6][4]) {
-    uint32_t k0[2][4], k1[2][4], m0[2][4], m1[2][4];
-    auto load = [&](int x) {
-        const uint32_t at = (x / 4) * 4096, ch = (x % 4) * 2 + fc;
-        const uint32_t lo = at + sw128_off(fr, ch), hi = at + sw128_off(16 + fr, ch);
-        ldsm4(k0[x & 1], aK + lo);
-        ldsm4(k1[x & 1], aK + hi);
-        if (QK) {
-            ldsm4(m0[x & 1], aM + lo);
-            ldsm4(m1[x & 1], aM + hi);
-        }
-    };
-    load(0);
-#pragma unroll
-    for (int x = 0; x < DK / 16; ++x) {
-        if (x + 1 < DK / 16) load(x + 1);
-        const auto& u0 = k0[x & 1];
-        const auto& u1 = k1[x & 1];
-        const auto& w0 = QK ? m0[x & 1] : k0[x & 1];
-        const auto& w1 = QK ? m1[x & 1] : k1[x & 1];
-        mma_16816(d[0], w0, u0[0], u0[2]);
-        mma_16816(d[1], w0, u0[1], u0[3]);
-        mma_16816(d[2], w1, u0[0], u0[2]);
-        mma_16816(d[3], w1, u0[1], u0[3]);
-        mma_16816(d[4], w1, u1[0], u1[2]);
-        mma_16816(d[5], w1, u1[1], u1[3]);
-    }
-}
-
-// One prep warp: T (two bf16 parts) and the gate vectors of every block, or
-// (QK) P of every block, as the loads' issuer besides.
+// T (two bf16 parts), P and the gate vectors of blocks pw, pw + kPrep, ...
 //
-// By 16x16 sub-blocks: on the diagonal lane l takes one column of sub-block
-// l / 16, D_tj being its running product, and inverts by forward substitution
-// in fp32; the sub-block below is T21 = -T22 (A21 T11) on the tensor cores,
-// operands in two bf16 parts, with D_tj = (g_16 .. g_t)(g_{j+1} .. g_15).
-template <int DK, bool QK>
-__device__ __forceinline__ void prep_warp(const CUtensorMap* tmq, const CUtensorMap* tmk, const CUtensorMap* tmv,
-                                          const StepArgs& a, const Item& it, uint8_t* sm, uint32_t sbase,
-                                          uint64_t* full, uint64_t* ready, uint64_t* empty, volatile int* abort_flag) {
+// By 16x16 sub-blocks: the diagonal ones by forward substitution in fp32, lane
+// l one column of sub-block l / 16; the one below them as T21 = -T22 (A21 T11)
+// on the tensor cores, operands in two bf16 parts. Between the halves the
+// decay factors: D_tj = (g_16 .. g_t)(g_{j+1} .. g_15) for j < 16 <= t.
+template <int DK>
+__device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uint8_t* sm, uint32_t sbase, int pw,
+                                          uint64_t* full, uint64_t* ready, volatile int* abort_flag) {
     using L = Layout<DK>;
     const int lane = threadIdx.x & 31, gq = lane >> 2, cq = lane & 3;
     const int blk = lane >> 4, col = lane & 15;
-    float* raw = reinterpret_cast<float*>(sm + L::SCRATCH) + (QK ? kScratch : 0);   // diagonal sub-blocks, then A
-    float* gs = raw + 2 * kSBlock;                                                  // gates [32]
+    float* kk = reinterpret_cast<float*>(sm + L::SCRATCH) + pw * kScratch;   // diagonal sub-blocks of K K^T, then A
+    float* qk = kk + 2 * kSBlock;                                            // and of Q K^T
+    float* gs = qk + 2 * kSBlock;                                            // gates [32]
     // A fragment of an m16 x k16 tile by ldmatrix: lane -> row, 16-byte chunk
     // (the same addresses, transposed, give the B fragments of a k16 x n16 tile)
     const int fr = (lane & 7) + ((lane >> 3) & 1) * 8, fc = lane >> 4;
@@ -173,180 +110,199 @@ __device__ __forceinline__ void prep_warp(const CUtensorMap* tmq, const CUtensor
         if (t < it.rq.len) {
             const size_t i = static_cast<size_t>(it.rq.row0 + t) * a.Hv + it.head;
             g = __ldg(a.gate + i);
-            if (!QK) b = __ldg(a.beta + i);
+            b = __ldg(a.beta + i);
         }
     };
-    if (QK && lane == 0)
-        for (int c = 0; c < kStages && c < it.blocks; ++c) issue_loads<DK>(tmq, tmk, tmv, it, sm, full, c, c);
     float gn, bn;
-    gates(0, gn, bn);
-    Ring at;   // block c
-    Ring old;  // block c - kStages + 1, whose stage block c + 1 takes
-    for (int c = 0; c < it.blocks; ++c, at.next()) {
-        const int s = at.s;
+    gates(pw, gn, bn);
+    for (int c = pw; c < it.blocks; c += kPrep) {
+        const int s = c % kStages;
         const uint32_t st = sbase + s * L::STAGE;
-        float* vec = reinterpret_cast<float*>(sm + s * L::STAGE + L::VEC);
         const float g = gn, b = bn;
-        gates(c + 1, gn, bn);
-        float Gh = g;   // product of the gates from the half's start up to this token
+        gates(c + kPrep, gn, bn);
+        // ---- gate vectors: products inside each half, then over the block ----------------
+        float G = g;
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, Gh, o);
-            if (col >= o) Gh *= y;
+            const float y = __shfl_up_sync(0xffffffffu, G, o);
+            if (col >= o) G *= y;
         }
-        const float G15 = __shfl_sync(0xffffffffu, Gh, 15), G31 = __shfl_sync(0xffffffffu, Gh, 31);
+        const float Gq = G;   // (second half) the gates from 16 up to this token
+        const float G15 = __shfl_sync(0xffffffffu, G, 15), G31 = __shfl_sync(0xffffffffu, G, 31);
+        if (blk) G *= G15;
         gs[lane] = g;
-        const bool ok = mbar_wait_or_abort(&full[s], at.phase, abort_flag);
+        bool ok = mbar_wait_or_abort(&full[s], (c / kStages) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) return;
+        float* vec = reinterpret_cast<float*>(sm + s * L::STAGE + L::VEC);
+        vec[lane] = b;
+        vec[C + lane] = b * G;
+        vec[2 * C + lane] = G;
         const int n = it.rq.len - c * C;   // tokens of the block
-        if (!QK && n < C) {                // rows of the next request (or past the tensor): zero
+        if (n < C) {                       // rows of the next request (or past the tensor): zero
             for (int i = lane; i < (C - n) * 8; i += 32) {
                 const uint32_t o = sw128_off(n + i / 8, i % 8);
 #pragma unroll
-                for (int x = 0; x < L::KA; ++x) st_shared_zero16(st + L::K + x * 4096 + o);
+                for (int at = 0; at < L::KA; ++at) {
+                    st_shared_zero16(st + L::K + at * 4096 + o);
+                    st_shared_zero16(st + L::Q + at * 4096 + o);
+                }
                 st_shared_zero16(st + L::V + o);
             }
+            __syncwarp();
         }
-        if (!QK) {
-            const float G = blk ? Gh * G15 : Gh;
-            vec[lane] = b;
-            vec[C + lane] = b * G;
-            vec[2 * C + lane] = G;
+        // ---- K K^T and Q K^T, lower tiles only; a key fragment serves as A and as B ----
+        float dk[6][4] = {}, dq[6][4] = {};   // tiles (m, n): (0,0) (0,1) (1,0) (1,1) (1,2) (1,3)
+        uint32_t f[2][4][4];                  // fragments k rows 0-15, 16-31, q rows 0-15, 16-31; one step ahead
+        auto load = [&](int x, uint32_t (&w)[4][4]) {
+            const uint32_t at = (x / 4) * 4096, ch = (x % 4) * 2 + fc;
+            ldsm4(w[0], st + L::K + at + sw128_off(fr, ch));
+            ldsm4(w[1], st + L::K + at + sw128_off(16 + fr, ch));
+            ldsm4(w[2], st + L::Q + at + sw128_off(fr, ch));
+            ldsm4(w[3], st + L::Q + at + sw128_off(16 + fr, ch));
+        };
+        load(0, f[0]);
+#pragma unroll
+        for (int x = 0; x < DK / 16; ++x) {
+            if (x + 1 < DK / 16) load(x + 1, f[(x + 1) & 1]);
+            const auto& w = f[x & 1];
+            mma_16816(dk[0], w[0], w[0][0], w[0][2]);
+            mma_16816(dk[1], w[0], w[0][1], w[0][3]);
+            mma_16816(dk[2], w[1], w[0][0], w[0][2]);
+            mma_16816(dk[3], w[1], w[0][1], w[0][3]);
+            mma_16816(dk[4], w[1], w[1][0], w[1][2]);
+            mma_16816(dk[5], w[1], w[1][1], w[1][3]);
+            mma_16816(dq[0], w[2], w[0][0], w[0][2]);
+            mma_16816(dq[1], w[2], w[0][1], w[0][3]);
+            mma_16816(dq[2], w[3], w[0][0], w[0][2]);
+            mma_16816(dq[3], w[3], w[0][1], w[0][3]);
+            mma_16816(dq[4], w[3], w[1][0], w[1][2]);
+            mma_16816(dq[5], w[3], w[1][1], w[1][3]);
         }
-        __syncwarp();
-        float d[6][4] = {};
-        lower_products<DK, QK>(st + (QK ? L::Q : L::K), st + L::K, fr, fc, d);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float* r0 = raw + h * kSBlock + gq * kSStride + 8 * i + 2 * cq;
-                const float(&x)[4] = d[4 * h + i];
-                *reinterpret_cast<float2*>(r0) = make_float2(x[0], x[1]);
-                *reinterpret_cast<float2*>(r0 + 8 * kSStride) = make_float2(x[2], x[3]);
+                float* k0 = kk + h * kSBlock + gq * kSStride + 8 * i + 2 * cq;
+                float* q0 = qk + h * kSBlock + gq * kSStride + 8 * i + 2 * cq;
+                const float(&x)[4] = dk[4 * h + i];
+                const float(&y)[4] = dq[4 * h + i];
+                *reinterpret_cast<float2*>(k0) = make_float2(x[0], x[1]);
+                *reinterpret_cast<float2*>(k0 + 8 * kSStride) = make_float2(x[2], x[3]);
+                *reinterpret_cast<float2*>(q0) = make_float2(y[0], y[1]);
+                *reinterpret_cast<float2*>(q0 + 8 * kSStride) = make_float2(y[2], y[3]);
             }
         __syncwarp();
-        float* rb = raw + blk * kSBlock;
-        float m[16], gt[16];
+        // ---- A and P of the diagonal sub-blocks: D_tj is the lane's running product -------
+        float* ak = kk + blk * kSBlock;
+        const float* aq = qk + blk * kSBlock;
+        float kc[16], qc[16], gt[16], bt[16];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) m[t] = rb[t * kSStride + col];
+        for (int t = 0; t < 16; ++t) {
+            kc[t] = ak[t * kSStride + col];
+            qc[t] = aq[t * kSStride + col];
+        }
 #pragma unroll
-        for (int t = 0; t < 16; t += 4)
+        for (int t = 0; t < 16; t += 4) {
             *reinterpret_cast<float4*>(&gt[t]) = *reinterpret_cast<const float4*>(gs + 16 * blk + t);
-        float D = 0.f;   // zero above the diagonal; at the end the gates behind this column in its half
-        const float Q0 = __shfl_sync(0xffffffffu, Gh, 16 + gq), Q1 = __shfl_sync(0xffffffffu, Gh, 24 + gq);
-        if constexpr (QK) {
+            *reinterpret_cast<float4*>(&bt[t]) = *reinterpret_cast<const float4*>(vec + 16 * blk + t);
+        }
+        float d = 0.f;   // zero above the diagonal
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                D = t == col ? 1.f : D * gt[t];
-                st_shared_u16(st + L::P + (16 * blk + t) * kTStride + 2 * lane, __float2bfloat16_rn(t >= col ? D * m[t] : 0.f));
+        for (int t = 0; t < 16; ++t) {
+            d = t == col ? 1.f : d * gt[t];
+            kc[t] = t > col ? bt[t] * d * kc[t] : 0.f;
+            qc[t] = t >= col ? d * qc[t] : 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            ak[t * kSStride + col] = kc[t];
+            st_shared_u16(st + L::P + (16 * blk + t) * kTStride + 2 * lane, __float2bfloat16_rn(qc[t]));
+        }
+        vec[3 * C + lane] = blk ? d : d * G31;
+        __syncwarp();
+        // ---- their inverses by forward substitution ----------------------------------------
+        float x[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            float s0 = t == col ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int i = 0; i < t; i += 4) {
+                const float4 r = *reinterpret_cast<const float4*>(ak + t * kSStride + i);
+                s0 -= r.x * x[i];
+                if (i + 1 < t) s1 -= r.y * x[i + 1];
+                if (i + 2 < t) s2 -= r.z * x[i + 2];
+                if (i + 3 < t) s3 -= r.w * x[i + 3];
             }
+            x[t] = (s0 + s1) + (s2 + s3);
+        }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {   // the sub-block below the diagonal
-                const float S0 = __shfl_sync(0xffffffffu, D, 8 * i + 2 * cq), S1 = __shfl_sync(0xffffffffu, D, 8 * i + 2 * cq + 1);
-                const float(&y)[4] = d[2 + i];
-                st_shared_b32(st + L::P + (16 + gq) * kTStride + 16 * i + 4 * cq, pack_bf16(Q0 * S0 * y[0], Q0 * S1 * y[1]));
-                st_shared_b32(st + L::P + (24 + gq) * kTStride + 16 * i + 4 * cq, pack_bf16(Q1 * S0 * y[2], Q1 * S1 * y[3]));
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&ready[s]);
-                // the block after next but one goes where block c - kStages + 1 was, once the chain has left it
-                if (c + 1 >= kStages && c + 1 < it.blocks) {
-                    if (mbar_wait_or_abort(&empty[old.s], old.phase, abort_flag))
-                        issue_loads<DK>(tmq, tmk, tmv, it, sm, full, c + 1, old.s);
-                }
-            }
-            if (c + 1 >= kStages) old.next();
-            __syncwarp();
-        } else {
-            float bt[16];
-#pragma unroll
-            for (int t = 0; t < 16; t += 4)
-                *reinterpret_cast<float4*>(&bt[t]) = *reinterpret_cast<const float4*>(vec + 16 * blk + t);
-#pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                D = t == col ? 1.f : D * gt[t];
-                rb[t * kSStride + col] = t > col ? bt[t] * D * m[t] : 0.f;
-            }
-            vec[3 * C + lane] = blk ? D : D * G31;
-            __syncwarp();
-            // forward substitution: x = column `col` of the sub-block's inverse
-            float x[16];
-#pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                float s0 = t == col ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-                for (int i = 0; i < t; i += 4) {
-                    const float4 r = *reinterpret_cast<const float4*>(rb + t * kSStride + i);
-                    s0 -= r.x * x[i];
-                    if (i + 1 < t) s1 -= r.y * x[i + 1];
-                    if (i + 2 < t) s2 -= r.z * x[i + 2];
-                    if (i + 3 < t) s3 -= r.w * x[i + 3];
-                }
-                x[t] = (s0 + s1) + (s2 + s3);
-            }
-#pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(x[t]);
-                st_shared_u16(st + L::TH + (16 * blk + t) * kTStride + 2 * lane, hi);
-                st_shared_u16(st + L::TL + (16 * blk + t) * kTStride + 2 * lane, __float2bfloat16_rn(x[t] - __bfloat162float(hi)));
-            }
-            // the sub-block below: A21 from its product tiles
-            const float b0 = Q0 * __shfl_sync(0xffffffffu, b, 16 + gq), b1 = Q1 * __shfl_sync(0xffffffffu, b, 24 + gq);
+        for (int t = 0; t < 16; ++t) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(x[t]);
+            st_shared_u16(st + L::TH + (16 * blk + t) * kTStride + 2 * lane, hi);
+            st_shared_u16(st + L::TL + (16 * blk + t) * kTStride + 2 * lane, __float2bfloat16_rn(x[t] - __bfloat162float(hi)));
+        }
+        // ---- the sub-block below: P21 = Q S qk, A21 = b Q S kk (Q by token, S by column) --------
+        const float Q0 = __shfl_sync(0xffffffffu, Gq, 16 + gq), Q1 = __shfl_sync(0xffffffffu, Gq, 24 + gq);
+        const float b0 = __shfl_sync(0xffffffffu, b, 16 + gq), b1 = __shfl_sync(0xffffffffu, b, 24 + gq);
+        uint32_t ah[4], al[4];
+        {
+            float S[2][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float S0 = __shfl_sync(0xffffffffu, D, 8 * i + 2 * cq), S1 = __shfl_sync(0xffffffffu, D, 8 * i + 2 * cq + 1);
-                float(&z)[4] = d[2 + i];
-                z[0] *= b0 * S0;
-                z[1] *= b0 * S1;
-                z[2] *= b1 * S0;
-                z[3] *= b1 * S1;
+                S[i][0] = __shfl_sync(0xffffffffu, d, 8 * i + 2 * cq);
+                S[i][1] = __shfl_sync(0xffffffffu, d, 8 * i + 2 * cq + 1);
+                float(&y)[4] = dq[2 + i];
+                st_shared_b32(st + L::P + (16 + gq) * kTStride + 16 * i + 4 * cq, pack_bf16(Q0 * S[i][0] * y[0], Q0 * S[i][1] * y[1]));
+                st_shared_b32(st + L::P + (24 + gq) * kTStride + 16 * i + 4 * cq, pack_bf16(Q1 * S[i][0] * y[2], Q1 * S[i][1] * y[3]));
+                float(&z)[4] = dk[2 + i];
+                z[0] *= b0 * Q0 * S[i][0];
+                z[1] *= b0 * Q0 * S[i][1];
+                z[2] *= b1 * Q1 * S[i][0];
+                z[3] *= b1 * Q1 * S[i][1];
             }
-            uint32_t ah[4], al[4];
-            split_tiles(d[2], d[3], ah, al);
-            __syncwarp();
-            float M[2][4] = {}, N[2][4] = {};
-            {
-                uint32_t th[4], tl[4];   // T11 [k = s][n = j]
-                ldsm4t(th, st + L::TH + fr * kTStride + 16 * fc);
-                ldsm4t(tl, st + L::TL + fr * kTStride + 16 * fc);
-                mma_16816(M[0], ah, th[0], th[1]);
-                mma_16816(M[1], ah, th[2], th[3]);
-                mma_16816(M[0], al, th[0], th[1]);
-                mma_16816(M[1], al, th[2], th[3]);
-                mma_16816(M[0], ah, tl[0], tl[1]);
-                mma_16816(M[1], ah, tl[2], tl[3]);
-            }
-            {
-                uint32_t th[4], tl[4], mh[4], ml[4];   // T22 [t][s]; M [k = s][n = j], transposed between lanes
-                ldsm4(th, st + L::TH + (16 + fr) * kTStride + 32 + 16 * fc);
-                ldsm4(tl, st + L::TL + (16 + fr) * kTStride + 32 + 16 * fc);
-                split_tiles(M[0], M[1], mh, ml);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mh[i] = transpose8x8(mh[i]);
-                    ml[i] = transpose8x8(ml[i]);
-                }
-                mma_16816(N[0], th, mh[0], mh[1]);
-                mma_16816(N[1], th, mh[2], mh[3]);
-                mma_16816(N[0], tl, mh[0], mh[1]);
-                mma_16816(N[1], tl, mh[2], mh[3]);
-                mma_16816(N[0], th, ml[0], ml[1]);
-                mma_16816(N[1], th, ml[2], ml[3]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t hi, lo;
-                    split2(-N[i][2 * h], -N[i][2 * h + 1], hi, lo);
-                    st_shared_b32(st + L::TH + (16 + 8 * h + gq) * kTStride + 16 * i + 4 * cq, hi);
-                    st_shared_b32(st + L::TL + (16 + 8 * h + gq) * kTStride + 16 * i + 4 * cq, lo);
-                }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ready[s]);
+            split_tiles(dk[2], dk[3], ah, al);
         }
+        __syncwarp();
+        float M[2][4] = {}, N[2][4] = {};
+        {
+            uint32_t th[4], tl[4];   // T11 [k = s][n = j]
+            ldsm4t(th, st + L::TH + fr * kTStride + 16 * fc);
+            ldsm4t(tl, st + L::TL + fr * kTStride + 16 * fc);
+            mma_16816(M[0], ah, th[0], th[1]);
+            mma_16816(M[1], ah, th[2], th[3]);
+            mma_16816(M[0], al, th[0], th[1]);
+            mma_16816(M[1], al, th[2], th[3]);
+            mma_16816(M[0], ah, tl[0], tl[1]);
+            mma_16816(M[1], ah, tl[2], tl[3]);
+        }
+        {
+            uint32_t th[4], tl[4], mh[4], ml[4];   // T22 [t][s]; M [k = s][n = j], transposed between lanes
+            ldsm4(th, st + L::TH + (16 + fr) * kTStride + 32 + 16 * fc);
+            ldsm4(tl, st + L::TL + (16 + fr) * kTStride + 32 + 16 * fc);
+            split_tiles(M[0], M[1], mh, ml);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mh[i] = transpose8x8(mh[i]);
+                ml[i] = transpose8x8(ml[i]);
+            }
+            mma_16816(N[0], th, mh[0], mh[1]);
+            mma_16816(N[1], th, mh[2], mh[3]);
+            mma_16816(N[0], tl, mh[0], mh[1]);
+            mma_16816(N[1], tl, mh[2], mh[3]);
+            mma_16816(N[0], th, ml[0], ml[1]);
+            mma_16816(N[1], th, ml[2], ml[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t hi, lo;
+                split2(-N[i][2 * h], -N[i][2 * h + 1], hi, lo);
+                st_shared_b32(st + L::TH + (16 + 8 * h + gq) * kTStride + 16 * i + 4 * cq, hi);
+                st_shared_b32(st + L::TL + (16 + 8 * h + gq) * kTStride + 16 * i + 4 * cq, lo);
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ready[s]);
     }
 }
 
@@ -365,16 +321,18 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BAR);   // [kStages] TMA: a block's tiles have arrived
-    uint64_t* ready = full + kStages;                            // [kStages] prep warps: T, P and vectors are written
-    uint64_t* empty = ready + kStages;                           // [kStages] chain warps: the stage is read
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + kStages);
+    uint64_t* ready = full + kStages;                            // [kStages] prep: T, P and vectors are written
+    int* left = reinterpret_cast<int*>(ready + kStages);         // [kStages] chain warps that have left the stage
+    volatile int* issued = left + kStages;                       // blocks whose loads were issued
+    volatile int* abort_flag = left + kStages + 1;
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&ready[i], kPrep);
-            mbar_init(&empty[i], kChain);
+            mbar_init(&ready[i], 1);
+            left[i] = 0;
         }
+        *issued = 0;
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmq);
@@ -395,11 +353,24 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     }
     __syncthreads();
 
+    auto issue = [&](int c) {   // loads of block c (one thread); rows past the tensor read as zeros
+        const int s = c % kStages, row = it.rq.row0 + c * C;
+        uint8_t* st = sm + s * L::STAGE;
+        mbar_arrive_expect_tx(&full[s], L::TX);
+#pragma unroll
+        for (int x = 0; x < L::KA; ++x) {
+            tma_load_3d(&tmk, &full[s], st + L::K + x * 4096, x * 64, it.khead, row);
+            tma_load_3d(&tmq, &full[s], st + L::Q + x * 4096, x * 64, it.khead, row);
+        }
+        tma_load_3d(&tmv, &full[s], st + L::V, it.split * kRows, it.head, row);
+        *issued = c + 1;
+    };
+    if (tid == 0)
+        for (int c = 0; c < kStages && c < it.blocks; ++c) issue(c);
+
     bool failed = false;
-    if (warp == kChain) {
-        prep_warp<DK, false>(&tmq, &tmk, &tmv, a, it, sm, sbase, full, ready, empty, abort_flag);
-    } else if (warp > kChain) {
-        prep_warp<DK, true>(&tmq, &tmk, &tmv, a, it, sm, sbase, full, ready, empty, abort_flag);
+    if (warp >= kChain) {
+        prep_warp<DK>(a, it, sm, sbase, warp - kChain, full, ready, abort_flag);
     } else {
         // ======================= chain warp: rows r0 + g and r0 + g + 8 ====================
         const int gq = lane >> 2, cq = lane & 3;
@@ -439,11 +410,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             }
         };
 
-        Ring at;
-        for (int c = 0; c < it.blocks; ++c, at.next()) {
-            const int s = at.s;
+        for (int c = 0; c < it.blocks; ++c) {
+            const int s = c % kStages;
+            const uint32_t ph = (c / kStages) & 1;
             const uint32_t st = sbase + s * L::STAGE;
-            const bool ok = mbar_wait_or_abort(&full[s], at.phase, abort_flag) && mbar_wait_or_abort(&ready[s], at.phase, abort_flag);
+            bool ok = mbar_wait_or_abort(&full[s], ph, abort_flag) && mbar_wait_or_abort(&ready[s], ph, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) {
                 failed = true;
                 break;
@@ -600,8 +571,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 mma_16816(X[n], l1, b1[0], b1[1]);
                 mma_16816(X[n + 1], l1, b1[2], b1[3]);
             }
+            // this warp has read the stage: the last one to say so reloads it
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);   // this warp has read the stage
+            if (lane == 0) {
+                int before;
+                asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(&left[s])) : "memory");
+                if (before == kChain - 1 && c + kStages < it.blocks) {
+                    left[s] = 0;
+                    issue(c + kStages);
+                }
+            }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 Y[n][0] = pack_bf16(O[n][0], O[n][1]);
@@ -623,13 +602,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             atomicOr(a.status, kStatusTmaWait);
         }
     }
-    // After a failure loads may be in flight: let them land before the CTA
-    // leaves (bounded: a phase that was never begun runs into the limit).
-    if (__syncthreads_or(failed) && tid == 0)
-        for (int i = 0; i < kStages; ++i) {
-            mbar_wait(&full[i], 0, 20000000ull);
-            mbar_wait(&full[i], 1, 20000000ull);
-        }
+    if (failed) {   // let the loads in flight land before the CTA leaves (bounded)
+        if (lane == 0)
+            for (int c = max(0, *issued - kStages); c < *issued; ++c)
+                mbar_wait(&full[c % kStages], (c / kStages) & 1, 100000000ull);
+    }
 }
 
 template <int DK>

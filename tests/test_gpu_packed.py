@@ -118,6 +118,21 @@ def test_plan_faults_drop_the_request_alone(name, args, faults):
     assert want["counts"][3] == faults
 
 
+@pytest.mark.parametrize("name,args,faults", [
+    ("outside", ([1, 1, -1, 2], [0, 1, 1, 7], [60000, -2, 60000, 59999], [0, 1], 2), la.LA_PLAN_FAULT_SLOT),
+    ("claimed twice", ([1, 1, 1], [1, 1, 1], [2, 2, 2], [0, 1, 3], 3), la.LA_PLAN_FAULT_OWNER),
+    ("given back twice", ([-1, -1, 1], [1, 1, 1], [2, 2, 2], [0, 1, 3], 3), la.LA_PLAN_FAULT_OWNER),
+    ("free and owned", ([1, 4], [0, 3], [-1, 2], [0, 2], 2), la.LA_PLAN_FAULT_OWNER),
+    ("free twice", ([1, 4], [0, 0], [-1, -1], [3, 3], 2), la.LA_PLAN_FAULT_OWNER),
+    ("back and taken", ([-1, 3, 2], [5, 0, 0], [59999, -1, -1], [7], 1), 0),
+])
+def test_plan_of_a_pool_whose_claims_do_not_fit_shared_memory(name, args, faults):
+    pool = 60000
+    lengths, seen, slots, free, count = args
+    c = PlanCase(lengths, seen, slots, free + [0] * (pool - len(free)), count, pool, 10)
+    assert c.check(c.run())["counts"][3] == faults
+
+
 # ------------------------------------------------------------------ the rule
 
 def handle_for(lens, Hk, Hv, dk, dv, io, pool, extra_rows=0):
