@@ -6,16 +6,25 @@
 //   u_i = beta (v_i - g S_i . k),   S_i = g S_i + u_i k,
 //   o_i = S_i . q = g (old S_i . q) + u_i (k . q)
 //
-// A warp owns a unit of state rows of one request's head: the rows are read
-// once, stay in registers over all the request's tokens and are written once,
-// so a one-token step moves each state once in and once out and HBM bounds
-// it; a request without tokens seen starts from zeros and reads nothing.
-// Each lane holds four consecutive columns of a row, as a 16-byte vector. The
-// two products S k and S q of the unit's eight row passes are summed over the
-// lanes together, by halving: each exchange sends the half of the partial sums
-// that the partner keeps, 17 shuffles for 16 sums where one by one would take
-// 80; the lane that ends up with S_i . k computes u_i. The next token's
-// vectors are loaded before the current one is used.
+// A warp owns a unit of state rows (4 KB) of one request's head: the rows are
+// read once, stay in registers over all the request's tokens and are written
+// once, so a one-token step moves each state once in and once out and HBM
+// bounds it; a request without tokens seen starts from zeros and reads nothing.
+// Eight lanes share a row (four at d_k 16), each with every eighth 16-byte
+// vector of it, so that a few tokens cost little besides: at d_k 128 four sums
+// over eight lanes where 32 lanes to a row would have sixteen over 32. The two
+// products S k and S q of a unit's row passes are summed over the lanes
+// together, by halving: each exchange sends the half of the partial sums that
+// the partner keeps; the lane that ends up with S_i . k computes u_i. The next
+// token's vectors are loaded before the current one is used.
+//
+// Measured, d 128, 16 heads, bf16: one token of 256 requests 83 us, 0.96 of the
+// measured copy bandwidth; of 4 requests 3.5 us, the launch and two trips to
+// memory; 400 tokens of 128 requests 53 us, 0.75 of it:
+// there the tokens' arithmetic, about 9 us a token, is in part beside the
+// traffic and in part before it. Tried and slower: the next unit's state into
+// shared memory (256 requests 90 us) or L2 (98 us) while one is computed; three
+// CTAs per SM at 80 registers (89 us).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -28,189 +37,252 @@ namespace packed {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPasses = 8;   // row passes of a unit: 16-byte loads in flight per lane
+constexpr int kVectors = 8;   // 16-byte vectors of the state per lane: loads in flight
 
-template <typename IO> __device__ __forceinline__ float4 ld4(const IO* p);
-template <> __device__ __forceinline__ float4 ld4<float>(const float* p) {
-    return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <> __device__ __forceinline__ float4 ld4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    const float2 a = unpack_bf16(u.x), b = unpack_bf16(u.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
+// Four elements as they are loaded, and as numbers.
+template <typename IO> struct Raw;
+template <> struct Raw<float> {
+    float4 u;
+    __device__ __forceinline__ void load(const float* p) { u = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ float4 get() const { return u; }
+};
+template <> struct Raw<__nv_bfloat16> {
+    uint2 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ float4 get() const {
+        const float2 a = unpack_bf16(u.x), b = unpack_bf16(u.y);
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+};
 __device__ __forceinline__ float ld1(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float ld1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void st1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void st1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
-
-// Sum of x over the W consecutive lanes of a group, in every lane.
-template <int W>
-__device__ __forceinline__ float group_sum(float x) {
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+// Two fp32 values in one register pair: one instruction for two multiply-adds.
+using Pair = unsigned long long;
+struct __align__(16) Pairs {   // four consecutive columns
+    Pair a, b;
+};
+__device__ __forceinline__ Pairs pairs(float4 x) {
+    Pairs y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y.a) : "f"(x.x), "f"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y.b) : "f"(x.z), "f"(x.w));
+    return y;
+}
+__device__ __forceinline__ Pair both(float x) {
+    Pair y;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ Pair fma2(Pair x, Pair y, Pair z) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair x, Pair y) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ float sum(Pair x) {
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+    return lo + hi;
 }
 
-// x[i] summed over the W lanes of a group, i < 16. By halving while there is
-// more than one value: lane l ends with the sum of value l * 16 / W (W 16 or 32).
-template <int W>
-__device__ __forceinline__ float sums_by_halving(float (&x)[16], int lane) {
-    int o = W / 2;
+// x[i] summed over the W lanes of a group, i < N. By halving while there is
+// more than one value: lane l ends with the sums of values l N / W ..
+template <int N, int W>
+__device__ __forceinline__ void sums_by_halving(float (&x)[N], int lane) {
+    int n = N / 2;
 #pragma unroll
-    for (int n = 8; n > 0; n >>= 1, o >>= 1) {
-        const bool up = lane & o;
+    for (int o = W / 2; o > 0; o >>= 1) {
+        if (n > 0) {
+            const bool up = lane & o;
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float keep = up ? x[i + n] : x[i], send = up ? x[i] : x[i + n];
-            x[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            for (int i = 0; i < n; ++i) {
+                const float keep = up ? x[i + n] : x[i], send = up ? x[i] : x[i + n];
+                x[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+            n /= 2;
+        } else {
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
         }
     }
-    if (W == 32) x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
-    return x[0];
+}
+
+// How a warp holds a unit: lane (sub, cl) has vectors cl, cl + LPR, ... of rows p RPP + sub.
+template <int DK>
+struct Unit {
+    static constexpr int LPR = DK >= 32 ? 8 : 4;      // lanes per row
+    static constexpr int V = DK / (4 * LPR);          // vectors of a row per lane
+    static constexpr int P = kVectors / V;            // row passes
+    static constexpr int RPP = 32 / LPR;              // rows per pass
+    static constexpr int R = RPP * P;                 // rows
+    static constexpr int Q = LPR / 2;                 // lanes that end with S k (the lower half of a row's), with S q
+    static constexpr int M = P >= Q ? P / Q : 1;      // passes whose sums a lane ends with,
+    static constexpr int DUP = P >= Q ? 1 : Q / P;    // or lanes that end with the same
+    Pairs S[P][V];
+    int sub, cl, pass0;
+    bool upper;
+
+    __device__ __forceinline__ explicit Unit(int lane)
+        : sub(lane / LPR), cl(lane % LPR), pass0(lane % LPR % Q / DUP * M), upper(lane % LPR >= Q) {}
+    // row of the unit whose u (i < M) this lane computes
+    __device__ __forceinline__ int own_row(int i) const { return (pass0 + i) * RPP + sub; }
+
+    // One token: the state's update and the outputs of the unit's `rows` rows.
+    template <typename IO>
+    __device__ __forceinline__ void step(const Pairs (&k4)[V], const Pairs (&q4)[V], const float (&v)[M], float g, float b,
+                                         IO* out, int rows) {
+        Pair kq2 = mul2(k4[0].a, q4[0].a);
+        kq2 = fma2(k4[0].b, q4[0].b, kq2);
+#pragma unroll
+        for (int w = 1; w < V; ++w) kq2 = fma2(k4[w].b, q4[w].b, fma2(k4[w].a, q4[w].a, kq2));
+        float kq = sum(kq2), d[2 * P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            Pair x = fma2(S[p][0].b, k4[0].b, mul2(S[p][0].a, k4[0].a)), y = fma2(S[p][0].b, q4[0].b, mul2(S[p][0].a, q4[0].a));
+#pragma unroll
+            for (int w = 1; w < V; ++w) {
+                x = fma2(S[p][w].b, k4[w].b, fma2(S[p][w].a, k4[w].a, x));
+                y = fma2(S[p][w].b, q4[w].b, fma2(S[p][w].a, q4[w].a, y));
+            }
+            d[p] = sum(x);
+            d[P + p] = sum(y);
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, o);
+        sums_by_halving<2 * P, LPR>(d, cl);
+        float u[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, d[i], Q);
+            const float sk = upper ? other : d[i], sq = upper ? d[i] : other;
+            u[i] = b * (v[i] - g * sk);
+            if (!upper && cl % DUP == 0 && own_row(i) < rows) st1(out + own_row(i), g * sq + u[i] * kq);
+        }
+        const Pair g2 = both(g);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const Pair c = both(__shfl_sync(0xffffffffu, u[p % M], sub * LPR + p / M * DUP));
+#pragma unroll
+            for (int w = 0; w < V; ++w) {
+                S[p][w].a = fma2(c, k4[w].a, mul2(g2, S[p][w].a));
+                S[p][w].b = fma2(c, k4[w].b, mul2(g2, S[p][w].b));
+            }
+        }
+    }
+    // The unit's rows to or from memory (vectors cl + LPR w of row p RPP + sub of `st`)
+    __device__ __forceinline__ size_t at(int p, int w) const { return static_cast<size_t>(p * RPP + sub) * DK + 4 * (cl + LPR * w); }
+    __device__ __forceinline__ void load(const float* st, int rows) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int w = 0; w < V; ++w)
+                S[p][w] = pairs(p * RPP + sub < rows ? __ldcs(reinterpret_cast<const float4*>(st + at(p, w))) : make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    __device__ __forceinline__ void store(float* st, int rows) const {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int w = 0; w < V; ++w)
+                if (p * RPP + sub < rows) __stcs(reinterpret_cast<ulonglong2*>(st + at(p, w)), make_ulonglong2(S[p][w].a, S[p][w].b));
+    }
+};
+
+// What a unit reads and writes.
+template <typename IO>
+struct Where {
+    const IO *q, *k, *v;
+    const float *gate, *beta;
+    float* st;
+    IO* out;
+    int len, rows;   // tokens; rows of the unit
+    bool fresh;
+};
+// Unit u; false if its request has no part.
+template <int DK, typename IO>
+__device__ __forceinline__ bool find(const StepArgs& a, int u, Where<IO>& x) {
+    constexpr int R = Unit<DK>::R;
+    const int uph = (a.dv + R - 1) / R, per_req = a.Hv * uph;   // units per head, per request
+    const int hu = u % per_req, h = hu / uph, r0 = hu % uph * R, hk = h / (a.Hv / a.Hk);
+    Request rq;
+    if (!read_request(a, u / per_req, rq)) return false;
+    const size_t row = static_cast<size_t>(rq.row0);
+    x.q = static_cast<const IO*>(a.q) + row * a.q_stride + hk * DK;
+    x.k = static_cast<const IO*>(a.k) + row * a.k_stride + hk * DK;
+    x.v = static_cast<const IO*>(a.v) + row * a.v_stride + static_cast<size_t>(h) * a.dv + r0;
+    x.gate = a.gate + row * a.Hv + h;
+    x.beta = a.beta + row * a.Hv + h;
+    x.st = a.states + ((static_cast<size_t>(rq.slot) * a.Hv + h) * a.dv + r0) * DK;
+    x.out = static_cast<IO*>(a.out) + (row * a.Hv + h) * a.dv + r0;
+    x.len = rq.len;
+    x.rows = min(R, a.dv - r0);
+    x.fresh = rq.fresh;
+    return true;
+}
+template <int DK>
+__host__ __device__ inline int unit_count(const StepArgs& a) {   // at most 2^14 requests x 2^12 heads x 2^4
+    return a.requests * a.Hv * ((a.dv + Unit<DK>::R - 1) / Unit<DK>::R);
 }
 
 template <int DK, typename IO>
-__global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
-    constexpr int LPR = DK / 4;          // lanes per row
-    constexpr int RPP = 32 / LPR;        // rows per pass
-    constexpr int R = RPP * kPasses;     // rows per unit
-    constexpr bool HALVING = LPR >= 16;
-    const int dv = a.dv;
-    const int uph = (dv + R - 1) / R;    // units per head
-    const int lane = threadIdx.x & 31;
-    const int sub = lane / LPR, cl = lane % LPR;
-    // by halving: the row pass whose sums this lane holds, and whether it
-    // holds S k (lower half of the group) or S q
-    const int myp = (cl * 16 / LPR) & 7;
-    const bool upper = cl >= LPR / 2;
-    const long long warp0 = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    const long long nwarps = (static_cast<long long>(gridDim.x) * kThreads) >> 5;
-    const IO* q = static_cast<const IO*>(a.q);
-    const IO* k = static_cast<const IO*>(a.k);
-    const IO* v = static_cast<const IO*>(a.v);
-    IO* out = static_cast<IO*>(a.out);
-
+__global__ void __launch_bounds__(kThreads, 2) step_kernel(const StepArgs a) {
+    using U = Unit<DK>;
+    U s(threadIdx.x & 31);
     griddep_launch_dependents();
     griddep_wait();   // the plan and the states of the step before are complete
-    const int per_req = a.Hv * uph;
-    const long long units = static_cast<long long>(a.requests) * per_req;
-    for (long long u = warp0; u < units; u += nwarps) {
-        const int r = static_cast<int>(u / per_req);
-        const int hu = static_cast<int>(u % per_req);
-        const int h = hu / uph, r0 = (hu % uph) * R;
-        const int hk = h / (a.Hv / a.Hk);
-        Request x;
-        if (!read_request(a, r, x)) continue;
-        float* st = a.states + (static_cast<size_t>(x.slot) * a.Hv + h) * dv * DK;
-        float4 S[kPasses];
+    const int units = unit_count<DK>(a), stride = (gridDim.x * kThreads) >> 5;
+    for (int u = (blockIdx.x * kThreads + threadIdx.x) >> 5; u < units; u += stride) {
+        Where<IO> x;
+        if (!find<DK>(a, u, x)) continue;
+        s.load(x.st, x.fresh ? 0 : x.rows);
+        Raw<IO> kn[U::V], qn[U::V];   // of the next token
+        float vn[U::M], gn, bn;
+        auto load = [&]() {
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            const int row = r0 + p * RPP + sub;
-            S[p] = (!x.fresh && row < dv) ? __ldcs(reinterpret_cast<const float4*>(st + static_cast<size_t>(row) * DK) + cl)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        const IO* qp = q + static_cast<size_t>(x.row0) * a.q_stride + hk * DK + 4 * cl;
-        const IO* kp = k + static_cast<size_t>(x.row0) * a.k_stride + hk * DK + 4 * cl;
-        const IO* vp = v + static_cast<size_t>(x.row0) * a.v_stride + static_cast<size_t>(h) * dv + r0;
-        const float* gp = a.gate + static_cast<size_t>(x.row0) * a.Hv + h;
-        const float* bp = a.beta + static_cast<size_t>(x.row0) * a.Hv + h;
-        IO* op = out + (static_cast<size_t>(x.row0) * a.Hv + h) * dv + r0;
-        const int myrow = myp * RPP + sub;   // row of the unit whose u this lane computes
-        const bool mine = r0 + myrow < dv;
-        auto load_v = [&](const IO* p, float (&w)[HALVING ? 1 : kPasses]) {
-            if (HALVING) {
-                w[0] = mine ? ld1(p + myrow) : 0.f;
-            } else {
-#pragma unroll
-                for (int i = 0; i < (HALVING ? 1 : kPasses); ++i)
-                    w[i] = r0 + i * RPP + sub < dv ? ld1(p + i * RPP + sub) : 0.f;
+            for (int w = 0; w < U::V; ++w) {
+                kn[w].load(x.k + 4 * (s.cl + U::LPR * w));
+                qn[w].load(x.q + 4 * (s.cl + U::LPR * w));
             }
-        };
-        float4 kn = ld4(kp), qn = ld4(qp);
-        float vn[HALVING ? 1 : kPasses];
-        load_v(vp, vn);
-        float gn = __ldg(gp), bn = __ldg(bp);
-        for (int t = 0; t < x.len; ++t) {
-            const float4 k4 = kn, q4 = qn;
-            float vr[HALVING ? 1 : kPasses];
 #pragma unroll
-            for (int i = 0; i < (HALVING ? 1 : kPasses); ++i) vr[i] = vn[i];
+            for (int i = 0; i < U::M; ++i) vn[i] = s.own_row(i) < x.rows ? ld1(x.v + s.own_row(i)) : 0.f;
+            gn = __ldg(x.gate);
+            bn = __ldg(x.beta);
+        };
+        load();
+        for (int t = 0; t < x.len; ++t) {
+            Pairs k4[U::V], q4[U::V];
+            float v[U::M];
+#pragma unroll
+            for (int w = 0; w < U::V; ++w) {
+                k4[w] = pairs(kn[w].get());
+                q4[w] = pairs(qn[w].get());
+            }
+#pragma unroll
+            for (int i = 0; i < U::M; ++i) v[i] = vn[i];
             const float g = gn, b = bn;
             if (t + 1 < x.len) {
-                kp += a.k_stride;
-                qp += a.q_stride;
-                vp += a.v_stride;
-                gp += a.Hv;
-                bp += a.Hv;
-                kn = ld4(kp);
-                qn = ld4(qp);
-                load_v(vp, vn);
-                gn = __ldg(gp);
-                bn = __ldg(bp);
+                x.k += a.k_stride;
+                x.q += a.q_stride;
+                x.v += a.v_stride;
+                x.gate += a.Hv;
+                x.beta += a.Hv;
+                load();
             }
-            const float kq = group_sum<LPR>(dot4(k4, q4));
-            if constexpr (HALVING) {
-                float d[16];
-#pragma unroll
-                for (int p = 0; p < kPasses; ++p) {
-                    d[p] = dot4(S[p], k4);
-                    d[8 + p] = dot4(S[p], q4);
-                }
-                const float s0 = sums_by_halving<LPR>(d, cl);
-                const float s1 = __shfl_xor_sync(0xffffffffu, s0, LPR / 2);
-                const float sk = upper ? s1 : s0, sq = upper ? s0 : s1;
-                const float ui = b * (vr[0] - g * sk);
-                if (!upper && mine && (LPR == 16 || !(cl & 1))) st1(op + myrow, g * sq + ui * kq);
-#pragma unroll
-                for (int p = 0; p < kPasses; ++p) {
-                    const float w = __shfl_sync(0xffffffffu, ui, sub * LPR + p * (LPR / 16));
-                    S[p].x = g * S[p].x + w * k4.x;
-                    S[p].y = g * S[p].y + w * k4.y;
-                    S[p].z = g * S[p].z + w * k4.z;
-                    S[p].w = g * S[p].w + w * k4.w;
-                }
-            } else {
-#pragma unroll
-                for (int p = 0; p < kPasses; ++p) {
-                    const float sk = group_sum<LPR>(dot4(S[p], k4));
-                    const float sq = group_sum<LPR>(dot4(S[p], q4));
-                    const float w = b * (vr[HALVING ? 0 : p] - g * sk);
-                    S[p].x = g * S[p].x + w * k4.x;
-                    S[p].y = g * S[p].y + w * k4.y;
-                    S[p].z = g * S[p].z + w * k4.z;
-                    S[p].w = g * S[p].w + w * k4.w;
-                    if (cl == 0 && r0 + p * RPP + sub < dv) st1(op + p * RPP + sub, g * sq + w * kq);
-                }
-            }
-            op += static_cast<size_t>(a.Hv) * dv;
+            s.step(k4, q4, v, g, b, x.out, x.rows);
+            x.out += static_cast<size_t>(a.Hv) * a.dv;
         }
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            const int row = r0 + p * RPP + sub;
-            if (row < dv) __stcs(reinterpret_cast<float4*>(st + static_cast<size_t>(row) * DK) + cl, S[p]);
-        }
+        s.store(x.st, x.rows);
     }
 }
 
 template <int DK, typename IO>
 cudaError_t run(const StepArgs& a, cudaStream_t s) {
-    // persistent: as many CTAs as are resident at once, no more than there are units
-    static int per_sm = 0;
-    if (per_sm == 0) {
-        int n = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, step_kernel<DK, IO>, kThreads, 0) != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            n = 1;
-        }
-        per_sm = n;
-    }
-    constexpr int rows = 32 / (DK / 4) * kPasses;
-    const long long units = static_cast<long long>(a.requests) * a.Hv * ((a.dv + rows - 1) / rows);
-    long long grid = (units + kThreads / 32 - 1) / (kThreads / 32);
-    if (grid > static_cast<long long>(a.sm_count) * per_sm) grid = static_cast<long long>(a.sm_count) * per_sm;
-    return launch_pdl(step_kernel<DK, IO>, static_cast<unsigned>(grid), kThreads, 0, s, a);
+    // two CTAs per SM, each warp one unit after another
+    const long long grid = (unit_count<DK>(a) + kThreads / 32 - 1) / (kThreads / 32), most = 2ll * a.sm_count;
+    return launch_pdl(step_kernel<DK, IO>, static_cast<unsigned>(grid < most ? grid : most), kThreads, 0, s, a);
 }
 
 template <typename IO>
