@@ -459,6 +459,11 @@ class PackedHandle:
         self.device = dev
         self.dtype = torch.bfloat16 if io == "bf16" else torch.float32
         self.H_k, self.H_v, self.d_k, self.d_v, self.slots = H_k, H_v, d_k, d_v, slots
+        # what every call looks up: a step of a few tokens takes the GPU less time than its enqueueing takes the host
+        self._index, self._i32, self._f32 = dev.index, torch.int32, torch.float32
+        self._empty, self._cuda = torch.empty, torch.cuda
+        self._current_stream = torch._C._cuda_getCurrentRawStream   # the number in torch.cuda.current_stream(device)
+        self._lib = lib()
         self.cfg = la_packed_config(max_requests, max_tokens, slots, H_k, H_v, d_k, d_v,
                                     LA_BF16 if io == "bf16" else LA_FP32, 0, dev.index)
         h = ctypes.c_void_p()
@@ -484,18 +489,17 @@ class PackedHandle:
             raise LAError(rc, lib().la_packed_last_error(self._h).decode())
 
     def _stream(self, stream):
-        import torch
-        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+        return self._current_stream(self._index) if stream is None else stream.cuda_stream
 
     def _expect(self, name, t, shape, dtype):
-        if t.dtype is not dtype or t.device != self.device:
+        if t.dtype is not dtype or t.get_device() != self._index:
             raise ValueError(f"{name}: expected a {dtype} tensor on {self.device}")
         if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous shape {tuple(shape)}, got {tuple(t.shape)}")
 
     def _rows(self, name, t, tokens, heads, d):
         """A packed tensor's row stride in elements; heads and channels of a row lie together."""
-        if t.dtype is not self.dtype or t.device != self.device:
+        if t.dtype is not self.dtype or t.get_device() != self._index:
             raise ValueError(f"{name}: expected a {self.dtype} tensor on {self.device}")
         if t.shape != (tokens, heads, d):
             raise ValueError(f"{name}: expected shape {(tokens, heads, d)}, got {tuple(t.shape)}")
@@ -513,43 +517,49 @@ class PackedHandle:
         [requests], free_slots int32 [slots], free_count int32 [1]; slots and
         the free stack are updated in place. ``tokens``: rows of the step's
         packed tensors. Returns ``plan`` (a new one if None)."""
-        import torch
         if plan is None:
             plan = self.new_plan()
-        elif plan.words.numel() != self._words or plan.words.device != self.device:
-            raise ValueError("plan: made by a handle of another configuration or device")
+        else:
+            self._own(plan)
         requests = lengths.numel()
-        for name, t, n in (("lengths", lengths, requests), ("seen", seen, requests), ("slots", slots, requests),
-                           ("free_slots", free_slots, self.slots), ("free_count", free_count, 1)):
-            self._expect(name, t, (n,), torch.int32)
-        self._check(lib().la_packed_plan(self._h, lengths.data_ptr(), seen.data_ptr(), slots.data_ptr(),
-                                         free_slots.data_ptr(), free_count.data_ptr(), plan.words.data_ptr(), requests,
-                                         tokens, self._stream(stream)))
+        i32, expect = self._i32, self._expect
+        expect("lengths", lengths, (requests,), i32)
+        expect("seen", seen, (requests,), i32)
+        expect("slots", slots, (requests,), i32)
+        expect("free_slots", free_slots, (self.slots,), i32)
+        expect("free_count", free_count, (1,), i32)
+        self._check(self._lib.la_packed_plan(self._h, lengths.data_ptr(), seen.data_ptr(), slots.data_ptr(),
+                                             free_slots.data_ptr(), free_count.data_ptr(), plan.words.data_ptr(), requests,
+                                             tokens, self._stream(stream)))
         plan._set(requests, tokens)
         return plan
 
-    def _step(self, call, plan, q, k, v, gate, beta, states, out, stream, *more):
-        import torch
-        n = plan.tokens
-        if plan.words.numel() != self._words or plan.words.device != self.device:
+    def _own(self, plan):
+        if plan.words.numel() != self._words or plan.words.get_device() != self._index:
             raise ValueError("plan: made by a handle of another configuration or device")
+
+    def _step(self, call, plan, q, k, v, gate, beta, states, out, stream, *more):
+        n, hv, dv = plan.tokens, self.H_v, self.d_v
+        self._own(plan)
         qs = self._rows("q", q, n, self.H_k, self.d_k)
         ks = self._rows("k", k, n, self.H_k, self.d_k)
-        vs = self._rows("v", v, n, self.H_v, self.d_v)
-        self._expect("gate", gate, (n, self.H_v), torch.float32)
-        self._expect("beta", beta, (n, self.H_v), torch.float32)
-        self._expect("states", states, (self.slots, self.H_v, self.d_v, self.d_k), torch.float32)
-        if out is None:
-            if stream is None:
-                out = torch.empty((n, self.H_v, self.d_v), dtype=self.dtype, device=self.device)
-            else:
-                with torch.cuda.stream(stream):   # the memory belongs to the stream that writes it
-                    out = torch.empty((n, self.H_v, self.d_v), dtype=self.dtype, device=self.device)
+        vs = self._rows("v", v, n, hv, dv)
+        f32, expect = self._f32, self._expect
+        expect("gate", gate, (n, hv), f32)
+        expect("beta", beta, (n, hv), f32)
+        expect("states", states, (self.slots, hv, dv, self.d_k), f32)
+        if out is not None:
+            expect("out", out, (n, hv, dv), self.dtype)
+        elif stream is None:
+            out = self._empty((n, hv, dv), dtype=self.dtype, device=self.device)
         else:
-            self._expect("out", out, (n, self.H_v, self.d_v), self.dtype)
-        self._check(call(self._h, plan.words.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
-                         beta.data_ptr(), states.data_ptr(), out.data_ptr(), plan.requests, n, qs, ks, vs, *more,
-                         self._stream(stream)))
+            with self._cuda.stream(stream):   # the memory belongs to the stream that writes it
+                out = self._empty((n, hv, dv), dtype=self.dtype, device=self.device)
+        rc = call(self._h, plan.words.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
+                  beta.data_ptr(), states.data_ptr(), out.data_ptr(), plan.requests, n, qs, ks, vs, *more,
+                  self._stream(stream))
+        if rc != LA_OK:
+            self._check(rc)
         return out
 
     def forward(self, plan, q, k, v, gate, beta, states, *, chunk=0, out=None, stream=None):
@@ -558,12 +568,12 @@ class PackedHandle:
         H_v], states fp32 [slots, H_v, d_v, d_k] updated in place. Returns out
         [tokens, H_v, d_v]; rows of no request are not written. ``chunk``: 0
         the default, 1 token by token, 32 in blocks."""
-        return self._step(lib().la_packed_forward, plan, q, k, v, gate, beta, states, out, stream, chunk)
+        return self._step(self._lib.la_packed_forward, plan, q, k, v, gate, beta, states, out, stream, chunk)
 
     def decode_step(self, plan, q, k, v, gate, beta, states, *, out=None, stream=None):
         """The same for one or a few tokens per request: token by token, each
         state read and written once."""
-        return self._step(lib().la_packed_decode_step, plan, q, k, v, gate, beta, states, out, stream)
+        return self._step(self._lib.la_packed_decode_step, plan, q, k, v, gate, beta, states, out, stream)
 
     def last_launches(self) -> int:
         """Kernels the last call enqueued."""
