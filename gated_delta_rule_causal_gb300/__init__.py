@@ -567,7 +567,8 @@ class PackedHandle:
         v [tokens, H_v, d_v] (rows may be strided), gate, beta fp32 [tokens,
         H_v], states fp32 [slots, H_v, d_v, d_k] updated in place. Returns out
         [tokens, H_v, d_v]; rows of no request are not written. ``chunk``: 0
-        the default, 1 token by token, 32 in blocks."""
+        the default, 1 token by token, 32 or 64 (d_v 128) in blocks of so
+        many tokens."""
         return self._step(self._lib.la_packed_forward, plan, q, k, v, gate, beta, states, out, stream, chunk)
 
     def decode_step(self, plan, q, k, v, gate, beta, states, *, out=None, stream=None):

@@ -13,7 +13,7 @@
 namespace la {
 namespace packed {
 
-constexpr int kBlock = 32;            // tokens per block of the chunkwise form
+constexpr int kBlock = 32;            // tokens per block that a plan orders its requests by
 constexpr int kMaxRequests = 16384;   // the plan kernel keeps the offsets of all requests in shared memory
 constexpr int kMaxTokens = 1 << 24;
 

@@ -70,6 +70,19 @@ int check_config(const la_packed_config* c) {
     return LA_OK;
 }
 
+// Whether a step at d_v 128 takes blocks of 64 tokens on the tcgen05 tensor cores (packed_tc.cu, one CTA per SM)
+// instead of blocks of 32 by warp-level MMAs (packed_chunk.cu, two CTAs per head, two per SM). The former starts
+// later and has the higher throughput; the latter waits less between the steps of one request. Measured, 32 / 64:
+//   d_k 128, one request, 16 heads: 64 rows 7.4 / 10.5 us, 256 18.7 / 20.6, 512 34.9 / 33.5, 4096 260 / 215;
+//            32 requests, 16 heads: 256 rows 29.0 / 31.2, 512 33.2 / 31.5, 4096 120 / 100
+//   d_k 64, one request, 16 heads: 512 rows 24.8 / 29.9, 32768 (two) 695 / 764; 64 requests, 16 heads: 4096 rows
+//           53 / 56, 8192 78 / 77, 32768 235 / 208; 16 requests of one length, 16 heads: 8192 67 / 61, 32768 258 / 211
+bool blocks_of_64(const la_packed* h, int requests, int tokens) {
+    if (h->cfg.d_v != 128) return false;
+    if (h->cfg.d_k == 128) return tokens > 256;
+    return static_cast<long long>(tokens) * h->cfg.H_v >= 1 << 17 && static_cast<long long>(requests) * h->cfg.H_v >= h->sm_count;
+}
+
 int run_step(la_packed* h, const int* plan, const void* q, const void* k, const void* v, const float* gate,
              const float* beta, float* states, void* out, int requests, int tokens, long long q_stride,
              long long k_stride, long long v_stride, int chunk, void* cuda_stream) {
@@ -80,11 +93,13 @@ int run_step(la_packed* h, const int* plan, const void* q, const void* k, const 
     if (requests < 0 || tokens < 0) return fail(h, LA_ERR_INVALID_ARG, "requests and tokens must be >= 0");
     if (requests > c.max_requests || tokens > c.max_tokens)
         return fail(h, LA_ERR_INVALID_ARG, "requests or tokens above the handle's maxima");
-    if (chunk != 0 && chunk != 1 && chunk != la::packed::kBlock)
-        return fail(h, LA_ERR_UNSUPPORTED, "chunk must be 0 (default), 1 (recurrent) or 32");
+    if (chunk != 0 && chunk != 1 && chunk != 32 && chunk != 64)
+        return fail(h, LA_ERR_UNSUPPORTED, "chunk must be 0 (default), 1 (recurrent), 32 or 64");
     const bool blocks_ok = c.io == LA_BF16 && c.d_k >= 64 && c.d_v >= 64;
-    if (chunk == la::packed::kBlock && !blocks_ok)
-        return fail(h, LA_ERR_UNSUPPORTED, "chunk 32 needs bf16 io and d_k, d_v in {64, 128}");
+    if (chunk >= 32 && !blocks_ok)
+        return fail(h, LA_ERR_UNSUPPORTED, "chunk 32 and 64 need bf16 io and d_k, d_v in {64, 128}");
+    if (chunk == 64 && c.d_v != 128) return fail(h, LA_ERR_UNSUPPORTED, "chunk 64 needs d_v 128");
+    const int form = chunk ? chunk : !blocks_ok ? 1 : blocks_of_64(h, requests, tokens) ? 64 : 32;
     if (requests == 0 || tokens == 0) return LA_OK;
     const void* ptrs[] = {plan, q, k, v, gate, beta, states, out};
     const char* names[] = {"plan", "q", "k", "v", "gate", "beta", "states", "out"};
@@ -128,10 +143,10 @@ int run_step(la_packed* h, const int* plan, const void* q, const void* k, const 
     DeviceGuard g(c.device);
     if (!g.ok) return fail(h, LA_ERR_CUDA, "cannot select the handle's device");
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    const cudaError_t e = chunk == 1 || !blocks_ok ? la::packed::launch_step(a, s)
-                          : c.d_v == 128       ? la::packed::launch_tc(a, s, h->encode)
-                                               : la::packed::launch_chunk(a, s, h->encode);
-    if (e != cudaSuccess) return cuda_fail(h, e, chunk != 1 && blocks_ok ? "packed prefill launch" : "packed step launch");
+    const cudaError_t e = form == 1    ? la::packed::launch_step(a, s)
+                          : form == 32 ? la::packed::launch_chunk(a, s, h->encode)
+                                       : la::packed::launch_tc(a, s, h->encode);
+    if (e != cudaSuccess) return cuda_fail(h, e, form == 1 ? "packed step launch" : "packed prefill launch");
     h->last_launches = 1;
     return LA_OK;
 }

@@ -14,9 +14,11 @@
 // from its own prefix sum over the lengths (a few microseconds of redundant
 // work instead of a second launch that waits for the first).
 //
-// Bound by latency: the longest case (8192 requests, 262144 rows) reads and
-// writes 2.3 MB, 0.3 us at the memory's rate; the dependent steps of CTA 0
-// (loads, three block-wide sums, claims, the sort) take the time.
+// Bound by latency: 8192 requests and 262144 rows are 2.3 MB to read and write,
+// 0.3 us at the memory's rate; the dependent steps of CTA 0 (loads, claims, two
+// block-wide sums, the sort) take the time, some 13000 clocks for a few requests
+// and 40000 for 8192, whose steps one SM works through by 32 warps. Measured: 8
+// requests 6.5 us, 512 7.3 us, 8192 20.4 us.
 #include <climits>
 
 #include "kernels.h"

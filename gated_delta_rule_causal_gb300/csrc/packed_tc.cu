@@ -19,14 +19,25 @@
 // Sixteen warps convert between them: thread (row r, part cp) takes a quarter
 // of the columns of each product in row r. Two groups of four prep warps
 // compute T' and P of the blocks that follow; of the others one issues the
-// chain's MMAs, one loads K and Q, one copies the outputs out, and one fetches
-// the work, loads V and issues the prep warps' [K;Q] K^T.
+// chain's MMAs, one loads K and Q and issues the prep warps' [K;Q] K^T, one
+// copies the outputs out, and one fetches the work and loads V.
 //
 // The chain's steps depend on one another, so what bounds a request is their
 // latency: three products (Z, R T'^T, U' K) with a conversion after each. High
 // parts are published first, so that a product starts while the low ones are
 // still formed. V^T T'^T, Q X^T, the scaling of X by G_63 and of O by G, and the
 // outputs run in the gaps.
+//
+// Measured, bf16, d 128: two requests of 8192 tokens, 16 heads (32 CTAs): 427 us,
+// 3.3 us or 6400 clocks a block; 96 requests of 65536 tokens together, 16 heads:
+// 446 us; 16 of 8191, 32 heads: 130 us. Of a block's clocks MMAs take 2700 (the
+// tensor pipe is 34 % busy), the chain's conversions 2500; the prep of a block
+// takes 10000 to 12000, half of which two groups make good. Issue slots are 53 %
+// busy, and 8 % of the warps' waiting is for instructions: 84 KB of code in
+// which every role has its own loop, where code beyond 32 KB was measured to
+// come at 3 clocks an instruction when all of it is walked in turn. Smaller was
+// slower all the same, the long requests as before: waits as a function (64 to
+// 73 KB) 507 us, conversions too 518, MMAs by one rolled loop 909.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -421,16 +432,29 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
                 float x[16];
                 tmem_ld16(tlane + L::COL_G + 16 * c16, x);
                 tmem_ld_wait();
+                if (u < 2 || n < C) {
 #pragma unroll
-                for (int q4 = 3; q4 >= 0; --q4) {
-                    const float4 g4 = *reinterpret_cast<const float4*>(vec + 16 * c16 + 4 * q4);
-                    const float gl[4] = {g4.x, g4.y, g4.z, g4.w};
+                    for (int q4 = 3; q4 >= 0; --q4) {
+                        const float4 g4 = *reinterpret_cast<const float4*>(vec + 16 * c16 + 4 * q4);
+                        const float gl[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
-                    for (int i = 3; i >= 0; --i) {
-                        const int j = 4 * q4 + i;
-                        d = j == diag ? 1.f : d;
-                        x[j] = j <= lim ? d * x[j] : 0.f;
-                        d *= gl[i];   // the gate of column j itself comes before the columns left of it
+                        for (int i = 3; i >= 0; --i) {
+                            const int j = 4 * q4 + i;
+                            d = j == diag ? 1.f : d;
+                            x[j] = j <= lim ? d * x[j] : 0.f;
+                            d *= gl[i];   // the gate of column j itself comes before the columns left of it
+                        }
+                    }
+                } else {   // whole columns left of every diagonal element
+#pragma unroll
+                    for (int q4 = 3; q4 >= 0; --q4) {
+                        const float4 g4 = *reinterpret_cast<const float4*>(vec + 16 * c16 + 4 * q4);
+                        const float gl[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+                        for (int i = 3; i >= 0; --i) {
+                            x[4 * q4 + i] *= d;
+                            d *= gl[i];
+                        }
                     }
                 }
                 if (isP) {

@@ -84,7 +84,8 @@ def rule_by_blocks(q, k, v, g, b, X, C=32):
     kernel: X, R, T and U in two bf16 parts (each split off by H^2), the lower
     parts' product dropped (H^2), X of the output and P in one (H), sums of
     fp32 products (64 F covers the longest, 128 terms by eight accumulations
-    of 16, with the decay products and the inverse's 32 steps)."""
+    of 16, with the decay products and the inverse's 32 or 64
+    steps)."""
     T = len(g)
     o, bo, E = np.zeros((T, v.shape[1])), np.zeros((T, v.shape[1])), 0.0
     e = H * H + 64 * F

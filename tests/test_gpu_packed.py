@@ -176,8 +176,9 @@ def make_plan(h, lens, seen, slots, rows=None):
     return h.plan(i32(lens), i32(seen), i32(slots), i32([0] * pool), i32([0]), tokens=sum(lens) if rows is None else rows)
 
 
-def check(x, lens, seen, states_before, out, io, by_blocks, only=None):
-    """Every request's outputs and state against the references; returns the largest share of a bound used."""
+def check(x, lens, seen, states_before, out, io, chunk, only=None):
+    """Every request's outputs and state against the references (chunk: 1, or the blocks' tokens); returns the largest
+    share of a bound used."""
     worst = 0.0
     d = lambda t: t.double().cpu().numpy()   # noqa: E731
     q, k, v, g, b = (d(x[n]) for n in ("q", "k", "v", "gate", "beta"))
@@ -191,7 +192,7 @@ def check(x, lens, seen, states_before, out, io, by_blocks, only=None):
                 hk = h * Hk // Hv
                 X0 = before[x["slots"][r], h] if seen[r] else np.zeros_like(before[0, 0])
                 args = (q[s, hk], k[s, hk], v[s, h], g[s, h], b[s, h], X0)
-                want, X, bo, E = ref.rule_by_blocks(*args) if by_blocks else ref.rule_by_tokens(
+                want, X, bo, E = ref.rule_by_blocks(*args, chunk) if chunk > 1 else ref.rule_by_tokens(
                     *args, ref.H if io == "bf16" else ref.F)
                 used = np.max(np.abs(o[s, h] - want) / (bo + 1e-30))
                 assert used <= 1.0, f"request {r} head {h}: output {used:.3g} of its bound"
@@ -206,17 +207,18 @@ LENS = [[1], [31, 1, 33], [64, 0, 65, 32], [130, 7, 0, 0, 97, 1], [513]]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=lambda x: "-".join(map(str, x)))
-@pytest.mark.parametrize("Hk,Hv,dk,dv", [(1, 1, 64, 64), (2, 4, 128, 128), (1, 3, 128, 64), (2, 2, 64, 128)])
-def test_prefill_by_blocks(lens, Hk, Hv, dk, dv):
+@pytest.mark.parametrize("Hk,Hv,dk,dv,chunk", [(1, 1, 64, 64, 32), (2, 4, 128, 128, 32), (1, 3, 128, 64, 32), (2, 2, 64, 128, 32),
+                                               (2, 4, 128, 128, 64), (2, 2, 64, 128, 64), (1, 2, 128, 128, 64)])
+def test_prefill_by_blocks(lens, Hk, Hv, dk, dv, chunk):
     x, pool = draw(lens, Hk, Hv, dk, dv, "bf16", seed=sum(lens) + dk, pad=8, extra_rows=3)
     h = handle_for(lens, Hk, Hv, dk, dv, "bf16", pool, extra_rows=3)
     seen = [r % 2 * 11 for r in range(len(lens))]
     plan = make_plan(h, lens, seen, x["slots"], rows=sum(lens) + 3)
     before = x["states"].clone()
     out = torch.full((sum(lens) + 3, Hv, dv), -7.5, device="cuda", dtype=torch.bfloat16)
-    h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], out=out, chunk=32)
+    h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], out=out, chunk=chunk)
     assert h.status() == la.LA_OK and h.last_launches() == 1
-    check(x, lens, seen, before, out, "bf16", True)
+    check(x, lens, seen, before, out, "bf16", chunk)
     # rows behind the last request, states of idle requests and of nobody: as they were
     assert out[sum(lens):].eq(-7.5).all()
     others = [s for s in range(pool) if s not in [x["slots"][r] for r, n in enumerate(lens) if n > 0]]
@@ -224,22 +226,22 @@ def test_prefill_by_blocks(lens, Hk, Hv, dk, dv):
 
 
 @pytest.mark.parametrize("gates", ["strong", "zero", "none"])
-@pytest.mark.parametrize("dk", [64, 128])
-def test_prefill_gates(gates, dk):
+@pytest.mark.parametrize("dk,dv,chunk", [(64, 64, 32), (128, 64, 32), (64, 128, 64), (128, 128, 64)])
+def test_prefill_gates(gates, dk, dv, chunk):
     lens = [70, 129]
-    x, pool = draw(lens, 1, 2, dk, 64, "bf16", seed=5, gates=gates)
+    x, pool = draw(lens, 1, 2, dk, dv, "bf16", seed=5, gates=gates)
     if gates == "none":   # the same key again and again, and its negative
         x["k"][:, 0] = x["k"][0, 0]
         x["k"][1::3, 0] *= -1
-    h = handle_for(lens, 1, 2, dk, 64, "bf16", pool)
+    h = handle_for(lens, 1, 2, dk, dv, "bf16", pool)
     plan = make_plan(h, lens, [0, 3], x["slots"])
     before = x["states"].clone()
-    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"])
+    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], chunk=chunk)
     assert h.status() == la.LA_OK
-    check(x, lens, [0, 3], before, out, "bf16", True)
+    check(x, lens, [0, 3], before, out, "bf16", chunk)
 
 
-@pytest.mark.parametrize("chunk", [1, 32])
+@pytest.mark.parametrize("chunk", [1, 32, 64])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_nothing_leaks_between_requests(bad, chunk):
     # requests 1 and 3 and the rows behind the last request hold NaN or infinities,
@@ -259,7 +261,7 @@ def test_nothing_leaks_between_requests(bad, chunk):
     before = x["states"].clone()
     out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], chunk=chunk)
     assert h.status() == la.LA_OK
-    check(x, lens, seen, before, out, "bf16", chunk == 32, only=(0, 2, 4))
+    check(x, lens, seen, before, out, "bf16", chunk, only=(0, 2, 4))
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
@@ -275,7 +277,7 @@ def test_token_by_token(io, dk, dv, lens):
     out = torch.full((sum(lens) + 2, Hv, dv), 3.25, device="cuda", dtype=h.dtype)
     h.decode_step(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], out=out)
     assert h.status() == la.LA_OK and h.last_launches() == 1
-    check(x, lens, seen, before, out, io, False)
+    check(x, lens, seen, before, out, io, 1)
     assert out[sum(lens):].eq(3.25).all()
     others = [s for s in range(pool) if s not in [x["slots"][r] for r, n in enumerate(lens) if n > 0]]
     assert torch.equal(x["states"][others], before[others])
@@ -308,7 +310,7 @@ def test_many_requests_and_heads():
     before = x["states"].clone()
     out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"])
     assert h.status() == la.LA_OK
-    check(x, lens, seen, before, out, "bf16", True, only=range(0, 150, 19))
+    check(x, lens, seen, before, out, "bf16", 64, only=range(0, 150, 19))
     # the same inputs again: the same bits
     again = before.clone()
     out2 = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], again)
@@ -362,12 +364,12 @@ def test_offsets_past_32_bits():
     plan = h.plan(i32([skip, n]), i32([4, 4]), i32([-1, slot]), i32([0] * pool), i32([0]), tokens=skip + n)
     assert plan.counts.tolist() == [skip + n, 1, 0, la.LA_PLAN_FAULT_STATE]
     out = torch.zeros(skip + n, Hv, d, device="cuda", dtype=torch.bfloat16)
-    for chunk in (32, 1):
+    for chunk in (64, 32, 1):
         states[slot] = start
         h.forward(plan, packed["q"], packed["k"], packed["v"], packed["gate"], packed["beta"], states, out=out, chunk=chunk)
         assert h.status() == la.LA_OK
         y = dict(x, states=states[slot:], slots=[0])
-        check(y, [n], [1], start[None], out[skip:], "bf16", chunk == 32)
+        check(y, [n], [1], start[None], out[skip:], "bf16", chunk)
         assert not out[:skip].any() and not states[:slot].any()
 
 
@@ -490,7 +492,7 @@ def test_a_stream_given_by_argument():
     plan = h.plan(*args, tokens=59, stream=st)
     out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], stream=st)
     assert h.status(stream=st) == la.LA_OK
-    check(x, lens, [1, 1], before, out, "bf16", True)
+    check(x, lens, [1, 1], before, out, "bf16", 32)
 
 
 # ------------------------------------------------------------------ refusals
@@ -557,13 +559,13 @@ def test_a_buffer_no_plan_was_made_in_reaches_nothing():
     # any words: the kernels take only what lies inside the tensors; here no word does
     lens = [40, 20]
     for words in (-1, 0, 2 ** 31 - 1, -2 ** 31, 1000):
-        x, pool = draw(lens, 1, 1, 64, 64, "bf16", seed=6)
-        h = handle_for(lens, 1, 1, 64, 64, "bf16", pool)
+        x, pool = draw(lens, 1, 1, 64, 128, "bf16", seed=6)
+        h = handle_for(lens, 1, 1, 64, 128, "bf16", pool)
         plan = make_plan(h, lens, [1, 1], x["slots"])
         plan.words.fill_(words)
         before = x["states"].clone()
-        out = torch.zeros(60, 1, 64, device="cuda", dtype=torch.bfloat16)
-        for f in (h.forward, h.decode_step):
-            f(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], out=out)
+        out = torch.zeros(60, 1, 128, device="cuda", dtype=torch.bfloat16)
+        for chunk in (1, 32, 64):
+            h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], out=out, chunk=chunk)
         assert h.status() == la.LA_OK
         assert not out.any() and torch.equal(before, x["states"])
