@@ -194,13 +194,13 @@ def host_cores() -> int:
 
 def kernel_source_hash() -> str:
     """sha1 (12 hex) of the CUDA sources of the forward and decode paths
-    (every file in csrc/ but the backward kernels, which none of the traffic
-    keys covers) and the C header."""
+    (every file in csrc/ but the backward and the packed kernels, which none
+    of the traffic keys covers) and the C header."""
     import glob
     import hashlib
     h = hashlib.sha1()
     files = sorted(f for f in glob.glob(os.path.join(ROOT, "gated_delta_rule_causal_gb300", "csrc", "*"))
-                   if not os.path.basename(f).startswith("backward"))
+                   if not os.path.basename(f).startswith(("backward", "packed", "warp_mma")))
     for f in files + [os.path.join(ROOT, "include", "la.h")]:
         with open(f, "rb") as fh:
             h.update(fh.read())
@@ -208,11 +208,12 @@ def kernel_source_hash() -> str:
 
 
 def all_source_hash() -> str:
-    """sha1 (12 hex) of every CUDA source and the C header."""
+    """sha1 (12 hex) of every CUDA source but the packed kernels', and the C header."""
     import glob
     import hashlib
     h = hashlib.sha1()
-    files = sorted(glob.glob(os.path.join(ROOT, "gated_delta_rule_causal_gb300", "csrc", "*")))
+    files = sorted(f for f in glob.glob(os.path.join(ROOT, "gated_delta_rule_causal_gb300", "csrc", "*"))
+                   if not os.path.basename(f).startswith(("packed", "warp_mma")))
     for f in files + [os.path.join(ROOT, "include", "la.h")]:
         with open(f, "rb") as fh:
             h.update(fh.read())
