@@ -80,6 +80,10 @@ struct StepArgs {
 };
 // Token by token, CUDA cores: any supported head size and type.
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
+// Whether every CTA of 32 state rows would have an SM to itself.
+inline bool chunk_is_alone(int requests, int Hv, int dv, int sm_count) {
+    return static_cast<long long>(requests) * Hv * (dv / 32) <= sm_count;
+}
 // In blocks of 32 tokens, warp-level MMAs: bf16, dk and dv in {64, 128}.
 cudaError_t launch_chunk(const StepArgs& a, cudaStream_t s, PFN_cuTensorMapEncodeTiled_v12000 enc);
 // In blocks of 64 tokens on the tcgen05 tensor cores: bf16, dk in {64, 128}, dv 128.

@@ -10,15 +10,18 @@
 // The decays are running products, never quotients or logarithms: any gate,
 // zero among them, gives what the recurrence gives.
 //
-// Work split. One CTA per (request, value head, 64 rows of the state), longest
-// requests first: rows of the state are independent. Four chain warps own 16
-// rows each, for the whole request. With X^T's products written as
+// Work split. One CTA per (request, value head, 64 or 32 rows of the state),
+// longest requests first: rows of the state are independent. Four chain warps
+// own 16 rows each, for the whole request. With X^T's products written as
 // [dv][token], a warp's accumulators (X, Z = X K^T, R, U) turn into the next
 // product's A operand inside its own registers, so from the state's load to
 // its store the chain exchanges nothing between warps. K, Q, V tiles come by
 // TMA into a ring of three stages; two prep warps compute T and P of a block
 // each, ahead of the chain. The last chain warp to leave a stage issues the
 // loads that reuse it.
+// Where there are no more CTAs of 32 rows than SMs, each has an SM to itself:
+// six stages, three prep warps, and two chain warps to 16 rows, half of the
+// channels each, who add up Z and O through shared memory.
 //
 // Precision. q, k, v are bf16 and enter the MMAs as they are. What the state
 // depends on (X in K X^T, R and T in T R, U in U^T K) is split into two bf16
@@ -30,10 +33,12 @@
 // Accumulators, gates, A and the inverse are fp32.
 //
 // Bound by latency: a block's products follow one another inside a warp, some
-// 2700 clocks for 110 MMAs of 8 each and their operands' splits at d_k 64.
-// Measured, 16 heads of d 64: one request of 130 tokens 9.7 us, of 2048 92 us
-// (1.4 us a block); nine of 2048 at d_k 128 137 us. Prep warps that took T and P
-// of every block instead of alternate blocks: 11.1 and 201 us.
+// 2500 clocks for 66 to 110 MMAs of 8 each and their operands' splits at d_k 64.
+// Measured, 16 heads: one request at d 64 of 130 tokens 8.3 us, of 2048 82 us
+// (1.3 us a block); at d_k 128, d_v 64 100 us; two of 8192 at d 128 399 us. By
+// CTAs of 64 rows: 9.7, 92, 131 and 511 us. Nine of 2048 at d_k 128, d_v 64 (64
+// rows): 136 us, and 201 us with prep warps that took T and P of every block
+// instead of alternate blocks.
 //
 // Rows past a request's end belong to the next request: they are zeroed in the
 // tiles before anything reads them, with gate 1 and beta 0, and are not
@@ -52,11 +57,6 @@ namespace packed {
 namespace {
 
 constexpr int C = 32;                      // tokens per block
-constexpr int kChain = 4;                  // chain warps: 16 state rows each
-constexpr int kRows = 16 * kChain;         // state rows of a CTA
-constexpr int kPrep = 2;                   // prep warps
-constexpr int kThreads = 32 * (kChain + kPrep);
-constexpr int kStages = 3;
 constexpr int kTStride = 80;               // bytes per row of a 32x32 bf16 tile: 16-byte chunks of 8 rows hit all banks
 // prep warps' fp32 scratch: two 16x16 sub-blocks each of K K^T and Q K^T, rows and blocks so far apart that the MMA
 // fragments' stores and the column reads of both halves of the warp hit all banks; then the gates
@@ -64,21 +64,38 @@ constexpr int kSStride = 24;
 constexpr int kSBlock = 16 * kSStride + 16;
 constexpr int kScratch = 4 * kSBlock + C;
 
-template <int DK>
+constexpr int lcm(int a, int b) {
+    int x = a;
+    while (x % b) x += a;
+    return x;
+}
+
+// A CTA's shape: ROWS state rows, the channels of each split over SPLIT warps, PREP prep warps, STAGES blocks in flight.
+template <int DK_, int ROWS_, int SPLIT_, int PREP_, int STAGES_>
 struct Layout {
+    static constexpr int DK = DK_, ROWS = ROWS_, SPLIT = SPLIT_, PREP = PREP_, STAGES = STAGES_;
+    static constexpr int GROUPS = ROWS / 16;                 // of 16 state rows
+    static constexpr int CHAIN = GROUPS * SPLIT;             // chain warps
+    static constexpr int THREADS = 32 * (CHAIN + PREP);
+    // barriers of arrived tiles: so many that a prep warp waits for every turn of those it waits for at all (one that
+    // sees every other turn of a barrier could take the turn before for its own)
+    static constexpr int FULL = lcm(PREP, STAGES);
     static constexpr int KA = DK / 64;                       // 64-channel atoms of [32][64] bf16, 4 KB, 128-byte swizzle
     static constexpr uint32_t K = 0;
     static constexpr uint32_t Q = K + KA * 4096;
-    static constexpr uint32_t V = Q + KA * 4096;             // [32][64]: the CTA's own rows of the state
+    static constexpr uint32_t V = Q + KA * 4096;             // [32][64]: the CTA's own rows of the state among them
     static constexpr uint32_t TX = V + 4096;                 // bytes a stage's loads bring
     static constexpr uint32_t TH = TX;                       // T, high and low parts, [t][j]
     static constexpr uint32_t TL = TH + C * kTStride;
     static constexpr uint32_t P = TL + C * kTStride;
     static constexpr uint32_t VEC = P + C * kTStride;        // fp32: b, b G, G, D_31 [32 each]
     static constexpr uint32_t STAGE = (VEC + 4 * C * 4 + 1023) / 1024 * 1024;
-    static constexpr uint32_t SCRATCH = kStages * STAGE;     // kScratch floats per prep warp
-    static constexpr uint32_t BAR = SCRATCH + kPrep * kScratch * 4;
-    static constexpr uint32_t BYTES = BAR + 128;
+    static constexpr uint32_t SCRATCH = STAGES * STAGE;      // kScratch floats per prep warp
+    static constexpr uint32_t ZX = SCRATCH + PREP * kScratch * 4;             // SPLIT 2: [2][CHAIN] partial Z, 2 KB
+    static constexpr uint32_t OX = ZX + (SPLIT > 1 ? 2 * CHAIN * 2048 : 0);   // and O of the partner's tokens, 1 KB
+    static constexpr uint32_t BAR = OX + (SPLIT > 1 ? 2 * CHAIN * 1024 : 0);
+    static constexpr uint32_t BYTES = BAR + 512;
+    static_assert(SPLIT <= 2 && (FULL + STAGES + GROUPS) * 8 + STAGES * 4 + 8 <= 512, "barrier space");
 };
 
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
@@ -92,16 +109,16 @@ struct Item {
 };
 
 // ---------------------------------------------------------------- prep warps
-// T (two bf16 parts), P and the gate vectors of blocks pw, pw + kPrep, ...
+// T (two bf16 parts), P and the gate vectors of blocks pw, pw + PREP, ...
 //
 // By 16x16 sub-blocks: the diagonal ones by forward substitution in fp32, lane
 // l one column of sub-block l / 16; the one below them as T21 = -T22 (A21 T11)
 // on the tensor cores, operands in two bf16 parts. Between the halves the
 // decay factors: D_tj = (g_16 .. g_t)(g_{j+1} .. g_15) for j < 16 <= t.
-template <int DK>
+template <class L>
 __device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uint8_t* sm, uint32_t sbase, int pw,
                                           uint64_t* full, uint64_t* ready, volatile int* abort_flag) {
-    using L = Layout<DK>;
+    constexpr int DK = L::DK;
     const int lane = threadIdx.x & 31, gq = lane >> 2, cq = lane & 3;
     const int blk = lane >> 4, col = lane & 15;
     float* kk = reinterpret_cast<float*>(sm + L::SCRATCH) + pw * kScratch;   // diagonal sub-blocks of K K^T, then A
@@ -122,11 +139,11 @@ __device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uin
     };
     float gn, bn;
     gates(pw, gn, bn);
-    for (int c = pw; c < it.blocks; c += kPrep) {
-        const int s = c % kStages;
+    for (int c = pw; c < it.blocks; c += L::PREP) {
+        const int s = c % L::STAGES;
         const uint32_t st = sbase + s * L::STAGE;
         const float g = gn, b = bn;
-        gates(c + kPrep, gn, bn);
+        gates(c + L::PREP, gn, bn);
         // ---- gate vectors: products inside each half, then over the block ----------------
         float G = g;
 #pragma unroll
@@ -138,7 +155,7 @@ __device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uin
         const float G15 = __shfl_sync(0xffffffffu, G, 15), G31 = __shfl_sync(0xffffffffu, G, 31);
         if (blk) G *= G15;
         gs[lane] = g;
-        bool ok = mbar_wait_or_abort(&full[s], (c / kStages) & 1, abort_flag);
+        bool ok = mbar_wait_or_abort(&full[c % L::FULL], (c / L::FULL) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) return;
         float* vec = reinterpret_cast<float*>(sm + s * L::STAGE + L::VEC);
         vec[lane] = b;
@@ -315,27 +332,30 @@ __device__ __forceinline__ void prep_warp(const StepArgs& a, const Item& it, uin
 
 // ---------------------------------------------------------------- the kernel
 
-template <int DK>
-__global__ void __launch_bounds__(kThreads, 2)
+template <class L, int RESIDENT>
+__global__ void __launch_bounds__(L::THREADS, RESIDENT)
 chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
              const __grid_constant__ CUtensorMap tmv, const StepArgs a) {
-    using L = Layout<DK>;
-    constexpr int NT = DK / 8;   // n-tiles of a warp's state rows
+    constexpr int DK = L::DK, SPLIT = L::SPLIT, STAGES = L::STAGES;
+    constexpr int NT = DK / 8 / SPLIT;   // n-tiles of a warp's part of its state rows
+    constexpr int OT = 4 / SPLIT;        // 8-token tiles of the outputs that a warp finishes
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     uint8_t* sm = smem_raw + (sbase - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BAR);   // [kStages] TMA: a block's tiles have arrived
-    uint64_t* ready = full + kStages;                            // [kStages] prep: T, P and vectors are written
-    int* left = reinterpret_cast<int*>(ready + kStages);         // [kStages] chain warps that have left the stage
-    volatile int* issued = left + kStages;                       // blocks whose loads were issued
-    volatile int* abort_flag = left + kStages + 1;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BAR);   // [FULL] TMA: a block's tiles have arrived
+    uint64_t* ready = full + L::FULL;                            // [STAGES] prep: T, P and vectors are written
+    uint64_t* swap = ready + STAGES;                             // [GROUPS] both warps of 16 rows have written their parts
+    int* left = reinterpret_cast<int*>(swap + L::GROUPS);        // [STAGES] chain warps that have left the stage
+    volatile int* issued = left + STAGES;                        // blocks whose loads were issued
+    volatile int* abort_flag = left + STAGES + 1;
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&full[i], 1);
+        for (int i = 0; i < L::FULL; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < L::GROUPS; ++i) mbar_init(&swap[i], SPLIT);
+        for (int i = 0; i < STAGES; ++i) {
             mbar_init(&ready[i], 1);
             left[i] = 0;
         }
@@ -349,7 +369,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     griddep_wait();
     Item it;
     {
-        const int splits = a.dv / kRows;
+        const int splits = a.dv / L::ROWS;
         const int per_req = a.Hv * splits;
         const int rank = blockIdx.x / per_req, hs = blockIdx.x % per_req;
         if (!read_request(a, rank, it.rq)) return;
@@ -361,28 +381,30 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     __syncthreads();
 
     auto issue = [&](int c) {   // loads of block c (one thread); rows past the tensor read as zeros
-        const int s = c % kStages, row = it.rq.row0 + c * C;
-        uint8_t* st = sm + s * L::STAGE;
-        mbar_arrive_expect_tx(&full[s], L::TX);
+        const int row = it.rq.row0 + c * C;
+        uint8_t* st = sm + c % STAGES * L::STAGE;
+        uint64_t* bar = &full[c % L::FULL];
+        mbar_arrive_expect_tx(bar, L::TX);
 #pragma unroll
         for (int x = 0; x < L::KA; ++x) {
-            tma_load_3d(&tmk, &full[s], st + L::K + x * 4096, x * 64, it.khead, row);
-            tma_load_3d(&tmq, &full[s], st + L::Q + x * 4096, x * 64, it.khead, row);
+            tma_load_3d(&tmk, bar, st + L::K + x * 4096, x * 64, it.khead, row);
+            tma_load_3d(&tmq, bar, st + L::Q + x * 4096, x * 64, it.khead, row);
         }
-        tma_load_3d(&tmv, &full[s], st + L::V, it.split * kRows, it.head, row);
+        tma_load_3d(&tmv, bar, st + L::V, it.split * L::ROWS / 64 * 64, it.head, row);
         *issued = c + 1;
     };
     if (tid == 0)
-        for (int c = 0; c < kStages && c < it.blocks; ++c) issue(c);
+        for (int c = 0; c < STAGES && c < it.blocks; ++c) issue(c);
 
     bool failed = false;
-    if (warp >= kChain) {
-        prep_warp<DK>(a, it, sm, sbase, warp - kChain, full, ready, abort_flag);
+    if (warp >= L::CHAIN) {
+        prep_warp<L>(a, it, sm, sbase, warp - L::CHAIN, full, ready, abort_flag);
     } else {
-        // ======================= chain warp: rows r0 + g and r0 + g + 8 ====================
+        // ======================= chain warp: rows r0 + g and r0 + g + 8, 8 NT channels ======
         const int gq = lane >> 2, cq = lane & 3;
-        const int r0 = it.split * kRows + 16 * warp;
-        float* sp = a.states + ((static_cast<size_t>(it.rq.slot) * a.Hv + it.head) * a.dv + r0 + gq) * DK + 2 * cq;
+        const int grp = warp % L::GROUPS, part = SPLIT > 1 ? warp / L::GROUPS : 0;
+        const int r0 = it.split * L::ROWS + 16 * grp;
+        float* sp = a.states + ((static_cast<size_t>(it.rq.slot) * a.Hv + it.head) * a.dv + r0 + gq) * DK + 8 * NT * part + 2 * cq;
         float X[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -405,11 +427,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         const size_t ostep = static_cast<size_t>(a.Hv) * a.dv;
         // outputs of the block before, rounded: [dv][token] fragments, turned
         // to [token][dv] pairs when they leave
-        uint32_t Y[4][2] = {};
-        auto store_out = [&](int n, int c) {   // tokens 8n .. 8n + 7 of block c
+        uint32_t Y[OT][2] = {};
+        auto store_out = [&](int n, int c) {   // the warp's n-th tile of 8 tokens of block c
             const uint32_t y0 = transpose8x8(Y[n][0]);   // token 8n + g, rows 2c, 2c + 1
             const uint32_t y1 = transpose8x8(Y[n][1]);   // rows 8 + 2c, ..
-            const int t = c * C + 8 * n + gq;
+            const int t = c * C + 8 * (OT * part + n) + gq;
             if (c >= 0 && t < it.rq.len) {
                 __nv_bfloat16* o = op + static_cast<size_t>(t) * ostep;
                 *reinterpret_cast<uint32_t*>(o) = y0;
@@ -417,11 +439,32 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             }
         };
 
+        // SPLIT 2: Z and O are sums over the channels of both warps of a row group. Each hands its part of Z over, and of O
+        // that of the other's tokens (scaled, with the next block's Z), in two buffers taken in turn: what is written
+        // for block c + 2 comes after a turn of the barrier that follows the other's reads for block c.
+        auto mine = [&](uint32_t area, int size, int c, int of) {
+            return sm + area + (((c & 1) * L::CHAIN + grp + L::GROUPS * of) * size + lane * 16);
+        };
+        float Op[OT][4];   // SPLIT 2: outputs of the block before, without the other's part
+        auto swapped = [&](int c) {   // both warps of the group have written for block c
+            __syncwarp();
+            const bool ok = mbar_wait_or_abort(&swap[grp], c & 1, abort_flag);
+            return __all_sync(0xffffffffu, ok);
+        };
+        auto join_out = [&](int c) {   // outputs of block c, whole and rounded
+#pragma unroll
+            for (int n = 0; n < OT; ++n) {
+                const float4 y = *reinterpret_cast<const float4*>(mine(L::OX, 1024, c, 1 - part) + 512 * n);
+                Y[n][0] = pack_bf16(Op[n][0] + y.x, Op[n][1] + y.y);
+                Y[n][1] = pack_bf16(Op[n][2] + y.z, Op[n][3] + y.w);
+            }
+        };
+
         for (int c = 0; c < it.blocks; ++c) {
-            const int s = c % kStages;
-            const uint32_t ph = (c / kStages) & 1;
+            const int s = c % STAGES;
             const uint32_t st = sbase + s * L::STAGE;
-            bool ok = mbar_wait_or_abort(&full[s], ph, abort_flag) && mbar_wait_or_abort(&ready[s], ph, abort_flag);
+            bool ok = mbar_wait_or_abort(&full[c % L::FULL], (c / L::FULL) & 1, abort_flag) &&
+                      mbar_wait_or_abort(&ready[s], (c / STAGES) & 1, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) {
                 failed = true;
                 break;
@@ -429,9 +472,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             // ---- Z = X K^T, both parts of X; the block before's outputs leave meanwhile ----
             float Z[4][4] = {}, O[4][4] = {};
 #pragma unroll
-            for (int x = 0; x < DK / 16; ++x) {
+            for (int x = 0; x < NT / 2; ++x) {
                 uint32_t hi[4], lo[4], b0[4], b1[4];
-                const uint32_t at = st + L::K + (x / 4) * 4096, ch = (x % 4) * 2 + bc;
+                const int xk = NT / 2 * part + x;   // 16 channels
+                const uint32_t at = st + L::K + (xk / 4) * 4096, ch = (xk % 4) * 2 + bc;
                 ldsm4(b0, at + sw128_off(br, ch));
                 ldsm4(b1, at + sw128_off(16 + br, ch));
                 split_tiles(X[2 * x], X[2 * x + 1], hi, lo);
@@ -439,7 +483,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 mma_16816(Z[1], hi, b0[2], b0[3]);
                 mma_16816(Z[2], hi, b1[0], b1[1]);
                 mma_16816(Z[3], hi, b1[2], b1[3]);
-                if (x < 4) store_out(x, c - 1);
+                if (SPLIT == 1 && x < 4) store_out(x, c - 1);
                 mma_16816(Z[0], lo, b0[0], b0[1]);
                 mma_16816(Z[1], lo, b0[2], b0[3]);
                 mma_16816(Z[2], lo, b1[0], b1[1]);
@@ -450,9 +494,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
 #pragma unroll
                 for (int x = x0; x < x1; ++x) {
                     uint32_t hi[4], b0[4], b1[4];
-                    const uint32_t at = st + L::Q + (x / 4) * 4096, ch = (x % 4) * 2 + bc;
-                    ldsm4(b0, at + sw128_off(br, ch));
-                    ldsm4(b1, at + sw128_off(16 + br, ch));
+                    const int xk = NT / 2 * part + x;
+                    const uint32_t at = st + L::Q + (xk / 4) * 4096, ch = (xk % 4) * 2 + bc;
+                    ldsm4(b0, at + sw128_off(16 * part + br, ch));         // (the warp's own tokens first)
+                    ldsm4(b1, at + sw128_off(16 * (1 - part) + br, ch));
                     hi[0] = pack_bf16(X[2 * x][0], X[2 * x][1]);
                     hi[1] = pack_bf16(X[2 * x][2], X[2 * x][3]);
                     hi[2] = pack_bf16(X[2 * x + 1][0], X[2 * x + 1][1]);
@@ -463,13 +508,34 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                     mma_16816(O[3], hi, b1[2], b1[3]);
                 }
             };
-            read_out(0, DK / 32);
+            if constexpr (SPLIT > 1) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    *reinterpret_cast<float4*>(mine(L::ZX, 2048, c, part) + 512 * n) = make_float4(Z[n][0], Z[n][1], Z[n][2], Z[n][3]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&swap[grp]);
+                read_out(0, NT / 2);
+                if (!swapped(c)) {
+                    failed = true;
+                    break;
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float4 z = *reinterpret_cast<const float4*>(mine(L::ZX, 2048, c, 1 - part) + 512 * n);
+                    Z[n][0] += z.x;
+                    Z[n][1] += z.y;
+                    Z[n][2] += z.z;
+                    Z[n][3] += z.w;
+                }
+            } else {
+                read_out(0, NT / 4);
+            }
             // ---- R = b (V - G Z), in Z --------------------------------------------------------
             const float* vec = reinterpret_cast<const float*>(sm + s * L::STAGE + L::VEC);
 #pragma unroll
             for (int n = 0; n < 4; n += 2) {
                 uint32_t v4[4];   // (token 8n, row g) (.., row g + 8) (token 8n + 8, ..) (..)
-                ldsm4t(v4, st + L::V + sw128_off(8 * n + (lane & 7) + (lane >> 4) * 8, 2 * warp + ((lane >> 3) & 1)));
+                ldsm4t(v4, st + L::V + sw128_off(8 * n + (lane & 7) + (lane >> 4) * 8, r0 % 64 / 8 + ((lane >> 3) & 1)));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int t = 8 * (n + i) + 2 * cq;
@@ -515,38 +581,59 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 mma_16816(U[2], h1, t2[0], t2[1]);
                 mma_16816(U[3], h1, t2[2], t2[3]);
             }
-            read_out(DK / 32, DK / 16);
+            if constexpr (SPLIT > 1) {
+                if (c > 0) {
+                    join_out(c - 1);
+#pragma unroll
+                    for (int n = 0; n < OT; ++n) store_out(n, c - 1);
+                }
+            } else {
+                read_out(NT / 4, NT / 2);
+            }
             // ---- O = G O + U P^T; X = G_31 X + (U D_31) K --------------------------------------
             uint32_t h0[4], l0[4], h1[4], l1[4];
             const float gc = vec[2 * C + C - 1];
             {
                 uint32_t t0[4], t1[4], t2[4];
                 const uint32_t tp = st + L::P + br * kTStride + bc * 16;
-                ldsm4(t0, tp);
-                ldsm4(t1, tp + 16 * kTStride);
-                ldsm4(t2, tp + 16 * kTStride + 32);
+                if (SPLIT == 1 || part == 0) ldsm4(t0, tp);
+                if (SPLIT == 1 || part == 1) {
+                    ldsm4(t1, tp + 16 * kTStride);
+                    ldsm4(t2, tp + 16 * kTStride + 32);
+                }
                 split_tiles(U[0], U[1], h0, l0);
                 split_tiles(U[2], U[3], h1, l1);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    const float2 g = *reinterpret_cast<const float2*>(vec + 2 * C + 8 * n + 2 * cq);
+                    const float2 g = *reinterpret_cast<const float2*>(vec + 2 * C + (8 * n + 16 * part) % C + 2 * cq);
                     O[n][0] *= g.x;
                     O[n][1] *= g.y;
                     O[n][2] *= g.x;
                     O[n][3] *= g.y;
                 }
-                mma_16816(O[0], h0, t0[0], t0[1]);
-                mma_16816(O[1], h0, t0[2], t0[3]);
-                mma_16816(O[2], h0, t1[0], t1[1]);
-                mma_16816(O[3], h0, t1[2], t1[3]);
-                mma_16816(O[0], l0, t0[0], t0[1]);
-                mma_16816(O[1], l0, t0[2], t0[3]);
-                mma_16816(O[2], l0, t1[0], t1[1]);
-                mma_16816(O[3], l0, t1[2], t1[3]);
-                mma_16816(O[2], h1, t2[0], t2[1]);
-                mma_16816(O[3], h1, t2[2], t2[3]);
-                mma_16816(O[2], l1, t2[0], t2[1]);
-                mma_16816(O[3], l1, t2[2], t2[3]);
+                if (SPLIT == 1 || part == 0) {   // tokens 0 .. 15
+                    mma_16816(O[0], h0, t0[0], t0[1]);
+                    mma_16816(O[1], h0, t0[2], t0[3]);
+                    mma_16816(O[0], l0, t0[0], t0[1]);
+                    mma_16816(O[1], l0, t0[2], t0[3]);
+                }
+                if (SPLIT == 1 || part == 1) {   // tokens 16 .. 31
+                    constexpr int n = SPLIT == 1 ? 2 : 0;
+                    mma_16816(O[n], h0, t1[0], t1[1]);
+                    mma_16816(O[n + 1], h0, t1[2], t1[3]);
+                    mma_16816(O[n], l0, t1[0], t1[1]);
+                    mma_16816(O[n + 1], l0, t1[2], t1[3]);
+                    mma_16816(O[n], h1, t2[0], t2[1]);
+                    mma_16816(O[n + 1], h1, t2[2], t2[3]);
+                    mma_16816(O[n], l1, t2[0], t2[1]);
+                    mma_16816(O[n + 1], l1, t2[2], t2[3]);
+                }
+                if constexpr (SPLIT > 1) {
+#pragma unroll
+                    for (int n = 0; n < OT; ++n)
+                        *reinterpret_cast<float4*>(mine(L::OX, 1024, c, part) + 512 * n) =
+                            make_float4(O[OT + n][0], O[OT + n][1], O[OT + n][2], O[OT + n][3]);
+                }
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -561,7 +648,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
 #pragma unroll
             for (int n = 0; n < NT; n += 2) {
                 uint32_t b0[4], b1[4];
-                const uint32_t at = st + L::K + (n / 8) * 4096, ch = n % 8 + tc;
+                const int nk = NT * part + n;
+                const uint32_t at = st + L::K + (nk / 8) * 4096, ch = nk % 8 + tc;
                 ldsm4t(b0, at + sw128_off(tr, ch));
                 ldsm4t(b1, at + sw128_off(16 + tr, ch));
 #pragma unroll
@@ -583,20 +671,33 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             if (lane == 0) {
                 int before;
                 asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(&left[s])) : "memory");
-                if (before == kChain - 1 && c + kStages < it.blocks) {
+                if (before == L::CHAIN - 1 && c + STAGES < it.blocks) {
                     left[s] = 0;
-                    issue(c + kStages);
+                    issue(c + STAGES);
                 }
             }
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                Y[n][0] = pack_bf16(O[n][0], O[n][1]);
-                Y[n][1] = pack_bf16(O[n][2], O[n][3]);
+            for (int n = 0; n < OT; ++n) {
+                if constexpr (SPLIT > 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) Op[n][i] = O[n][i];
+                } else {
+                    Y[n][0] = pack_bf16(O[n][0], O[n][1]);
+                    Y[n][1] = pack_bf16(O[n][2], O[n][3]);
+                }
+            }
+        }
+        if constexpr (SPLIT > 1) {
+            if (!failed) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&swap[grp]);
+                failed = !swapped(it.blocks);
+                if (!failed) join_out(it.blocks - 1);
             }
         }
         if (!failed) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) store_out(n, it.blocks - 1);
+            for (int n = 0; n < OT; ++n) store_out(n, it.blocks - 1);
         }
         if (!failed) {
 #pragma unroll
@@ -611,20 +712,28 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     }
     if (failed) {   // let the loads in flight land before the CTA leaves (bounded)
         if (lane == 0)
-            for (int c = max(0, *issued - kStages); c < *issued; ++c)
-                mbar_wait(&full[c % kStages], (c / kStages) & 1, 100000000ull);
+            for (int c = max(0, *issued - STAGES); c < *issued; ++c)
+                mbar_wait(&full[c % L::FULL], (c / L::FULL) & 1, 100000000ull);
     }
+}
+
+template <class L, int RESIDENT>
+cudaError_t run_shape(const StepArgs& a, cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v) {
+    constexpr uint32_t smem = L::BYTES + 1024;
+    static_assert(RESIDENT * (smem + 1024) <= 228 * 1024 && smem <= 232448, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(chunk_kernel<L, RESIDENT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long grid = static_cast<long long>(a.requests) * a.Hv * (a.dv / L::ROWS);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_pdl(chunk_kernel<L, RESIDENT>, static_cast<unsigned>(grid), L::THREADS, smem, s, q, k, v, a);
 }
 
 template <int DK>
 cudaError_t run(const StepArgs& a, cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v) {
-    constexpr uint32_t smem = Layout<DK>::BYTES + 1024;
-    static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
-    const cudaError_t e = cudaFuncSetAttribute(chunk_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const long long grid = static_cast<long long>(a.requests) * a.Hv * (a.dv / kRows);
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_pdl(chunk_kernel<DK>, static_cast<unsigned>(grid), kThreads, smem, s, q, k, v, a);
+    // one request of 2048 tokens, 16 heads, d 64 (d_k 128): 82 (100) us, by CTAs of 64 rows 92 (131); the latter have
+    // two CTAs to an SM and half of the prep, which counts where SMs are short
+    if (chunk_is_alone(a.requests, a.Hv, a.dv, a.sm_count)) return run_shape<Layout<DK, 32, 2, 3, 6>, 1>(a, s, q, k, v);
+    return run_shape<Layout<DK, 64, 1, 2, 3>, 2>(a, s, q, k, v);
 }
 
 }  // namespace

@@ -299,21 +299,22 @@ def test_default_form_by_type():
         assert e.value.code == la.LA_ERR_UNSUPPORTED
 
 
-def test_many_requests_and_heads():
+@pytest.mark.parametrize("dk,dv,chunk", [(128, 128, 64), (64, 128, 64), (128, 128, 32), (64, 64, 32), (128, 64, 32)])
+def test_many_requests_and_heads(dk, dv, chunk):
     # more CTAs than are resident, long and short ones mixed; every head of a few requests checked
     rng = random.Random(4)
     lens = [rng.choice((0, 1, 2, 33, 64, 200, 260)) for _ in range(150)]
-    x, pool = draw(lens, 4, 8, 128, 128, "bf16", seed=8)
-    h = handle_for(lens, 4, 8, 128, 128, "bf16", pool)
+    x, pool = draw(lens, 4, 8, dk, dv, "bf16", seed=8)
+    h = handle_for(lens, 4, 8, dk, dv, "bf16", pool)
     seen = [r % 3 for r in range(len(lens))]
     plan = make_plan(h, lens, seen, x["slots"])
     before = x["states"].clone()
-    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"])
+    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], chunk=chunk)
     assert h.status() == la.LA_OK
-    check(x, lens, seen, before, out, "bf16", 64, only=range(0, 150, 19))
+    check(x, lens, seen, before, out, "bf16", chunk, only=range(0, 150, 19))
     # the same inputs again: the same bits
     again = before.clone()
-    out2 = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], again)
+    out2 = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], again, chunk=chunk)
     assert torch.equal(again, x["states"])
     for r in range(150):
         a, e = int(plan.offsets[r]), int(plan.offsets[r + 1])
