@@ -73,8 +73,8 @@ int check_config(const la_packed_config* c) {
 // Whether a step at d_v 128 takes blocks of 64 tokens on the tcgen05 tensor cores (packed_tc.cu, one CTA per SM)
 // instead of blocks of 32 by warp-level MMAs (packed_chunk.cu, two or four CTAs per head). The former starts later and
 // has the higher throughput; the latter waits less between the steps of one request. Measured, 32 / 64:
-//   few heads (every CTA of 32 state rows has an SM), d_k 128: 16 of 64 rows 6.6 / 10.6 us, of 8192 397 / 423; 32 of
-//            16384 (two requests) 399 / 426; d_k 64: 16 of 64 5.4 / 9.4, of 8192 325 / 384
+//   few heads (every CTA of 32 state rows has an SM), d_k 128: 16 of 64 rows 6.5 / 10.6 us, of 8192 320 / 422; 32 of
+//            16384 (two requests) 363 / 426; d_k 64: 16 of 64 5.5 / 9.3, of 8192 256 / 383
 //   d_k 128, 32 requests, 16 heads: 256 rows 29.0 / 31.2, 512 33.2 / 31.5, 4096 120 / 100
 //   d_k 64, 64 requests, 16 heads: 4096 rows 53 / 56, 8192 78 / 77, 32768 235 / 208; 16 requests of one length,
 //           16 heads: 8192 67 / 61, 32768 258 / 211

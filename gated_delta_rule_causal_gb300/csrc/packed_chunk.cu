@@ -20,8 +20,9 @@
 // each, ahead of the chain. The last chain warp to leave a stage issues the
 // loads that reuse it.
 // Where there are no more CTAs of 32 rows than SMs, each has an SM to itself:
-// six stages, three prep warps, and two chain warps to 16 rows, half of the
-// channels each, who add up Z and O through shared memory.
+// more stages, two chain warps to 16 rows, half of the channels each, who add
+// up Z through shared memory, and an output warp to 16 rows, to which they hand
+// X (high parts) and U.
 //
 // Precision. q, k, v are bf16 and enter the MMAs as they are. What the state
 // depends on (X in K X^T, R and T in T R, U in U^T K) is split into two bf16
@@ -33,12 +34,13 @@
 // Accumulators, gates, A and the inverse are fp32.
 //
 // Bound by latency: a block's products follow one another inside a warp, some
-// 2500 clocks for 66 to 110 MMAs of 8 each and their operands' splits at d_k 64.
-// Measured, 16 heads: one request at d 64 of 130 tokens 8.3 us, of 2048 82 us
-// (1.3 us a block); at d_k 128, d_v 64 100 us; two of 8192 at d 128 399 us. By
-// CTAs of 64 rows: 9.7, 92, 131 and 511 us. Nine of 2048 at d_k 128, d_v 64 (64
-// rows): 136 us, and 201 us with prep warps that took T and P of every block
-// instead of alternate blocks.
+// 2000 to 2700 clocks at d_k 64 for 66 to 110 MMAs of 8 each and their operands'
+// splits. Measured, 16 heads: one request at d 64 of 130 tokens 8.4 us, of 2048
+// 66 us (1.0 us a block); at d_k 128, d_v 64 82 us; two of 8192 at d 128 363 us.
+// By CTAs of 64 rows: 9.7, 92, 131 and 511 us; without the output warps 8.3, 82,
+// 100 and 399. Nine of 2048 at d_k 128, d_v 64 (64 rows): 136 us, and 201 us with
+// prep warps that took T and P of every block instead of alternate blocks.
+// Fragments loaded ahead of the exchange of Z: no gain (74 us for 71).
 //
 // Rows past a request's end belong to the next request: they are zeroed in the
 // tiles before anything reads them, with gate 1 and beta 0, and are not
@@ -76,7 +78,8 @@ struct Layout {
     static constexpr int DK = DK_, ROWS = ROWS_, SPLIT = SPLIT_, PREP = PREP_, STAGES = STAGES_;
     static constexpr int GROUPS = ROWS / 16;                 // of 16 state rows
     static constexpr int CHAIN = GROUPS * SPLIT;             // chain warps
-    static constexpr int THREADS = 32 * (CHAIN + PREP);
+    static constexpr int OUT = SPLIT > 1 ? GROUPS : 0;       // warps that compute the outputs (else the chain does)
+    static constexpr int THREADS = 32 * (CHAIN + OUT + PREP);
     // barriers of arrived tiles: so many that a prep warp waits for every turn of those it waits for at all (one that
     // sees every other turn of a barrier could take the turn before for its own)
     static constexpr int FULL = lcm(PREP, STAGES);
@@ -92,12 +95,19 @@ struct Layout {
     static constexpr uint32_t STAGE = (VEC + 4 * C * 4 + 1023) / 1024 * 1024;
     static constexpr uint32_t SCRATCH = STAGES * STAGE;      // kScratch floats per prep warp
     static constexpr uint32_t ZX = SCRATCH + PREP * kScratch * 4;             // SPLIT 2: [2][CHAIN] partial Z, 2 KB
-    static constexpr uint32_t OX = ZX + (SPLIT > 1 ? 2 * CHAIN * 2048 : 0);   // and O of the partner's tokens, 1 KB
-    static constexpr uint32_t BAR = OX + (SPLIT > 1 ? 2 * CHAIN * 1024 : 0);
+    static constexpr uint32_t XO = ZX + (SPLIT > 1 ? 2 * CHAIN * 2048 : 0);        // [2][OUT] X, high parts: 512 a step of 16
+    static constexpr uint32_t UO = XO + 2 * OUT * (DK / 16) * 512;                 // [2][OUT] U, both parts: 2 KB
+    static constexpr uint32_t BAR = UO + 2 * OUT * 2048;
     static constexpr uint32_t BYTES = BAR + 512;
-    static_assert(SPLIT <= 2 && (FULL + STAGES + GROUPS) * 8 + STAGES * 4 + 8 <= 512, "barrier space");
+    static_assert(SPLIT <= 2 && (FULL + STAGES + 5 * GROUPS) * 8 + STAGES * 4 + 8 <= 512, "barrier space");
 };
 
+__device__ __forceinline__ void st_shared_4(uint32_t addr, const uint32_t (&x)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+}
+__device__ __forceinline__ void ld_shared_4(uint32_t (&x)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(addr), "r"(0) : "memory");
 }
@@ -338,7 +348,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
              const __grid_constant__ CUtensorMap tmv, const StepArgs a) {
     constexpr int DK = L::DK, SPLIT = L::SPLIT, STAGES = L::STAGES;
     constexpr int NT = DK / 8 / SPLIT;   // n-tiles of a warp's part of its state rows
-    constexpr int OT = 4 / SPLIT;        // 8-token tiles of the outputs that a warp finishes
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -348,13 +357,21 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BAR);   // [FULL] TMA: a block's tiles have arrived
     uint64_t* ready = full + L::FULL;                            // [STAGES] prep: T, P and vectors are written
     uint64_t* swap = ready + STAGES;                             // [GROUPS] both warps of 16 rows have written their parts
-    int* left = reinterpret_cast<int*>(swap + L::GROUPS);        // [STAGES] chain warps that have left the stage
+    uint64_t* given = swap + L::GROUPS;                          // [2][GROUPS] chain: X and U are there for the outputs
+    uint64_t* taken = given + 2 * L::GROUPS;                     // [2][GROUPS] output warp: they are read
+    int* left = reinterpret_cast<int*>(taken + 2 * L::GROUPS);   // [STAGES] warps that have left the stage
     volatile int* issued = left + STAGES;                        // blocks whose loads were issued
     volatile int* abort_flag = left + STAGES + 1;
 
     if (tid == 0) {
         for (int i = 0; i < L::FULL; ++i) mbar_init(&full[i], 1);
-        for (int i = 0; i < L::GROUPS; ++i) mbar_init(&swap[i], SPLIT);
+        for (int i = 0; i < L::GROUPS; ++i) {
+            mbar_init(&swap[i], SPLIT);
+            for (int b = i; b < 2 * L::GROUPS; b += L::GROUPS) {   // one for each buffer: the sides may be two blocks apart
+                mbar_init(&given[b], SPLIT);
+                mbar_init(&taken[b], 1);
+            }
+        }
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&ready[i], 1);
             left[i] = 0;
@@ -396,9 +413,127 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
     if (tid == 0)
         for (int c = 0; c < STAGES && c < it.blocks; ++c) issue(c);
 
+    // a warp has read stage c % STAGES: the last one to say so reloads it
+    auto leave = [&](int c) {
+        __syncwarp();
+        if (lane == 0) {
+            const int s = c % STAGES;
+            int before;
+            asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(&left[s])) : "memory");
+            if (before == L::CHAIN + L::OUT - 1 && c + STAGES < it.blocks) {
+                left[s] = 0;
+                issue(c + STAGES);
+            }
+        }
+    };
+    auto here = [&](int c) {   // block c's tiles, T, P and vectors
+        const bool ok = mbar_wait_or_abort(&full[c % L::FULL], (c / L::FULL) & 1, abort_flag) &&
+                        mbar_wait_or_abort(&ready[c % STAGES], (c / STAGES) & 1, abort_flag);
+        return __all_sync(0xffffffffu, ok);
+    };
+    const int br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;   // ldmatrix: B fragments of two n-tiles (rows = n, 16-byte chunks along k)
+    const size_t ostep = static_cast<size_t>(a.Hv) * a.dv;
+    // outputs, rounded: [dv][token] fragments y of tokens 8n .. of block c, turned to [token][dv] pairs
+    auto store_out = [&](__nv_bfloat16* op, int n, int c, const uint32_t (&y)[2]) {
+        const uint32_t y0 = transpose8x8(y[0]);   // token 8n + g, rows 2c, 2c + 1
+        const uint32_t y1 = transpose8x8(y[1]);   // rows 8 + 2c, ..
+        const int t = c * C + 8 * n + (lane >> 2);
+        if (c >= 0 && t < it.rq.len) {
+            __nv_bfloat16* o = op + static_cast<size_t>(t) * ostep;
+            *reinterpret_cast<uint32_t*>(o) = y0;
+            *reinterpret_cast<uint32_t*>(o + 8) = y1;
+        }
+    };
+    auto out_rows = [&](int r0) {
+        return static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(it.rq.row0) * a.Hv + it.head) * a.dv + r0 + 2 * (lane & 3);
+    };
+    // O = X Q^T (channels 16 x ..), high parts of X
+    auto read_step = [&](uint32_t st, int x, const uint32_t (&hi)[4], float (&O)[4][4]) {
+        uint32_t b0[4], b1[4];
+        const uint32_t at = st + L::Q + (x / 4) * 4096, ch = (x % 4) * 2 + bc;
+        ldsm4(b0, at + sw128_off(br, ch));
+        ldsm4(b1, at + sw128_off(16 + br, ch));
+        mma_16816(O[0], hi, b0[0], b0[1]);
+        mma_16816(O[1], hi, b0[2], b0[3]);
+        mma_16816(O[2], hi, b1[0], b1[1]);
+        mma_16816(O[3], hi, b1[2], b1[3]);
+    };
+    // O = G O + P U
+    auto load_p = [&](uint32_t st, uint32_t (&t0)[4], uint32_t (&t1)[4], uint32_t (&t2)[4]) {
+        const uint32_t tp = st + L::P + br * kTStride + bc * 16;
+        ldsm4(t0, tp);
+        ldsm4(t1, tp + 16 * kTStride);
+        ldsm4(t2, tp + 16 * kTStride + 32);
+    };
+    auto finish_out = [&](const float* vec, const uint32_t (&t0)[4], const uint32_t (&t1)[4], const uint32_t (&t2)[4],
+                          const uint32_t (&h0)[4], const uint32_t (&l0)[4], const uint32_t (&h1)[4], const uint32_t (&l1)[4],
+                          float (&O)[4][4]) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float2 g = *reinterpret_cast<const float2*>(vec + 2 * C + 8 * n + 2 * (lane & 3));
+            O[n][0] *= g.x;
+            O[n][1] *= g.y;
+            O[n][2] *= g.x;
+            O[n][3] *= g.y;
+        }
+        mma_16816(O[0], h0, t0[0], t0[1]);
+        mma_16816(O[1], h0, t0[2], t0[3]);
+        mma_16816(O[2], h0, t1[0], t1[1]);
+        mma_16816(O[3], h0, t1[2], t1[3]);
+        mma_16816(O[0], l0, t0[0], t0[1]);
+        mma_16816(O[1], l0, t0[2], t0[3]);
+        mma_16816(O[2], l0, t1[0], t1[1]);
+        mma_16816(O[3], l0, t1[2], t1[3]);
+        mma_16816(O[2], h1, t2[0], t2[1]);
+        mma_16816(O[3], h1, t2[2], t2[3]);
+        mma_16816(O[2], l1, t2[0], t2[1]);
+        mma_16816(O[3], l1, t2[2], t2[3]);
+    };
+
     bool failed = false;
-    if (warp >= L::CHAIN) {
-        prep_warp<L>(a, it, sm, sbase, warp - L::CHAIN, full, ready, abort_flag);
+    if (warp >= L::CHAIN + L::OUT) {
+        prep_warp<L>(a, it, sm, sbase, warp - L::CHAIN - L::OUT, full, ready, abort_flag);
+    } else if (warp >= L::CHAIN) {
+        // ======================= output warp: 16 rows =======================================
+        const int grp = warp - L::CHAIN;
+        __nv_bfloat16* op = out_rows(it.split * L::ROWS + 16 * grp);
+        for (int c = 0; c < it.blocks; ++c) {
+            const uint32_t st = sbase + c % STAGES * L::STAGE;
+            bool ok = here(c);
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&given[(c & 1) * L::GROUPS + grp], (c >> 1) & 1, abort_flag));
+            if (!ok) {
+                failed = true;
+                break;
+            }
+            const uint32_t buf = ((c & 1) * L::OUT + grp), xo = sbase + L::XO + buf * (DK / 16) * 512 + lane * 16;
+            const uint32_t uo = sbase + L::UO + buf * 2048 + lane * 16;
+            float O[4][4] = {};
+#pragma unroll
+            for (int x = 0; x < DK / 16; ++x) {
+                uint32_t hi[4];
+                ld_shared_4(hi, xo + 512 * x);
+                read_step(st, x, hi, O);
+            }
+            uint32_t h0[4], l0[4], h1[4], l1[4], t0[4], t1[4], t2[4];
+            load_p(st, t0, t1, t2);
+            ld_shared_4(h0, uo);
+            ld_shared_4(l0, uo + 512);
+            ld_shared_4(h1, uo + 1024);
+            ld_shared_4(l1, uo + 1536);
+            finish_out(reinterpret_cast<const float*>(sm + c % STAGES * L::STAGE + L::VEC), t0, t1, t2, h0, l0, h1, l1, O);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&taken[(c & 1) * L::GROUPS + grp]);
+            leave(c);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const uint32_t y[2] = {pack_bf16(O[n][0], O[n][1]), pack_bf16(O[n][2], O[n][3])};
+                store_out(op, n, c, y);
+            }
+        }
+        if (failed && lane == 0) {
+            *abort_flag = 1;
+            atomicOr(a.status, kStatusTmaWait);
+        }
     } else {
         // ======================= chain warp: rows r0 + g and r0 + g + 8, 8 NT channels ======
         const int gq = lane >> 2, cq = lane & 3;
@@ -418,57 +553,26 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
             X[n][2] = w.x;
             X[n][3] = w.y;
         }
-        // ldmatrix lane addresses: B fragments of two n-tiles (rows = n, 16-byte
-        // chunks along k) and, transposed, of K as [k = token][n = channel]
-        const int br = (lane & 7) + (lane >> 4) * 8, bc = (lane >> 3) & 1;
-        const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = lane >> 4;
-        __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) +
-                            (static_cast<size_t>(it.rq.row0) * a.Hv + it.head) * a.dv + r0 + 2 * cq;
-        const size_t ostep = static_cast<size_t>(a.Hv) * a.dv;
-        // outputs of the block before, rounded: [dv][token] fragments, turned
-        // to [token][dv] pairs when they leave
-        uint32_t Y[OT][2] = {};
-        auto store_out = [&](int n, int c) {   // the warp's n-th tile of 8 tokens of block c
-            const uint32_t y0 = transpose8x8(Y[n][0]);   // token 8n + g, rows 2c, 2c + 1
-            const uint32_t y1 = transpose8x8(Y[n][1]);   // rows 8 + 2c, ..
-            const int t = c * C + 8 * (OT * part + n) + gq;
-            if (c >= 0 && t < it.rq.len) {
-                __nv_bfloat16* o = op + static_cast<size_t>(t) * ostep;
-                *reinterpret_cast<uint32_t*>(o) = y0;
-                *reinterpret_cast<uint32_t*>(o + 8) = y1;
-            }
-        };
+        const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = lane >> 4;   // transposed, of K as [k = token][n = channel]
+        __nv_bfloat16* op = out_rows(r0);
+        uint32_t Y[4][2] = {};   // (SPLIT 1) outputs of the block before
 
-        // SPLIT 2: Z and O are sums over the channels of both warps of a row group. Each hands its part of Z over, and of O
-        // that of the other's tokens (scaled, with the next block's Z), in two buffers taken in turn: what is written
-        // for block c + 2 comes after a turn of the barrier that follows the other's reads for block c.
-        auto mine = [&](uint32_t area, int size, int c, int of) {
-            return sm + area + (((c & 1) * L::CHAIN + grp + L::GROUPS * of) * size + lane * 16);
+        // SPLIT 2: Z is a sum over the channels of both warps of a row group, each of which hands its part over, in two
+        // buffers taken in turn: what is written for block c + 2 comes after a turn of the barrier that follows the
+        // other's reads for block c.
+        auto zx = [&](int c, int of) {
+            return sm + L::ZX + ((c & 1) * L::CHAIN + grp + L::GROUPS * of) * 2048 + lane * 16;
         };
-        float Op[OT][4];   // SPLIT 2: outputs of the block before, without the other's part
-        auto swapped = [&](int c) {   // both warps of the group have written for block c
-            __syncwarp();
-            const bool ok = mbar_wait_or_abort(&swap[grp], c & 1, abort_flag);
-            return __all_sync(0xffffffffu, ok);
-        };
-        auto join_out = [&](int c) {   // outputs of block c, whole and rounded
-#pragma unroll
-            for (int n = 0; n < OT; ++n) {
-                const float4 y = *reinterpret_cast<const float4*>(mine(L::OX, 1024, c, 1 - part) + 512 * n);
-                Y[n][0] = pack_bf16(Op[n][0] + y.x, Op[n][1] + y.y);
-                Y[n][1] = pack_bf16(Op[n][2] + y.z, Op[n][3] + y.w);
-            }
-        };
-
         for (int c = 0; c < it.blocks; ++c) {
             const int s = c % STAGES;
             const uint32_t st = sbase + s * L::STAGE;
-            bool ok = mbar_wait_or_abort(&full[c % L::FULL], (c / L::FULL) & 1, abort_flag) &&
-                      mbar_wait_or_abort(&ready[s], (c / STAGES) & 1, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) {
+            bool ok = here(c);
+            if (SPLIT > 1 && c >= 2) ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&taken[(c & 1) * L::GROUPS + grp], ((c >> 1) - 1) & 1, abort_flag));
+            if (!ok) {
                 failed = true;
                 break;
             }
+            const uint32_t buf = (c & 1) * L::OUT + grp, xo = sbase + L::XO + buf * (DK / 16) * 512 + lane * 16;
             // ---- Z = X K^T, both parts of X; the block before's outputs leave meanwhile ----
             float Z[4][4] = {}, O[4][4] = {};
 #pragma unroll
@@ -483,45 +587,36 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 mma_16816(Z[1], hi, b0[2], b0[3]);
                 mma_16816(Z[2], hi, b1[0], b1[1]);
                 mma_16816(Z[3], hi, b1[2], b1[3]);
-                if (SPLIT == 1 && x < 4) store_out(x, c - 1);
+                if (SPLIT == 1 && x < 4) store_out(op, x, c - 1, Y[x]);
+                if (SPLIT > 1) st_shared_4(xo + 512 * xk, hi);
                 mma_16816(Z[0], lo, b0[0], b0[1]);
                 mma_16816(Z[1], lo, b0[2], b0[3]);
                 mma_16816(Z[2], lo, b1[0], b1[1]);
                 mma_16816(Z[3], lo, b1[2], b1[3]);
             }
-            // ---- O = X Q^T, the high part, in two runs between the steps of U --------------
+            // ---- (SPLIT 1) O = X Q^T, the high part, in two runs between the steps of U --------
             auto read_out = [&](int x0, int x1) {
 #pragma unroll
                 for (int x = x0; x < x1; ++x) {
-                    uint32_t hi[4], b0[4], b1[4];
-                    const int xk = NT / 2 * part + x;
-                    const uint32_t at = st + L::Q + (xk / 4) * 4096, ch = (xk % 4) * 2 + bc;
-                    ldsm4(b0, at + sw128_off(16 * part + br, ch));         // (the warp's own tokens first)
-                    ldsm4(b1, at + sw128_off(16 * (1 - part) + br, ch));
-                    hi[0] = pack_bf16(X[2 * x][0], X[2 * x][1]);
-                    hi[1] = pack_bf16(X[2 * x][2], X[2 * x][3]);
-                    hi[2] = pack_bf16(X[2 * x + 1][0], X[2 * x + 1][1]);
-                    hi[3] = pack_bf16(X[2 * x + 1][2], X[2 * x + 1][3]);
-                    mma_16816(O[0], hi, b0[0], b0[1]);
-                    mma_16816(O[1], hi, b0[2], b0[3]);
-                    mma_16816(O[2], hi, b1[0], b1[1]);
-                    mma_16816(O[3], hi, b1[2], b1[3]);
+                    const uint32_t hi[4] = {pack_bf16(X[2 * x][0], X[2 * x][1]), pack_bf16(X[2 * x][2], X[2 * x][3]),
+                                            pack_bf16(X[2 * x + 1][0], X[2 * x + 1][1]), pack_bf16(X[2 * x + 1][2], X[2 * x + 1][3])};
+                    read_step(st, x, hi, O);
                 }
             };
             if constexpr (SPLIT > 1) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
-                    *reinterpret_cast<float4*>(mine(L::ZX, 2048, c, part) + 512 * n) = make_float4(Z[n][0], Z[n][1], Z[n][2], Z[n][3]);
+                    *reinterpret_cast<float4*>(zx(c, part) + 512 * n) = make_float4(Z[n][0], Z[n][1], Z[n][2], Z[n][3]);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&swap[grp]);
-                read_out(0, NT / 2);
-                if (!swapped(c)) {
+                ok = mbar_wait_or_abort(&swap[grp], c & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
                     failed = true;
                     break;
                 }
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    const float4 z = *reinterpret_cast<const float4*>(mine(L::ZX, 2048, c, 1 - part) + 512 * n);
+                    const float4 z = *reinterpret_cast<const float4*>(zx(c, 1 - part) + 512 * n);
                     Z[n][0] += z.x;
                     Z[n][1] += z.y;
                     Z[n][2] += z.z;
@@ -581,59 +676,24 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 mma_16816(U[2], h1, t2[0], t2[1]);
                 mma_16816(U[3], h1, t2[2], t2[3]);
             }
-            if constexpr (SPLIT > 1) {
-                if (c > 0) {
-                    join_out(c - 1);
-#pragma unroll
-                    for (int n = 0; n < OT; ++n) store_out(n, c - 1);
-                }
-            } else {
-                read_out(NT / 4, NT / 2);
-            }
+            if constexpr (SPLIT == 1) read_out(NT / 4, NT / 2);
             // ---- O = G O + U P^T; X = G_31 X + (U D_31) K --------------------------------------
             uint32_t h0[4], l0[4], h1[4], l1[4];
             const float gc = vec[2 * C + C - 1];
-            {
+            if constexpr (SPLIT > 1) {   // half of U by each warp
+                if (part == 0) split_tiles(U[0], U[1], h0, l0);
+                else split_tiles(U[2], U[3], h0, l0);
+                const uint32_t uo = sbase + L::UO + buf * 2048 + part * 1024 + lane * 16;
+                st_shared_4(uo, h0);
+                st_shared_4(uo + 512, l0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&given[(c & 1) * L::GROUPS + grp]);
+            } else {
                 uint32_t t0[4], t1[4], t2[4];
-                const uint32_t tp = st + L::P + br * kTStride + bc * 16;
-                if (SPLIT == 1 || part == 0) ldsm4(t0, tp);
-                if (SPLIT == 1 || part == 1) {
-                    ldsm4(t1, tp + 16 * kTStride);
-                    ldsm4(t2, tp + 16 * kTStride + 32);
-                }
+                load_p(st, t0, t1, t2);
                 split_tiles(U[0], U[1], h0, l0);
                 split_tiles(U[2], U[3], h1, l1);
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 g = *reinterpret_cast<const float2*>(vec + 2 * C + (8 * n + 16 * part) % C + 2 * cq);
-                    O[n][0] *= g.x;
-                    O[n][1] *= g.y;
-                    O[n][2] *= g.x;
-                    O[n][3] *= g.y;
-                }
-                if (SPLIT == 1 || part == 0) {   // tokens 0 .. 15
-                    mma_16816(O[0], h0, t0[0], t0[1]);
-                    mma_16816(O[1], h0, t0[2], t0[3]);
-                    mma_16816(O[0], l0, t0[0], t0[1]);
-                    mma_16816(O[1], l0, t0[2], t0[3]);
-                }
-                if (SPLIT == 1 || part == 1) {   // tokens 16 .. 31
-                    constexpr int n = SPLIT == 1 ? 2 : 0;
-                    mma_16816(O[n], h0, t1[0], t1[1]);
-                    mma_16816(O[n + 1], h0, t1[2], t1[3]);
-                    mma_16816(O[n], l0, t1[0], t1[1]);
-                    mma_16816(O[n + 1], l0, t1[2], t1[3]);
-                    mma_16816(O[n], h1, t2[0], t2[1]);
-                    mma_16816(O[n + 1], h1, t2[2], t2[3]);
-                    mma_16816(O[n], l1, t2[0], t2[1]);
-                    mma_16816(O[n + 1], l1, t2[2], t2[3]);
-                }
-                if constexpr (SPLIT > 1) {
-#pragma unroll
-                    for (int n = 0; n < OT; ++n)
-                        *reinterpret_cast<float4*>(mine(L::OX, 1024, c, part) + 512 * n) =
-                            make_float4(O[OT + n][0], O[OT + n][1], O[OT + n][2], O[OT + n][3]);
-                }
+                finish_out(vec, t0, t1, t2, h0, l0, h1, l1, O);
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -666,38 +726,18 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
                 mma_16816(X[n], l1, b1[0], b1[1]);
                 mma_16816(X[n + 1], l1, b1[2], b1[3]);
             }
-            // this warp has read the stage: the last one to say so reloads it
-            __syncwarp();
-            if (lane == 0) {
-                int before;
-                asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(&left[s])) : "memory");
-                if (before == L::CHAIN - 1 && c + STAGES < it.blocks) {
-                    left[s] = 0;
-                    issue(c + STAGES);
-                }
-            }
+            leave(c);
+            if constexpr (SPLIT == 1) {
 #pragma unroll
-            for (int n = 0; n < OT; ++n) {
-                if constexpr (SPLIT > 1) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) Op[n][i] = O[n][i];
-                } else {
+                for (int n = 0; n < 4; ++n) {
                     Y[n][0] = pack_bf16(O[n][0], O[n][1]);
                     Y[n][1] = pack_bf16(O[n][2], O[n][3]);
                 }
             }
         }
-        if constexpr (SPLIT > 1) {
-            if (!failed) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&swap[grp]);
-                failed = !swapped(it.blocks);
-                if (!failed) join_out(it.blocks - 1);
-            }
-        }
-        if (!failed) {
+        if (SPLIT == 1 && !failed) {
 #pragma unroll
-            for (int n = 0; n < OT; ++n) store_out(n, it.blocks - 1);
+            for (int n = 0; n < 4; ++n) store_out(op, n, it.blocks - 1, Y[n]);
         }
         if (!failed) {
 #pragma unroll
@@ -730,9 +770,13 @@ cudaError_t run_shape(const StepArgs& a, cudaStream_t s, const CUtensorMap& q, c
 
 template <int DK>
 cudaError_t run(const StepArgs& a, cudaStream_t s, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v) {
-    // one request of 2048 tokens, 16 heads, d 64 (d_k 128): 82 (100) us, by CTAs of 64 rows 92 (131); the latter have
-    // two CTAs to an SM and half of the prep, which counts where SMs are short
-    if (chunk_is_alone(a.requests, a.Hv, a.dv, a.sm_count)) return run_shape<Layout<DK, 32, 2, 3, 6>, 1>(a, s, q, k, v);
+    // Rows of 32 while every CTA has an SM: one request of 2048 tokens, 16 heads, d 64 (d_k 128, d_v 64) 66 (82) us, with
+    // 64 rows 92 (131). With 64 rows two CTAs share an SM and half of the prep, which counts where SMs are short.
+    // Two prep warps are enough and disturb the chain less (three: 74 and 93 us), but with more CTAs than half of the
+    // SMs three did better: 32 sequence-heads of 8192 tokens at d 128 363 us, by two prep warps 378.
+    const long long rows32 = static_cast<long long>(a.requests) * a.Hv * (a.dv / 32);
+    if (2 * rows32 <= a.sm_count) return run_shape<Layout<DK, 32, 2, 2, 4>, 1>(a, s, q, k, v);
+    if (chunk_is_alone(a.requests, a.Hv, a.dv, a.sm_count)) return run_shape<Layout<DK, 32, 2, 3, 5>, 1>(a, s, q, k, v);
     return run_shape<Layout<DK, 64, 1, 2, 3>, 2>(a, s, q, k, v);
 }
 
