@@ -398,6 +398,7 @@ class PackedPlan:
         import torch
         self.words = torch.empty(words, dtype=torch.int32, device=device)
         self.cfg = cfg
+        self._maxima = cfg.max_requests, cfg.max_tokens, cfg.slots
         self.requests = self.tokens = 0
         self._views = None
 
@@ -472,6 +473,7 @@ class PackedHandle:
             raise LAError(rc, "la_packed_create failed")
         self._h = h
         self._words = lib().la_packed_plan_words(ctypes.byref(self.cfg))
+        self._maxima = max_requests, max_tokens, slots
 
     def close(self):
         if getattr(self, "_h", None):
@@ -517,10 +519,13 @@ class PackedHandle:
         [requests], free_slots int32 [slots], free_count int32 [1]; slots and
         the free stack are updated in place. ``tokens``: rows of the step's
         packed tensors. Returns ``plan`` (a new one if None)."""
-        if plan is None:
+        if plan is not None:
+            self._own(plan)
+        elif stream is None:
             plan = self.new_plan()
         else:
-            self._own(plan)
+            with self._cuda.stream(stream):   # the memory belongs to the stream that writes it
+                plan = self.new_plan()
         requests = lengths.numel()
         i32, expect = self._i32, self._expect
         expect("lengths", lengths, (requests,), i32)
@@ -535,7 +540,7 @@ class PackedHandle:
         return plan
 
     def _own(self, plan):
-        if plan.words.numel() != self._words or plan.words.get_device() != self._index:
+        if plan._maxima != self._maxima or plan.words.get_device() != self._index:
             raise ValueError("plan: made by a handle of another configuration or device")
 
     def _step(self, call, plan, q, k, v, gate, beta, states, out, stream, *more):

@@ -6,10 +6,11 @@
 //   u_i = beta (v_i - g S_i . k),   S_i = g S_i + u_i k,
 //   o_i = S_i . q = g (old S_i . q) + u_i (k . q)
 //
-// A warp owns a unit of state rows (4 KB) of one request's head: the rows are
-// read once, stay in registers over all the request's tokens and are written
-// once, so a one-token step moves each state once in and once out and HBM
-// bounds it; a request without tokens seen starts from zeros and reads nothing.
+// A warp owns a unit of state rows (4 KB, less where there are few) of one
+// request's head: the rows are read once, stay in registers over all the
+// request's tokens and are written once, so a one-token step moves each state
+// once in and once out and HBM bounds it; a request without tokens seen starts
+// from zeros and reads nothing.
 // Eight lanes share a row (four at d_k 16), each with every eighth 16-byte
 // vector of it, so that a few tokens cost little besides: at d_k 128 four sums
 // over eight lanes where 32 lanes to a row would have sixteen over 32. The two
@@ -20,9 +21,9 @@
 //
 // Measured, d 128, 16 heads, bf16: one token of 256 requests 83 us, 0.96 of the
 // measured copy bandwidth; of 4 requests 3.5 us, the launch and two trips to
-// memory; 400 tokens of 128 requests 53 us, 0.75 of it:
-// there the tokens' arithmetic, about 9 us a token, is in part beside the
-// traffic and in part before it. Tried and slower: the next unit's state into
+// memory; 400 tokens of 128 requests 53 us, 0.75 of it: there the tokens'
+// arithmetic, about 9 us a token, is in part beside the traffic and in part
+// before it. Tried and slower: the next unit's state into
 // shared memory (256 requests 90 us) or L2 (98 us) while one is computed; three
 // CTAs per SM at 80 registers (89 us).
 #include <cuda_bf16.h>
@@ -113,10 +114,14 @@ __device__ __forceinline__ void sums_by_halving(float (&x)[N], int lane) {
 
 // How a warp holds a unit: lane (sub, cl) has vectors cl, cl + LPR, ... of rows p RPP + sub.
 template <int DK>
-struct Unit {
+struct Lanes {
     static constexpr int LPR = DK >= 32 ? 8 : 4;      // lanes per row
     static constexpr int V = DK / (4 * LPR);          // vectors of a row per lane
-    static constexpr int P = kVectors / V;            // row passes
+};
+template <int DK, int P_>
+struct Unit {
+    static constexpr int LPR = Lanes<DK>::LPR, V = Lanes<DK>::V;
+    static constexpr int P = P_;                      // row passes
     static constexpr int RPP = 32 / LPR;              // rows per pass
     static constexpr int R = RPP * P;                 // rows
     static constexpr int Q = LPR / 2;                 // lanes that end with S k (the lower half of a row's), with S q
@@ -202,9 +207,9 @@ struct Where {
     bool fresh;
 };
 // Unit u; false if its request has no part.
-template <int DK, typename IO>
+template <class U, int DK, typename IO>
 __device__ __forceinline__ bool find(const StepArgs& a, int u, Where<IO>& x) {
-    constexpr int R = Unit<DK>::R;
+    constexpr int R = U::R;
     const int uph = (a.dv + R - 1) / R, per_req = a.Hv * uph;   // units per head, per request
     const int hu = u % per_req, h = hu / uph, r0 = hu % uph * R, hk = h / (a.Hv / a.Hk);
     Request rq;
@@ -222,21 +227,21 @@ __device__ __forceinline__ bool find(const StepArgs& a, int u, Where<IO>& x) {
     x.fresh = rq.fresh;
     return true;
 }
-template <int DK>
-__host__ __device__ inline int unit_count(const StepArgs& a) {   // at most 2^14 requests x 2^12 heads x 2^4
-    return a.requests * a.Hv * ((a.dv + Unit<DK>::R - 1) / Unit<DK>::R);
+template <class U>
+__host__ __device__ inline long long unit_count(const StepArgs& a) {
+    return static_cast<long long>(a.requests) * a.Hv * ((a.dv + U::R - 1) / U::R);
 }
 
-template <int DK, typename IO>
+template <int DK, typename IO, int P>
 __global__ void __launch_bounds__(kThreads, 2) step_kernel(const StepArgs a) {
-    using U = Unit<DK>;
+    using U = Unit<DK, P>;
     U s(threadIdx.x & 31);
     griddep_launch_dependents();
     griddep_wait();   // the plan and the states of the step before are complete
-    const int units = unit_count<DK>(a), stride = (gridDim.x * kThreads) >> 5;
+    const int units = static_cast<int>(unit_count<U>(a)), stride = (gridDim.x * kThreads) >> 5;
     for (int u = (blockIdx.x * kThreads + threadIdx.x) >> 5; u < units; u += stride) {
         Where<IO> x;
-        if (!find<DK>(a, u, x)) continue;
+        if (!find<U, DK>(a, u, x)) continue;
         s.load(x.st, x.fresh ? 0 : x.rows);
         Raw<IO> kn[U::V], qn[U::V];   // of the next token
         float vn[U::M], gn, bn;
@@ -278,11 +283,19 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const StepArgs a) {
     }
 }
 
+template <int DK, typename IO, int P>
+cudaError_t run_units(const StepArgs& a, cudaStream_t s) {
+    // two CTAs per SM, each warp one unit after another (at most 2^14 requests x 2^12 heads x 2^4 units of 4 KB)
+    const long long grid = (unit_count<Unit<DK, P>>(a) + kThreads / 32 - 1) / (kThreads / 32), most = 2ll * a.sm_count;
+    return launch_pdl(step_kernel<DK, IO, P>, static_cast<unsigned>(grid < most ? grid : most), kThreads, 0, s, a);
+}
 template <int DK, typename IO>
 cudaError_t run(const StepArgs& a, cudaStream_t s) {
-    // two CTAs per SM, each warp one unit after another
-    const long long grid = (unit_count<DK>(a) + kThreads / 32 - 1) / (kThreads / 32), most = 2ll * a.sm_count;
-    return launch_pdl(step_kernel<DK, IO>, static_cast<unsigned>(grid < most ? grid : most), kThreads, 0, s, a);
+    // Units of one pass (4 or 8 rows) while no SM gets more than a CTA of them: a token takes a warp less time. Measured
+    // against units of 4 KB, fp32, four requests of 64 tokens, 8 heads: d 64 25.0 us (27.6), d 128 32.3 (37.5), d_k 16
+    // and d_v 128 20.9 (51.7); six requests of 611 tokens, 8 heads of 64: 75 us (96).
+    if (unit_count<Unit<DK, 1>>(a) <= a.sm_count * (kThreads / 32)) return run_units<DK, IO, 1>(a, s);
+    return run_units<DK, IO, kVectors / Lanes<DK>::V>(a, s);
 }
 
 template <typename IO>

@@ -283,6 +283,23 @@ def test_token_by_token(io, dk, dv, lens):
     assert torch.equal(x["states"][others], before[others])
 
 
+@pytest.mark.parametrize("io,dk,dv", [("bf16", 128, 128), ("fp32", 128, 16), ("fp32", 64, 64), ("bf16", 16, 128), ("fp32", 32, 32), ("bf16", 64, 128)])
+def test_token_by_token_for_many_requests(io, dk, dv):
+    # more state rows than a warp each could hold at once
+    rng = random.Random(dk + dv)
+    lens = [rng.choice((0, 1, 1, 1, 2, 5, 9)) for _ in range(220)]
+    x, pool = draw(lens, 2, 8, dk, dv, io, seed=dk * 3 + dv)
+    h = handle_for(lens, 2, 8, dk, dv, io, pool)
+    seen = [r % 3 for r in range(len(lens))]
+    plan = make_plan(h, lens, seen, x["slots"])
+    before = x["states"].clone()
+    out = h.decode_step(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"])
+    assert h.status() == la.LA_OK
+    check(x, lens, seen, before, out, io, 1, only=range(0, 220, 7))
+    others = [s for s in range(pool) if s not in [x["slots"][r] for r, n in enumerate(lens) if n > 0]]
+    assert torch.equal(x["states"][others], before[others])
+
+
 def test_default_form_by_type():
     # fp32 and small heads have no blockwise form: the default is token by token, bit for bit the decode step
     for io, dk, dv in (("fp32", 64, 64), ("bf16", 32, 64), ("bf16", 64, 32)):
@@ -521,6 +538,11 @@ def test_python_refuses_wrong_tensors():
         h.plan(i32([1]), i32([1]).long(), i32([0]), i32([0] * pool), i32([0]), tokens=1)
     with pytest.raises(ValueError):   # a plan of other maxima
         h.forward(handle_for([1], 2, 2, 64, 64, "bf16", pool).new_plan(), *good)
+    heads = dict(H_k=1, H_v=1, d_k=16, d_v=16)   # of as many words, laid out otherwise
+    one, other = la.PackedHandle(max_requests=2, max_tokens=4, slots=16, **heads), la.PackedHandle(max_requests=2, max_tokens=8, slots=8, **heads)
+    assert one.new_plan().words.numel() == other.new_plan().words.numel()
+    with pytest.raises(ValueError):
+        one.plan(i32([1]), i32([0]), i32([-1]), i32([0] * 16), i32([1]), tokens=1, plan=other.new_plan())
     torch.cuda.synchronize()
     assert torch.equal(before, x["states"])
 
