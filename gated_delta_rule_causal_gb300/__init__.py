@@ -462,6 +462,7 @@ class PackedHandle:
         self.H_k, self.H_v, self.d_k, self.d_v, self.slots = H_k, H_v, d_k, d_v, slots
         # what every call looks up: a step of a few tokens takes the GPU less time than its enqueueing takes the host
         self._index, self._i32, self._f32 = dev.index, torch.int32, torch.float32
+        self._pool = (slots, H_v, d_v, d_k)
         self._empty, self._cuda = torch.empty, torch.cuda
         self._current_stream = torch._C._cuda_getCurrentRawStream   # the number in torch.cuda.current_stream(device)
         self._lib = lib()
@@ -544,25 +545,37 @@ class PackedHandle:
             raise ValueError("plan: made by a handle of another configuration or device")
 
     def _step(self, call, plan, q, k, v, gate, beta, states, out, stream, *more):
-        n, hv, dv = plan.tokens, self.H_v, self.d_v
-        self._own(plan)
-        qs = self._rows("q", q, n, self.H_k, self.d_k)
-        ks = self._rows("k", k, n, self.H_k, self.d_k)
-        vs = self._rows("v", v, n, hv, dv)
-        f32, expect = self._f32, self._expect
-        expect("gate", gate, (n, hv), f32)
-        expect("beta", beta, (n, hv), f32)
-        expect("states", states, (self.slots, hv, dv, self.d_k), f32)
+        n, hk, hv, dk, dv = plan.tokens, self.H_k, self.H_v, self.d_k, self.d_v
+        index, dtype, f32 = self._index, self.dtype, self._f32
+        key, value, scalar = (n, hk, dk), (n, hv, dv), (n, hv)
+        qs, ks, vs = q.stride(), k.stride(), v.stride()
+        # the usual case in one go; anything else goes through the checks one by one
+        if (plan._maxima == self._maxima and plan.words.get_device() == index and n > 1 and
+                q.dtype is dtype and q.get_device() == index and q.shape == key and qs[1] == dk and qs[2] == 1 and
+                k.dtype is dtype and k.get_device() == index and k.shape == key and ks[1] == dk and ks[2] == 1 and
+                v.dtype is dtype and v.get_device() == index and v.shape == value and vs[1] == dv and vs[2] == 1 and
+                gate.dtype is f32 and gate.get_device() == index and gate.shape == scalar and gate.is_contiguous() and
+                beta.dtype is f32 and beta.get_device() == index and beta.shape == scalar and beta.is_contiguous() and
+                states.dtype is f32 and states.get_device() == index and states.shape == self._pool and states.is_contiguous()):
+            qs, ks, vs = qs[0], ks[0], vs[0]
+        else:
+            self._own(plan)
+            qs = self._rows("q", q, n, hk, dk)
+            ks = self._rows("k", k, n, hk, dk)
+            vs = self._rows("v", v, n, hv, dv)
+            self._expect("gate", gate, scalar, f32)
+            self._expect("beta", beta, scalar, f32)
+            self._expect("states", states, self._pool, f32)
         if out is not None:
-            expect("out", out, (n, hv, dv), self.dtype)
+            self._expect("out", out, value, dtype)
         elif stream is None:
-            out = self._empty((n, hv, dv), dtype=self.dtype, device=self.device)
+            out = self._empty(value, dtype=dtype, device=self.device)
         else:
             with self._cuda.stream(stream):   # the memory belongs to the stream that writes it
-                out = self._empty((n, hv, dv), dtype=self.dtype, device=self.device)
+                out = self._empty(value, dtype=dtype, device=self.device)
         rc = call(self._h, plan.words.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(),
                   beta.data_ptr(), states.data_ptr(), out.data_ptr(), plan.requests, n, qs, ks, vs, *more,
-                  self._stream(stream))
+                  self._current_stream(index) if stream is None else stream.cuda_stream)
         if rc != LA_OK:
             self._check(rc)
         return out
