@@ -28,16 +28,17 @@
 // still formed. V^T T'^T, Q X^T, the scaling of X by G_63 and of O by G, and the
 // outputs run in the gaps.
 //
-// Measured, bf16, d 128: two requests of 8192 tokens, 16 heads (32 CTAs): 427 us,
-// 3.3 us or 6400 clocks a block; 96 requests of 65536 tokens together, 16 heads:
-// 446 us; 16 of 8191, 32 heads: 130 us. Of a block's clocks MMAs take 2700 (the
-// tensor pipe is 34 % busy), the chain's conversions 2500; the prep of a block
-// takes 10000 to 12000, half of which two groups make good. Issue slots are 53 %
-// busy, and 8 % of the warps' waiting is for instructions: 84 KB of code in
-// which every role has its own loop, where code beyond 32 KB was measured to
-// come at 3 clocks an instruction when all of it is walked in turn. Smaller was
-// slower all the same, the long requests as before: waits as a function (64 to
-// 73 KB) 507 us, conversions too 518, MMAs by one rolled loop 909.
+// Measured, bf16, d 128: two requests of 8192 tokens, 16 heads (32 CTAs, where the
+// blocks of 32 are faster): 427 us, 3.3 us or 6400 clocks a block; 96 requests of
+// 65536 tokens together, 16 heads: 447 us; 16 of 8191, 32 heads: 130 us. Of a
+// block's clocks MMAs take 2700 (the tensor pipe is 34 % busy), the chain's
+// conversions 2500; the prep of a block takes 10000 to 12000, half of which two
+// groups make good. Issue slots are 53 % busy, and 8 % of the warps' waiting is
+// for instructions: 84 KB of code in which every role has its own loop, where
+// code beyond 32 KB was measured to come at 3 clocks an instruction when all of
+// it is walked in turn. Smaller was slower all the same, for the two requests of
+// 8192: waits as a function (73 KB) 507 us, conversions too 518, MMAs by one
+// rolled loop 909.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
