@@ -77,9 +77,13 @@ struct StepArgs {
     int io;               // Io
     int sm_count;
     int* status;
+    int above, upto;      // only requests of above < tokens <= upto
 };
 // Token by token, CUDA cores: any supported head size and type.
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
+// The same beside the blockwise launch before it on the stream, which takes the step's other requests (bf16, dk in
+// {64, 128}).
+cudaError_t launch_step_beside(const StepArgs& a, cudaStream_t s);
 // Whether every CTA of 32 state rows would have an SM to itself.
 inline bool chunk_is_alone(int requests, int Hv, int dv, int sm_count) {
     return static_cast<long long>(requests) * Hv * (dv / 32) <= sm_count;
@@ -111,15 +115,18 @@ struct Request {
     int row0, len, slot;
     bool fresh;   // no token seen: the state starts at zero
 };
+template <bool PAST = false>   // past the SM's own cache
 __device__ __forceinline__ bool read_request(const StepArgs& a, int rank, Request& x) {
-    const int n = a.plan[4];
-    const int4 w = reinterpret_cast<const int4*>(a.plan + a.lay.items())[rank];
+    const int* count = a.plan + 4;
+    const int4* item = reinterpret_cast<const int4*>(a.plan + a.lay.items()) + rank;
+    const int n = PAST ? __ldcg(count) : *count;
+    const int4 w = PAST ? __ldcg(item) : *item;
     x.row0 = w.x;
     x.len = w.y;
     x.slot = w.z;
     x.fresh = w.w <= 0;
     return rank < n && x.slot >= 0 && x.slot < a.lay.S && x.len > 0 && x.len <= a.rows && x.row0 >= 0 &&
-           x.row0 <= a.rows - x.len;
+           x.row0 <= a.rows - x.len && x.len > a.above && x.len <= a.upto;
 }
 
 }  // namespace packed

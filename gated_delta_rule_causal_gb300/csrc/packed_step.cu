@@ -40,23 +40,29 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVectors = 8;   // 16-byte vectors of the state per lane: loads in flight
 
+// Loads of what other launches write; PAST: past the SM's own cache, for a launch that does not begin with a wait for the
+// one before it.
+template <bool PAST, typename T>
+__device__ __forceinline__ T fetch(const T* p) {
+    return PAST ? __ldcg(p) : __ldg(p);
+}
 // Four elements as they are loaded, and as numbers.
-template <typename IO> struct Raw;
-template <> struct Raw<float> {
+template <typename IO, bool PAST> struct Raw;
+template <bool PAST> struct Raw<float, PAST> {
     float4 u;
-    __device__ __forceinline__ void load(const float* p) { u = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void load(const float* p) { u = fetch<PAST>(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ float4 get() const { return u; }
 };
-template <> struct Raw<__nv_bfloat16> {
+template <bool PAST> struct Raw<__nv_bfloat16, PAST> {
     uint2 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = fetch<PAST>(reinterpret_cast<const uint2*>(p)); }
     __device__ __forceinline__ float4 get() const {
         const float2 a = unpack_bf16(u.x), b = unpack_bf16(u.y);
         return make_float4(a.x, a.y, b.x, b.y);
     }
 };
-__device__ __forceinline__ float ld1(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float ld1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+template <bool PAST> __device__ __forceinline__ float ld1(const float* p) { return fetch<PAST>(p); }
+template <bool PAST> __device__ __forceinline__ float ld1(const __nv_bfloat16* p) { return __bfloat162float(fetch<PAST>(p)); }
 __device__ __forceinline__ void st1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void st1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 // Two fp32 values in one register pair: one instruction for two multiply-adds.
@@ -180,12 +186,15 @@ struct Unit {
     }
     // The unit's rows to or from memory (vectors cl + LPR w of row p RPP + sub of `st`)
     __device__ __forceinline__ size_t at(int p, int w) const { return static_cast<size_t>(p * RPP + sub) * DK + 4 * (cl + LPR * w); }
+    template <bool PAST>
     __device__ __forceinline__ void load(const float* st, int rows) {
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int w = 0; w < V; ++w)
-                S[p][w] = pairs(p * RPP + sub < rows ? __ldcs(reinterpret_cast<const float4*>(st + at(p, w))) : make_float4(0.f, 0.f, 0.f, 0.f));
+            for (int w = 0; w < V; ++w) {
+                const float4* from = reinterpret_cast<const float4*>(st + at(p, w));
+                S[p][w] = pairs(p * RPP + sub < rows ? (PAST ? __ldcg(from) : __ldcs(from)) : make_float4(0.f, 0.f, 0.f, 0.f));
+            }
     }
     __device__ __forceinline__ void store(float* st, int rows) const {
 #pragma unroll
@@ -207,13 +216,13 @@ struct Where {
     bool fresh;
 };
 // Unit u; false if its request has no part.
-template <class U, int DK, typename IO>
+template <class U, int DK, bool PAST, typename IO>
 __device__ __forceinline__ bool find(const StepArgs& a, int u, Where<IO>& x) {
     constexpr int R = U::R;
     const int uph = (a.dv + R - 1) / R, per_req = a.Hv * uph;   // units per head, per request
     const int hu = u % per_req, h = hu / uph, r0 = hu % uph * R, hk = h / (a.Hv / a.Hk);
     Request rq;
-    if (!read_request(a, u / per_req, rq)) return false;
+    if (!read_request<PAST>(a, u / per_req, rq)) return false;
     const size_t row = static_cast<size_t>(rq.row0);
     x.q = static_cast<const IO*>(a.q) + row * a.q_stride + hk * DK;
     x.k = static_cast<const IO*>(a.k) + row * a.k_stride + hk * DK;
@@ -232,18 +241,22 @@ __host__ __device__ inline long long unit_count(const StepArgs& a) {
     return static_cast<long long>(a.requests) * a.Hv * ((a.dv + U::R - 1) / U::R);
 }
 
-template <int DK, typename IO, int P>
+// BESIDE: the launch before this one runs other requests of the same step, and lets this one start once it has waited
+// for what came before it; no row or slot is in both.
+template <int DK, typename IO, int P, bool BESIDE>
 __global__ void __launch_bounds__(kThreads, 2) step_kernel(const StepArgs a) {
     using U = Unit<DK, P>;
     U s(threadIdx.x & 31);
-    griddep_launch_dependents();
-    griddep_wait();   // the plan and the states of the step before are complete
+    if constexpr (!BESIDE) {   // (beside, the next launch would only wait on the same SMs)
+        griddep_launch_dependents();
+        griddep_wait();   // the plan and the states of the step before are complete
+    }
     const int units = static_cast<int>(unit_count<U>(a)), stride = (gridDim.x * kThreads) >> 5;
     for (int u = (blockIdx.x * kThreads + threadIdx.x) >> 5; u < units; u += stride) {
         Where<IO> x;
-        if (!find<U, DK>(a, u, x)) continue;
-        s.load(x.st, x.fresh ? 0 : x.rows);
-        Raw<IO> kn[U::V], qn[U::V];   // of the next token
+        if (!find<U, DK, BESIDE>(a, u, x)) continue;
+        s.template load<BESIDE>(x.st, x.fresh ? 0 : x.rows);
+        Raw<IO, BESIDE> kn[U::V], qn[U::V];   // of the next token
         float vn[U::M], gn, bn;
         auto load = [&]() {
 #pragma unroll
@@ -252,9 +265,9 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const StepArgs a) {
                 qn[w].load(x.q + 4 * (s.cl + U::LPR * w));
             }
 #pragma unroll
-            for (int i = 0; i < U::M; ++i) vn[i] = s.own_row(i) < x.rows ? ld1(x.v + s.own_row(i)) : 0.f;
-            gn = __ldg(x.gate);
-            bn = __ldg(x.beta);
+            for (int i = 0; i < U::M; ++i) vn[i] = s.own_row(i) < x.rows ? ld1<BESIDE>(x.v + s.own_row(i)) : 0.f;
+            gn = fetch<BESIDE>(x.gate);
+            bn = fetch<BESIDE>(x.beta);
         };
         load();
         for (int t = 0; t < x.len; ++t) {
@@ -281,21 +294,24 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const StepArgs a) {
         }
         s.store(x.st, x.rows);
     }
+    // Whoever waits for this launch waits for both: one warp stays until the other is complete. (All of them, 304 CTAs,
+    // slow what runs beside them down.)
+    if (BESIDE && blockIdx.x == 0 && threadIdx.x < 32) griddep_wait();
 }
 
-template <int DK, typename IO, int P>
+template <int DK, typename IO, int P, bool BESIDE>
 cudaError_t run_units(const StepArgs& a, cudaStream_t s) {
     // two CTAs per SM, each warp one unit after another (at most 2^14 requests x 2^12 heads x 2^4 units of 4 KB)
     const long long grid = (unit_count<Unit<DK, P>>(a) + kThreads / 32 - 1) / (kThreads / 32), most = 2ll * a.sm_count;
-    return launch_pdl(step_kernel<DK, IO, P>, static_cast<unsigned>(grid < most ? grid : most), kThreads, 0, s, a);
+    return launch_pdl(step_kernel<DK, IO, P, BESIDE>, static_cast<unsigned>(grid < most ? grid : most), kThreads, 0, s, a);
 }
 template <int DK, typename IO>
 cudaError_t run(const StepArgs& a, cudaStream_t s) {
     // Units of one pass (4 or 8 rows) while no SM gets more than a CTA of them: a token takes a warp less time. Measured
     // against units of 4 KB, fp32, four requests of 64 tokens, 8 heads: d 64 25.0 us (27.6), d 128 32.3 (37.5), d_k 16
     // and d_v 128 20.9 (51.7); six requests of 611 tokens, 8 heads of 64: 75 us (96).
-    if (unit_count<Unit<DK, 1>>(a) <= a.sm_count * (kThreads / 32)) return run_units<DK, IO, 1>(a, s);
-    return run_units<DK, IO, kVectors / Lanes<DK>::V>(a, s);
+    if (unit_count<Unit<DK, 1>>(a) <= a.sm_count * (kThreads / 32)) return run_units<DK, IO, 1, false>(a, s);
+    return run_units<DK, IO, kVectors / Lanes<DK>::V, false>(a, s);
 }
 
 template <typename IO>
@@ -311,6 +327,11 @@ cudaError_t run_dk(const StepArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t launch_step_beside(const StepArgs& a, cudaStream_t s) {
+    if (a.io == kBf16 && a.dk == 64) return run_units<64, __nv_bfloat16, kVectors / Lanes<64>::V, true>(a, s);
+    if (a.io == kBf16 && a.dk == 128) return run_units<128, __nv_bfloat16, kVectors / Lanes<128>::V, true>(a, s);
+    return cudaErrorInvalidValue;
+}
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s) {
     return a.io == kFp32 ? run_dk<float>(a, s) : run_dk<__nv_bfloat16>(a, s);
 }

@@ -472,14 +472,15 @@ int la_packed_plan(la_packed* h, const int* lengths, const int* seen, int* slots
  * la_packed_plan.
  *   chunk  0 = default: in blocks where there is such a form (bf16, d_k and
  *          d_v in {64, 128}), of 32 or 64 tokens (by d_k, d_v and the step's
- *          size, whichever measured faster), else token by token. 1 = token
- *          by token. 32, 64 = blocks of so many (64: d_v 128), or
+ *          size, whichever measured faster), else token by token; in larger
+ *          steps requests of up to four tokens run token by token beside the
+ *          others, in a second launch. 1 = token by token. 32, 64 = blocks of so many (64: d_v 128), or
  *          LA_ERR_UNSUPPORTED where there is no such form.
  * The blockwise form keeps the state to a few 10^-6 of itself (q, k and v enter
  * its matrix products exactly, what the state depends on in two bf16 parts,
  * 2^-16 each); outputs are off by a few roundings to bf16. A NaN or infinity in
  * a request's rows may reach that request's outputs from the start of its
- * block on. One launch, no workspace.
+ * block on. One launch (or two, see chunk 0), no workspace.
  * Errors: LA_ERR_INVALID_ARG (a NULL or rows that overlap, sizes above the
  * handle's), LA_ERR_MISALIGNED (a pointer or a row not 16-byte aligned; gate
  * and beta need 4 bytes),

@@ -338,6 +338,49 @@ def test_many_requests_and_heads(dk, dv, chunk):
         assert torch.equal(out[a:e], out2[a:e])
 
 
+@pytest.mark.parametrize("dk,dv,chunk", [(128, 128, 64), (64, 64, 32), (128, 64, 32)])
+def test_a_larger_step_runs_its_short_requests_token_by_token(dk, dv, chunk):
+    # bit for bit the two forms' own results; and call after call without a pause, eager and from a graph
+    rng = random.Random(dk + dv)
+    lens = [rng.choice((0, 1, 1, 2, 3, 4, 4, 5, 6, 40, 130, 300)) for _ in range(45)]
+    x, pool = draw(lens, 4, 8, dk, dv, "bf16", seed=dk - dv + 200)
+    h = handle_for(lens, 4, 8, dk, dv, "bf16", pool)
+    plan = make_plan(h, lens, [r % 2 for r in range(len(lens))], x["slots"])
+    args = [x[n] for n in ("q", "k", "v", "gate", "beta")]
+    start = x["states"]
+    mixed, blocks, tokens = start.clone(), start.clone(), start.clone()
+    o1 = h.forward(plan, *args, mixed)
+    assert h.last_launches() == 2
+    o2 = h.forward(plan, *args, blocks, chunk=chunk)
+    assert h.last_launches() == 1
+    o3 = h.decode_step(plan, *args, tokens)
+    assert h.status() == la.LA_OK
+    for r, n in enumerate(lens):
+        a, e = int(plan.offsets[r]), int(plan.offsets[r + 1])
+        o, st = (o3, tokens) if n <= 4 else (o2, blocks)
+        assert torch.equal(o1[a:e], o[a:e]) and torch.equal(mixed[x["slots"][r]], st[x["slots"][r]]), r
+    plan = make_plan(h, lens, [5] * len(lens), x["slots"])   # states go on from call to call
+    want, got, replayed = start.clone(), start.clone(), start.clone()
+    for _ in range(6):
+        o1 = h.forward(plan, *args, want)
+        torch.cuda.synchronize()
+    for _ in range(6):
+        o2 = h.forward(plan, *args, got)
+    assert torch.equal(got, want)
+    out = torch.empty_like(o1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            h.forward(plan, *args, replayed, out=out)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert h.status() == la.LA_OK and torch.equal(replayed, want)
+    for r, n in enumerate(lens):
+        a, e = int(plan.offsets[r]), int(plan.offsets[r + 1])
+        assert torch.equal(o2[a:e], o1[a:e]) and torch.equal(out[a:e], o1[a:e])
+
+
 def test_a_prompt_in_two_steps_is_the_prompt():
     lens = [200]
     x, pool = draw(lens, 1, 2, 128, 128, "bf16", seed=12)
