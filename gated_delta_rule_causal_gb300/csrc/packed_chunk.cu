@@ -389,7 +389,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CU
         const int splits = a.dv / L::ROWS;
         const int per_req = a.Hv * splits;
         const int rank = blockIdx.x / per_req, hs = blockIdx.x % per_req;
-        griddep_launch_dependents();
+        if (a.above) griddep_launch_dependents();   // a launch for the shorter requests follows, which may run beside this one
         if (!read_request(a, rank, it.rq)) return;
         it.head = hs / splits;
         it.split = hs % splits;

@@ -629,7 +629,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
     griddep_wait();
     {   // requests without a part come last: where this CTA's has none, nobody's after it has
         Request rq;
-        griddep_launch_dependents();
+        if (a.above) griddep_launch_dependents();   // a launch for the shorter requests follows, which may run beside this one
         if (!read_request(a, blockIdx.x / a.Hv, rq)) return;
     }
     if (warp == 0) tmem_alloc(&B->tmem, L::TMEM_COLS);
