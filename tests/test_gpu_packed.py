@@ -264,6 +264,34 @@ def test_nothing_leaks_between_requests(bad, chunk):
     check(x, lens, seen, before, out, "bf16", chunk, only=(0, 2, 4))
 
 
+@pytest.mark.parametrize("dk,dv,chunk", [(64, 128, 64), (128, 128, 64), (64, 64, 32), (128, 128, 32)])
+def test_a_last_block_is_cleared_in_its_own_tile(dk, dv, chunk):
+    # whole blocks, then one whose rows past the request's end hold the next request's NaN: whoever clears them has not
+    # looked at the tiles of the blocks before. Many CTAs, so that loads take their time; the requests between the NaN
+    # ones give the bits that they give beside finite neighbours
+    rng = random.Random(dk + dv)
+    blocks = [rng.choice((2, 3, 4, 5, 7)) * chunk + rng.choice((1, 2, chunk // 2, chunk - 1)) for _ in range(24)]
+    x, pool = draw(blocks, 8, 16, dk, dv, "bf16", seed=dk * 5 + dv)
+    h = handle_for(blocks, 8, 16, dk, dv, "bf16", pool)
+    seen = [r % 3 for r in range(len(blocks))]
+    plan = make_plan(h, blocks, seen, x["slots"])
+    before, starts = x["states"].clone(), np.concatenate([[0], np.cumsum(blocks)])
+    args = [x[n] for n in ("q", "k", "v", "gate", "beta")]
+    clean = h.forward(plan, *args, x["states"], chunk=chunk)
+    assert h.status() == la.LA_OK
+    check(x, blocks, seen, before, clean, "bf16", chunk, only=(0, 10))
+    for r in range(1, len(blocks), 2):
+        for t in args:
+            t[starts[r]:starts[r + 1]] = float("nan")
+    for _ in range(10):
+        states = before.clone()
+        out = h.forward(plan, *args, states, chunk=chunk)
+        assert h.status() == la.LA_OK
+        for r in range(0, len(blocks), 2):
+            assert torch.equal(out[starts[r]:starts[r + 1]], clean[starts[r]:starts[r + 1]]), r
+            assert torch.equal(states[x["slots"][r]], x["states"][x["slots"][r]]), r
+
+
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
 @pytest.mark.parametrize("dk,dv", [(16, 16), (32, 64), (64, 16), (128, 128), (16, 128), (128, 32), (64, 64), (32, 16)])
 @pytest.mark.parametrize("lens", [[1, 1, 1], [0, 3, 1, 17]], ids=["ones", "few"])
