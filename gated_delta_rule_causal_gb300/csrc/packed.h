@@ -124,7 +124,7 @@ __device__ __forceinline__ bool read_request(const StepArgs& a, int rank, Reques
     x.row0 = w.x;
     x.len = w.y;
     x.slot = w.z;
-    x.fresh = w.w <= 0;
+    x.fresh = w.w == 0;
     return rank < n && x.slot >= 0 && x.slot < a.lay.S && x.len > 0 && x.len <= a.rows && x.row0 >= 0 &&
            x.row0 <= a.rows - x.len && x.len > a.above && x.len <= a.upto;
 }

@@ -241,6 +241,22 @@ def test_prefill_gates(gates, dk, dv, chunk):
     check(x, lens, [0, 3], before, out, "bf16", chunk)
 
 
+@pytest.mark.parametrize("chunk", [1, 32, 64, 0])
+def test_only_requests_that_have_seen_nothing_start_from_zeros(chunk):
+    # any other number, a negative one too, goes on from the slot's state (chunk 0: short requests beside the others)
+    lens = [70, 2, 40, 1, 9] * 4 if chunk == 0 else [70, 2, 40]
+    Hk, Hv = (4, 8) if chunk == 0 else (1, 2)
+    x, pool = draw(lens, Hk, Hv, 128, 128, "bf16", seed=17)
+    h = handle_for(lens, Hk, Hv, 128, 128, "bf16", pool)
+    seen = [(-3, 0, -2 ** 31, -1, 2 ** 31 - 100)[r % 5] for r in range(len(lens))]
+    plan = make_plan(h, lens, seen, x["slots"])
+    assert plan.counts.tolist() == [sum(lens), len(lens), 0, 0]
+    before = x["states"].clone()
+    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], chunk=chunk)
+    assert h.status() == la.LA_OK and h.last_launches() == (2 if chunk == 0 else 1)
+    check(x, lens, seen, before, out, "bf16", chunk or 64)
+
+
 @pytest.mark.parametrize("chunk", [1, 32, 64])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_nothing_leaks_between_requests(bad, chunk):
