@@ -106,11 +106,12 @@ struct __align__(16) Work {
 
 // Barriers, in shared memory.
 struct Bars {
-    // (six of those that a prep group waits for, block nb's at nb % 6: a wait for a turn takes the turn two before
-    // for it while the one before is not complete. The group looks at tiles only where a block has rows past the
-    // request's end, so it may have seen none of block nb - 2's or nb - 3's; block nb - 6's are long complete)
+    // (A wait for a turn takes the turn two before for it while the one before is not complete, so whoever waits has to
+    // know that one complete. A prep group looks at K's arrival only where a block has rows past the request's end:
+    // six of them, block nb's at nb % 6, whose turn before, block nb - 6's, the group's T' of block nb - 4 came after.)
     uint64_t kq_full[6], kq_free[kTiles];        // TMA; MMA: every product of the block is done
-    uint64_t v_full[6], v_free[2];               // TMA; copier: the output tile over V has left
+    uint64_t v_full[2], v_free[2];               // TMA; copier: the output tile over V has left
+    uint64_t v_clear[2];                         // work warp: V's rows past the request's end are zero
     uint64_t vec_free[6];                        // converters: the block's vectors are read (16)
     uint64_t ot_full[2];                         // converters: the output tile is written (16)
     uint64_t ready[2], t_free[2], p_free[2];     // prep warps: T', P and vectors (4); MMA: T', P is read
@@ -390,16 +391,13 @@ __device__ __forceinline__ bool prep_warps(const StepArgs& a, uint8_t* sm, uint3
             ok = nb < kTiles || wait(&B->vec_free[b3], six.phase ^ (six.s < 3 ? 1 : 0));
             if (ok) write_gates(vec, gn, bn);
         }
-        if (more && n < C) {   // rows of the next request (or past the tensor): K and V zero, so that they leave the state alone
-            ok = ok && wait(&B->kq_full[six.s], six.phase) && wait(&B->v_full[six.s], six.phase);
+        if (more && n < C) {   // rows of the next request (or past the tensor): K (and V) zero, so that they leave the state alone
+            ok = ok && wait(&B->kq_full[six.s], six.phase);
             if (ok) {
-                const uint32_t v = sbase + L::V + group * L::V_BYTES;
                 for (int i = ptid; i < (C - n) * 8; i += kPrepThreads) {
                     const uint32_t o = sw128_off(n + i / 8, i % 8);
 #pragma unroll
                     for (int x = 0; x < L::KA; ++x) st_shared_v4(kq + x * 16384 + o, 0, 0, 0, 0);
-                    st_shared_v4(v + o, 0, 0, 0, 0);
-                    st_shared_v4(v + 8192 + o, 0, 0, 0, 0);
                 }
             }
             fence_proxy_async_smem();
@@ -601,12 +599,13 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         }
         for (int i = 0; i < 6; ++i) {
             mbar_init(&B->kq_full[i], 1);
-            mbar_init(&B->v_full[i], 1);
             mbar_init(&B->vec_free[i], kConvWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&B->g[i], 1);
+            mbar_init(&B->v_full[i], 1);
             mbar_init(&B->v_free[i], 1);
+            mbar_init(&B->v_clear[i], 1);
             mbar_init(&B->ot_full[i], kConvWarps);
             mbar_init(&B->ready[i], kPrepWarps);
             mbar_init(&B->t_free[i], 1);
@@ -834,14 +833,20 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             Ring<6> six;
             Work w;
             int nb = 0;   // blocks of the CTA so far
+            uint32_t clear = 0;   // the turn of each v_clear, a bit each
             for (int k = 0; !fail && next_item(B, k, w, fail); ++k)
             for (int c = 0; c < w.blocks && !fail; ++c, ++nb, at.next(), six.next()) {
                 const uint32_t p = nb & 1;
                 const uint64_t dK = dK0 + at.s * (L::KQ_BYTES / 16), dKm = dKm0 + at.s * (L::KQ_BYTES / 16);
                 const uint64_t dV = dV0 + p * (L::V_BYTES / 16);
                 const uint64_t dT = dT0 + p * (L::TP_BYTES / 16);
+                const bool part = w.len - c * C < C;
                 auto start_u = [&]() {   // U = V^T T'^T, both parts of T'; the parts of the U before are read by now
-                    wait_w(&B->v_full[six.s], six.phase);
+                    wait_w(&B->v_full[p], (nb >> 1) & 1);
+                    if (part) {
+                        wait_w(&B->v_clear[p], (clear >> p) & 1);
+                        clear ^= 1u << p;
+                    }
                     if (nb >= 1) wait_w(&B->o, p ^ 1);
                     if (!fail && el) {
 #pragma unroll
@@ -853,11 +858,12 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 };
                 // before X is published if T' and V are there already and the block before's products are done
                 const bool u_early = __all_sync(0xffffffffu, mbar_test(smem_u32(&B->ready[p]), (nb >> 1) & 1) &&
-                                                                 mbar_test(smem_u32(&B->v_full[six.s]), six.phase) &&
+                                                                 mbar_test(smem_u32(&B->v_full[p]), (nb >> 1) & 1) &&
+                                                                 (!part || mbar_test(smem_u32(&B->v_clear[p]), (clear >> p) & 1)) &&
                                                                  (nb == 0 || mbar_test(smem_u32(&B->o), p ^ 1)));
                 if (u_early) start_u();
                 wait_w(&B->kq_full[six.s], six.phase);
-                if (w.len - c * C < C) wait_w(&B->ready[p], (nb >> 1) & 1);   // K's rows past the end are zeroed
+                if (part) wait_w(&B->ready[p], (nb >> 1) & 1);   // K's rows past the end are zeroed
                 wait_w(&B->xh, p);
                 if (fail) break;
                 if (el) {
@@ -1037,7 +1043,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
     } else {
         // ======================= work, V loads =======================================
         int idx = blockIdx.x, nb = 0;
-        Ring<6> six;
+        int keep = C;   // tokens of the block before, if it has rows past its request's end
         for (int k = 0;; ++k) {
             Request rq;
             const bool have = idx >= 0 && read_request(a, idx / a.Hv, rq);
@@ -1058,21 +1064,39 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 B->item[i] = w;
                 mbar_arrive(&B->item_full[i]);
             }
+            if (keep < C) {   // those rows of V, zero (once the next item is out: the prep of its first blocks starts with it)
+                const int m = nb - 1;
+                // (the turn before is complete: V of block m was loaded after block m - 2's outputs had left)
+                if (!warp_wait(smem_u32(&B->v_full[m & 1]), (m >> 1) & 1, abort)) {
+                    fail = true;
+                    break;
+                }
+                const uint32_t v = sbase + L::V + (m & 1) * L::V_BYTES;
+                for (int x = lane; x < (C - keep) * 8; x += 32) {
+                    const uint32_t o = sw128_off(keep + x / 8, x % 8);
+                    st_shared_v4(v + o, 0, 0, 0, 0);
+                    st_shared_v4(v + 8192 + o, 0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->v_clear[m & 1]);
+            }
             if (!have) break;
+            keep = w.len - (w.blocks - 1) * C;
             if (!w.fresh) {   // the state, into L2
                 const float* st = a.states + (static_cast<size_t>(w.slot) * a.Hv + w.head) * DV * DK;
                 for (int x = lane; x < DV * DK / 32; x += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(st + 32 * x));
             }
-            for (int c = 0; c < w.blocks && !fail; ++c, ++nb, six.next()) {
+            for (int c = 0; c < w.blocks && !fail; ++c, ++nb) {
                 const int vs = nb & 1, row = w.row0 + c * C;
                 // more work only once this item's last loads are at hand: what waits here could run elsewhere
                 if (c + 1 == w.blocks && lane == 0) steal_request(&B->answer, &B->stolen);
                 if (nb >= 2) fail = !warp_wait(smem_u32(&B->v_free[vs]), ((nb - 2) >> 1) & 1, abort);
                 if (lane == 0 && !fail) {
                     uint8_t* v = sm + L::V + vs * L::V_BYTES;
-                    mbar_arrive_expect_tx(&B->v_full[six.s], L::V_BYTES);
+                    mbar_arrive_expect_tx(&B->v_full[vs], L::V_BYTES);
 #pragma unroll 1
-                    for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[six.s], v + x * 8192, x * 64, w.head, row);
+                    for (int x = 0; x < DV / 64; ++x) tma_load_3d(&tmv, &B->v_full[vs], v + x * 8192, x * 64, w.head, row);
                 }
                 // the block after next, into L2 (K, Q and V; lanes 0 ..)
                 if (c + kTiles < w.blocks && lane < 2 * KA + DV / 64) {
@@ -1091,7 +1115,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         if (fail) {
             status = kStatusFlagWait;
             if (lane == 0)
-                for (int i = 0; i < 6; ++i)
+                for (int i = 0; i < 2; ++i)
                     for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(&B->v_full[i], ph, 10000000ull);
             __syncwarp();
         }
