@@ -7,8 +7,9 @@
 //   A_tj = b_t D_tj k_t.k_j  (j < t),   T = (I + A)^-1,   P_tj = D_tj q_t.k_j  (j <= t)
 //   R = diag(b) (V - diag(G) K X^T),   U = T R             [token][dv]
 //   O = diag(G) Q X^T + P U,           X <- G_31 X + U^T diag(D_31,.) K
-// The decays are running products, never quotients or logarithms: any gate,
-// zero among them, gives what the recurrence gives.
+// The decays are running products, never quotients or logarithms, so a gate may
+// be zero or negative. (Gates above 1 whose product over a block overflows give
+// infinity times zero where the recurrence may stay finite.)
 //
 // Work split. One CTA per (request, value head, 64 or 32 rows of the state),
 // longest requests first: rows of the state are independent. Four chain warps

@@ -378,8 +378,13 @@ int la_last_launches(const la_handle* h);
  *   v          [N, H_v, d_v]   (v_stride) apart, a multiple of 16 bytes, at
  *                              least a row's own extent: slices of one
  *                              projection's rows need no copy
- *   gate, beta [N, H_v]        fp32, contiguous. Any finite value (the gate
- *                              enters as a factor, zero included)
+ *   gate, beta [N, H_v]        fp32, contiguous. Any finite value token by
+ *                              token (the gate enters as a factor, zero
+ *                              included). The blockwise forms multiply the
+ *                              gates of up to 64 consecutive tokens first:
+ *                              such products have to be finite too, as they
+ *                              are where |gate| <= 1, or the request's
+ *                              results may be NaN
  *   out        [N, H_v, d_v]   io dtype, contiguous; written only in rows of
  *                              requests that take part
  *   states     [slots, H_v, d_v, d_k] fp32; only the slots of requests that

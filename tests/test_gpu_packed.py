@@ -257,6 +257,37 @@ def test_only_requests_that_have_seen_nothing_start_from_zeros(chunk):
     check(x, lens, seen, before, out, "bf16", chunk or 64)
 
 
+@pytest.mark.parametrize("dk,dv,chunk", [(64, 64, 32), (128, 128, 32), (64, 128, 64), (128, 128, 64), (64, 128, 1)])
+def test_gates_above_one_and_below_zero(dk, dv, chunk):
+    lens = [67, 130]
+    x, pool = draw(lens, 1, 2, dk, dv, "bf16", seed=dk + chunk)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda: torch.rand(sum(lens), 2, generator=gen, device="cuda")   # noqa: E731
+    x["gate"] = (0.7 + 0.6 * rnd()) * torch.where(rnd() < 0.5, -1.0, 1.0)   # products of 64 stay below 2^25
+    h = handle_for(lens, 1, 2, dk, dv, "bf16", pool)
+    plan = make_plan(h, lens, [0, 3], x["slots"])
+    before = x["states"].clone()
+    out = h.forward(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"], chunk=chunk)
+    assert h.status() == la.LA_OK
+    check(x, lens, [0, 3], before, out, "bf16", chunk)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_token_by_token_takes_any_finite_gate(io):
+    # powers of two whose products leave fp32's range while the states stay inside: with beta 0 states are scaled exactly
+    lens, Hv, d = [8, 4], 2, 64
+    x, pool = draw(lens, 1, Hv, d, d, io, seed=2)
+    x["gate"] = torch.tensor([2.0 ** e for e in (100, 60, -100, -60)] * 3, device="cuda")[:, None].expand(12, Hv).contiguous()
+    x["beta"].zero_()
+    x["states"] = x["states"].mul(2.0 ** -90)
+    h = handle_for(lens, 1, Hv, d, d, io, pool)
+    plan = make_plan(h, lens, [1, 1], x["slots"])
+    before = x["states"].clone()
+    out = h.decode_step(plan, x["q"], x["k"], x["v"], x["gate"], x["beta"], x["states"])
+    assert h.status() == la.LA_OK
+    assert torch.equal(x["states"], before) and torch.isfinite(out).all()
+
+
 @pytest.mark.parametrize("chunk", [1, 32, 64])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_nothing_leaks_between_requests(bad, chunk):
