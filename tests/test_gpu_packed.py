@@ -456,6 +456,100 @@ def test_a_larger_step_runs_its_short_requests_token_by_token(dk, dv, chunk):
         assert torch.equal(o2[a:e], o1[a:e]) and torch.equal(out[a:e], o1[a:e])
 
 
+# ------------------------------------------------------------------ which form runs
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("dk,dv,share", [(64, 64, 1), (128, 64, 1), (64, 128, 1), (128, 128, 1), (64, 64, 2), (128, 128, 2), (64, 64, 0), (128, 64, 0)])
+def test_long_requests_in_blocks_of_32(dk, dv, share):
+    # dozens of turns of every ring. CTAs of 32 state rows on more (share 1) or fewer (2) than half of the SMs, each on
+    # its own; or more than there are SMs, of 64 rows (0)
+    R = 2
+    per_head = R * (dv // 32)
+    Hv = sms() // (share * per_head) if share else sms() // per_head + 3
+    ctas = per_head * Hv
+    assert {0: ctas > sms(), 1: sms() / 2 < ctas <= sms(), 2: ctas <= sms() / 2}[share]
+    lens = [1003, 1057]
+    x, pool = draw(lens, 1, Hv, dk, dv, "bf16", seed=dk + 2 * dv + share, pad=8)
+    h = handle_for(lens, 1, Hv, dk, dv, "bf16", pool)
+    plan = make_plan(h, lens, [1, 0], x["slots"])
+    before, args = x["states"].clone(), [x[n] for n in ("q", "k", "v", "gate", "beta")]
+    out = h.forward(plan, *args, x["states"], chunk=32)
+    assert h.status() == la.LA_OK
+    check(x, lens, [1, 0], before, out, "bf16", 32)
+    for _ in range(10):
+        again = before.clone()
+        assert torch.equal(h.forward(plan, *args, again, chunk=32), out) and torch.equal(again, x["states"])
+
+
+def test_long_requests_in_blocks_of_64():
+    lens = [1003, 1057]
+    for dk, Hv in ((64, 11), (128, 11)):
+        x, pool = draw(lens, 1, Hv, dk, 128, "bf16", seed=dk, pad=8)
+        h = handle_for(lens, 1, Hv, dk, 128, "bf16", pool)
+        plan = make_plan(h, lens, [1, 0], x["slots"])
+        before, args = x["states"].clone(), [x[n] for n in ("q", "k", "v", "gate", "beta")]
+        out = h.forward(plan, *args, x["states"], chunk=64)
+        assert h.status() == la.LA_OK
+        check(x, lens, [1, 0], before, out, "bf16", 64)
+        for _ in range(10):
+            again = before.clone()
+            assert torch.equal(h.forward(plan, *args, again, chunk=64), out) and torch.equal(again, x["states"])
+
+
+def even_lengths(R, n):
+    return [n * (r + 1) // R - n * r // R for r in range(R)]
+
+
+def edge_cases():
+    """(d_k, requests, tokens, blocks of the default form): both sides of every rule's edge at d_v 128, 16
+    value heads."""
+    few = sms() // 64            # requests whose CTAs of 32 state rows have an SM each
+    full = -(-sms() // 16)       # requests with at least a head per SM
+    return [(128, few, 300, 32), (128, few + 1, 256, 32), (128, few + 1, 257, 64),
+            (64, full, 8191, 32), (64, full, 8192, 64), (64, full - 1, 8192, 32)]
+
+
+@pytest.mark.parametrize("case", range(6))
+def test_default_blocks_at_the_edges_of_their_rules(case):
+    dk, R, n, blocks = edge_cases()[case]
+    lens = even_lengths(R, n)
+    x, pool = draw(lens, 8, 16, dk, 128, "bf16", seed=n + R)
+    h = handle_for(lens, 8, 16, dk, 128, "bf16", pool)
+    plan = make_plan(h, lens, [1] * R, x["slots"])
+    got = {}
+    for chunk in (0, 32, 64):
+        states = x["states"].clone()
+        got[chunk] = h.forward(plan, *(x[y] for y in ("q", "k", "v", "gate", "beta")), states, chunk=chunk), states
+    assert h.status() == la.LA_OK
+    same = {c: all(torch.equal(a, b) for a, b in zip(got[0], got[c])) for c in (32, 64)}
+    assert same[blocks] and not same[96 - blocks]
+
+
+def test_a_larger_step_of_64_channels_runs_its_short_requests_beside_blocks_of_64():
+    lens = [700, 1, 4, 33, 2] * 12
+    R, Hv = len(lens), 16
+    assert sum(lens) * Hv >= 1 << 17 and R * Hv > sms()
+    x, pool = draw(lens, 8, Hv, 64, 128, "bf16", seed=77)
+    h = handle_for(lens, 8, Hv, 64, 128, "bf16", pool)
+    plan = make_plan(h, lens, [r % 2 for r in range(R)], x["slots"])
+    args = [x[n] for n in ("q", "k", "v", "gate", "beta")]
+    mixed, blocks, tokens = (x["states"].clone() for _ in range(3))
+    o1 = h.forward(plan, *args, mixed)
+    assert h.last_launches() == 2
+    o2 = h.forward(plan, *args, blocks, chunk=64)
+    o3 = h.decode_step(plan, *args, tokens)
+    assert h.status() == la.LA_OK
+    at = 0
+    for r, n in enumerate(lens):
+        o, st = (o3, tokens) if n <= 4 else (o2, blocks)
+        s = x["slots"][r]
+        assert torch.equal(o1[at:at + n], o[at:at + n]) and torch.equal(mixed[s], st[s]), r
+        at += n
+
+
 def test_a_prompt_in_two_steps_is_the_prompt():
     lens = [200]
     x, pool = draw(lens, 1, 2, 128, 128, "bf16", seed=12)
