@@ -415,35 +415,40 @@ class PackedPlan:
             self._views = (w[:4], w[offsets:offsets + requests + 1], w[slots:slots + requests],
                            w[order:order + requests], w[treq:treq + tokens], w[tpos:tpos + tokens])
 
+    def _section(self, i):
+        if self._views is None:
+            raise ValueError("plan: no step has been planned in this buffer yet")
+        return self._views[i]
+
     @property
     def counts(self):
         """int32 [4]: rows used, requests taking part, free slots left, faults (LA_PLAN_FAULT_* bits)."""
-        return self._views[0]
+        return self._section(0)
 
     @property
     def offsets(self):
         """int32 [requests + 1]: first row of every request."""
-        return self._views[1]
+        return self._section(1)
 
     @property
     def state_slots(self):
         """int32 [requests]: state slot of a request that takes part, else -1."""
-        return self._views[2]
+        return self._section(2)
 
     @property
     def order(self):
         """int32 [requests]: the order in which the prefill walks the requests."""
-        return self._views[3]
+        return self._section(3)
 
     @property
     def token_request(self):
         """int32 [tokens]: every row's request, -1 in rows of none."""
-        return self._views[4]
+        return self._section(4)
 
     @property
     def token_position(self):
         """int32 [tokens]: every row's position in its request (tokens seen before included), -1 in rows of none."""
-        return self._views[5]
+        return self._section(5)
 
 
 class PackedHandle:
@@ -560,6 +565,7 @@ class PackedHandle:
             qs, ks, vs = qs[0], ks[0], vs[0]
         else:
             self._own(plan)
+            plan._section(0)   # (refuses a buffer that no plan was made in)
             qs = self._rows("q", q, n, hk, dk)
             ks = self._rows("k", k, n, hk, dk)
             vs = self._rows("v", v, n, hv, dv)

@@ -759,6 +759,16 @@ def test_python_refuses_wrong_tensors():
     assert torch.equal(before, x["states"])
 
 
+def test_a_buffer_without_a_plan_is_refused():
+    for n in (0, 1, 9):
+        x, pool = draw([9], 2, 2, 64, 64, "bf16", seed=1)
+        h = handle_for([9], 2, 2, 64, 64, "bf16", pool)
+        with pytest.raises(ValueError, match="no step has been planned|shape"):
+            h.forward(h.new_plan(), *(x[y][:n] for y in ("q", "k", "v", "gate", "beta")), x["states"])
+    with pytest.raises(ValueError, match="no step has been planned"):
+        h.decode_step(h.new_plan(), *(x[y][:0] for y in ("q", "k", "v", "gate", "beta")), x["states"])
+
+
 def test_the_library_refuses_before_it_launches():
     lens = [5, 4]
     x, pool = draw(lens, 2, 2, 64, 64, "bf16", seed=1)

@@ -94,6 +94,16 @@ def test_plan_sections_agree_with_the_header(lib, tmp_path, R, N, S):
     assert [v.numel() for v in views] == [4, R + 1, R, R, N, N]
 
 
+def test_a_plan_has_sections_once_a_step_is_planned(lib):
+    c = config()
+    p = la.PackedPlan(c, lib.la_packed_plan_words(ctypes.byref(c)), "cpu")
+    for name in ("counts", "offsets", "state_slots", "order", "token_request", "token_position"):
+        with pytest.raises(ValueError, match="no step has been planned"):
+            getattr(p, name)
+    p._set(0, 0)
+    assert p.counts.numel() == 4 and p.offsets.numel() == 1 and p.order.numel() == 0
+
+
 def test_fault_numbers_agree():
     src = open(os.path.join(ROOT, "include", "la.h")).read()
     for name in ("ROWS", "FREE", "SLOT", "OWNER", "STATE", "OVERFLOW"):
