@@ -592,12 +592,15 @@ class PackedHandle:
         H_v], states fp32 [slots, H_v, d_v, d_k] updated in place. Returns out
         [tokens, H_v, d_v]; rows of no request are not written. ``chunk``: 0
         the default, 1 token by token, 32 or 64 (d_v 128) in blocks of so
-        many tokens."""
+        many tokens. By default the form, and with it a request's last bits,
+        goes by the whole step's size; chunk 1 and 64 give the same bits in
+        any step."""
         return self._step(self._lib.la_packed_forward, plan, q, k, v, gate, beta, states, out, stream, chunk)
 
     def decode_step(self, plan, q, k, v, gate, beta, states, *, out=None, stream=None):
         """The same for one or a few tokens per request: token by token, each
-        state read and written once."""
+        state read and written once. States are those after the last token;
+        to take tokens back, copy the slots before."""
         return self._step(self._lib.la_packed_decode_step, plan, q, k, v, gate, beta, states, out, stream)
 
     def last_launches(self) -> int:

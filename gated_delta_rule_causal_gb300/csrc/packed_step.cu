@@ -1,5 +1,5 @@
 // The gated delta rule token by token over packed requests, states in a pool
-// of slots: decode steps, a few drafted tokens, and every type and head size
+// of slots: decode steps, a few tokens a request, and every type and head size
 // that the blockwise kernel does not take. Per value head and state row i
 // (key head h * Hk / Hv), for each token
 //

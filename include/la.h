@@ -479,13 +479,21 @@ int la_packed_plan(la_packed* h, const int* lengths, const int* seen, int* slots
  *          d_v in {64, 128}), of 32 or 64 tokens (by d_k, d_v and the step's
  *          size, whichever measured faster), else token by token; in larger
  *          steps requests of up to four tokens run token by token beside the
- *          others, in a second launch. 1 = token by token. 32, 64 = blocks of so many (64: d_v 128), or
- *          LA_ERR_UNSUPPORTED where there is no such form.
- * The blockwise form keeps the state to a few 10^-6 of itself (q, k and v enter
- * its matrix products exactly, what the state depends on in two bf16 parts,
- * 2^-16 each); outputs are off by a few roundings to bf16. A NaN or infinity in
- * a request's rows may reach that request's outputs from the start of its
- * block on. One launch (or two, see chunk 0), no workspace.
+ *          others, in a second launch. 1 = token by token. 32, 64 = blocks of
+ *          so many (64: d_v 128), or LA_ERR_UNSUPPORTED where there is no such
+ *          form.
+ * Precision. Token by token everything is fp32 up to the outputs' rounding. The
+ * blockwise forms keep the state to a few 10^-6 of itself: q, k and v enter
+ * their matrix products exactly, what the state depends on in two bf16 parts
+ * (2^-16 each, products of two low parts left out). Of what only an output
+ * depends on, the state in S q and the decayed products q_t.k_j enter rounded
+ * to bf16: outputs are off by 2.4e-3 of their size (root mean square), where
+ * the output's own rounding alone gives 1.7e-3.
+ * With chunk 1 or 64 a request's results are the same bits whatever else is in
+ * the step. With chunk 0 the form, with chunk 32 the order of a sum, goes by
+ * the size of the whole step, and a request's last bits with it.
+ * A NaN or infinity in a request's rows may reach that request's outputs from
+ * the start of its block on. One launch (or two, see chunk 0), no workspace.
  * Errors: LA_ERR_INVALID_ARG (a NULL or rows that overlap, sizes above the
  * handle's), LA_ERR_MISALIGNED (a pointer or a row not 16-byte aligned; gate
  * and beta need 4 bytes),
@@ -496,7 +504,10 @@ int la_packed_forward(la_packed* h, const int* plan, const void* q, const void* 
                       long long k_stride, long long v_stride, int chunk, void* cuda_stream);
 
 /* The same for steps of one or a few tokens per request: each state is read
- * once and written once, token by token (chunk 1). */
+ * once and written once, token by token (chunk 1). The slot then holds the
+ * state after the request's last token and none before it: a caller that may
+ * take tokens back (a draft that is not accepted) keeps a copy of the slot and
+ * runs the accepted ones again from it. */
 int la_packed_decode_step(la_packed* h, const int* plan, const void* q, const void* k, const void* v,
                           const float* gate, const float* beta, float* states, void* out, int requests, int tokens,
                           long long q_stride, long long k_stride, long long v_stride, void* cuda_stream);

@@ -550,6 +550,24 @@ def test_a_larger_step_of_64_channels_runs_its_short_requests_beside_blocks_of_6
         at += n
 
 
+@pytest.mark.parametrize("dk,chunk", [(64, 1), (128, 1), (64, 64), (128, 64)])
+def test_bits_do_not_depend_on_the_other_requests(dk, chunk):
+    # chunk 1 and 64: one request in a step of its own gives what it gives among many others
+    rng = random.Random(dk + chunk)
+    lens = [rng.choice((1, 3, 20, 64, 130)) for _ in range(60)]
+    lens[20] = 150
+    x, pool = draw(lens, 4, 8, dk, 128, "bf16", seed=dk)
+    h = handle_for(lens, 4, 8, dk, 128, "bf16", pool)
+    names, start = ("q", "k", "v", "gate", "beta"), x["states"].clone()
+    out = h.forward(make_plan(h, lens, [1] * 60, x["slots"]), *(x[n] for n in names), x["states"], chunk=chunk)
+    for r in (0, 20, 59):
+        a, s = sum(lens[:r]), x["slots"][r]
+        own = start.clone()
+        o = h.forward(make_plan(h, [lens[r]], [1], [s]), *(x[n][a:a + lens[r]].clone() for n in names), own, chunk=chunk)
+        assert h.status() == la.LA_OK
+        assert torch.equal(o, out[a:a + lens[r]]) and torch.equal(own[s], x["states"][s])
+
+
 def test_a_prompt_in_two_steps_is_the_prompt():
     lens = [200]
     x, pool = draw(lens, 1, 2, 128, 128, "bf16", seed=12)
