@@ -242,7 +242,9 @@ __host__ __device__ inline long long unit_count(const StepArgs& a) {
 }
 
 // BESIDE: the launch before this one runs other requests of the same step, and lets this one start once it has waited
-// for what came before it; no row or slot is in both.
+// for what came before it; no row or slot is in both. So whatever wrote the plan, the tensors and the states is complete
+// when a CTA of this launch starts, without a wait of its own. That holds even if another thread's launch came in
+// between on the stream: it starts no earlier than every CTA of the blockwise launch has let it, which is after its wait.
 template <int DK, typename IO, int P, bool BESIDE>
 __global__ void __launch_bounds__(kThreads, 2) step_kernel(const StepArgs a) {
     using U = Unit<DK, P>;

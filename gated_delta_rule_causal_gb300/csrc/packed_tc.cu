@@ -1,6 +1,6 @@
 // The gated delta rule over packed requests on the tcgen05 tensor cores: bf16
 // q, k and v, value heads of 128, blocks of 64 tokens. The algebra is that of
-// packed_chunk.cu (value heads of 64, warp-level MMAs), with b's columns in T:
+// packed_chunk.cu (value heads of 64 and 128, warp-level MMAs), with b's columns in T:
 //   T' = (I + A)^-1 diag(b),   U = T' (V - diag(G) K X^T)
 //   O = diag(G) Q X^T + P U,   X <- G_63 X + U^T diag(D_63,.) K
 // and so is the precision: q, k, v exact; X, G Z, T' and U in two bf16 parts
@@ -20,7 +20,9 @@
 // of the columns of each product in row r. Two groups of four prep warps
 // compute T' and P of the blocks that follow; of the others one issues the
 // chain's MMAs, one loads K and Q and issues the prep warps' [K;Q] K^T, one
-// copies the outputs out, and one fetches the work and loads V.
+// copies the outputs out, and one fetches the work, loads V and clears its rows
+// behind a request (prep warps that did so waited for V, which comes only after
+// the outputs of the block before the last: 65536 tokens 457 us for 453).
 //
 // The chain's steps depend on one another, so what bounds a request is their
 // latency: three products (Z, R T'^T, U' K) with a conversion after each. High
@@ -627,7 +629,8 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         tma_prefetch_desc(&tmv);
     }
     griddep_wait();
-    {   // requests without a part come last: where this CTA's has none, nobody's after it has
+    {   // This CTA's request has no part, or is short and left to the launch that follows: others of the grid may have work
+        // all the same, which is theirs or whoever's takes it over.
         Request rq;
         if (a.above) griddep_launch_dependents();   // a launch for the shorter requests follows, which may run beside this one
         if (!read_request(a, blockIdx.x / a.Hv, rq)) return;
@@ -1046,6 +1049,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         int keep = C;   // tokens of the block before, if it has rows past its request's end
         for (int k = 0;; ++k) {
             Request rq;
+            // (a CTA that takes over a request without a part, or a short one, ends; those not yet started start by themselves)
             const bool have = idx >= 0 && read_request(a, idx / a.Hv, rq);
             const int i = k % kItems;
             if (k >= kItems) fail = !warp_wait(smem_u32(&B->item_free[i]), ((k / kItems) & 1) ^ 1, abort);
