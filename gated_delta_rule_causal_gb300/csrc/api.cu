@@ -11,6 +11,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/la.h"
+#include "host.h"
 #include "kernels.h"
 #include "prefill.h"
 
@@ -38,6 +39,10 @@ struct la_handle {
 };
 
 namespace {
+
+using la::aligned16;
+using la::DeviceGuard;
+using la::supported_d;
 
 // la_forward_host: how a call crosses the host link. Below kLargeCall bytes
 // per call: two groups of sequence-heads (best of 1, 2, 4, 8 on the
@@ -126,24 +131,6 @@ int fail(la_handle* h, int code, const std::string& msg) {
 int cuda_fail(la_handle* h, cudaError_t e, const char* what) {
     return fail(h, LA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
 }
-
-bool supported_d(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Make the handle's device current for the duration of a call.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) return;
-        ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 bool valid_variant(int v) {
     return v == LA_NORM_ELU1 || v == LA_GLA || v == LA_GDN || v == LA_NORM_DECAY || v == LA_KDA;

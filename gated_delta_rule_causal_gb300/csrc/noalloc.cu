@@ -23,10 +23,13 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/la.h"
+#include "host.h"
 #include "kernels.h"
 #include "prefill.h"
 
 namespace {
+
+using la::aligned16;
 
 constexpr size_t kScratchBytes = size_t(16) << 20;  // 16 MiB per device
 constexpr size_t kStatusBytes = 256;                // status word, padded
@@ -78,8 +81,6 @@ int setup(int dev, void** addr, int* sms) {
     *sms = g_sms[dev];
     return LA_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Scratch the chunked prefill needs for this shape: the segment summaries the
 // normalized / gated launcher picks (mirrors it), or the least the gated

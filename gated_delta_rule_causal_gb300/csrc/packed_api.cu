@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/la.h"
+#include "host.h"
 #include "kernels.h"
 #include "packed.h"
 
@@ -24,6 +25,9 @@ struct la_packed {
 
 namespace {
 
+using la::aligned16;
+using la::DeviceGuard;
+using la::supported_d;
 using la::packed::PlanLayout;
 using la::packed::StepArgs;
 
@@ -39,23 +43,6 @@ int cuda_fail(la_packed* h, cudaError_t e, const char* what) {
     std::snprintf(h->last_error, sizeof(h->last_error), "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
     return LA_ERR_CUDA;
 }
-
-bool supported_d(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Make the handle's device current for the duration of a call.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) return;
-        ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 // What a configuration has to satisfy; LA_OK or the error.
 int check_config(const la_packed_config* c) {
