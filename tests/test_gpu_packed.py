@@ -729,6 +729,32 @@ def test_two_servers_on_two_streams():
                 s.check(lens, decode)
 
 
+@pytest.mark.parametrize("dk,chunk", [(128, 64), (64, 64), (128, 0), (64, 32)])
+def test_large_steps_at_once_on_two_streams(dk, chunk):
+    # one handle, two plans, pools and outputs: more CTAs than SMs each, several calls without a pause
+    rng = random.Random(dk)
+    lens = [rng.choice((1, 4, 64, 129, 200)) for _ in range(30)]
+    h, parts = None, []
+    for seed in (1, 2):
+        x, pool = draw(lens, 8, 16, dk, 128, "bf16", seed=seed)
+        h = h or handle_for(lens, 8, 16, dk, 128, "bf16", pool)
+        plan = make_plan(h, lens, [7] * 30, x["slots"])
+        args = [x[n] for n in ("q", "k", "v", "gate", "beta")]
+        want = x["states"].clone()
+        for _ in range(6):
+            o = h.forward(plan, *args, want, chunk=chunk)
+            torch.cuda.synchronize()
+        parts.append((plan, args, x["states"], torch.zeros_like(o), want, o, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for plan, args, states, out, _, _, st in parts:
+            h.forward(plan, *args, states, out=out, chunk=chunk, stream=st)
+    torch.cuda.synchronize()
+    assert h.status() == la.LA_OK
+    for _, _, states, out, want, o, _ in parts:
+        assert torch.equal(states, want) and torch.equal(out, o)
+
+
 def test_a_stream_given_by_argument():
     lens = [50, 9]
     x, pool = draw(lens, 1, 2, 64, 64, "bf16", seed=31)
