@@ -272,7 +272,9 @@ int la_packed_status(la_packed* h, void* cuda_stream) {
     if (word != 0) {
         e = cudaMemset(h->d_status, 0, sizeof(int));
         if (e != cudaSuccess) return cuda_fail(h, e, "status clear");
-        return fail(h, LA_ERR_TIMEOUT, "a bounded device wait expired");
+        std::snprintf(h->last_error, sizeof(h->last_error),
+                      "a bounded device wait expired (status bits 0x%x: 1=TMA, 2=MMA, 8=work items and V)", word);
+        return LA_ERR_TIMEOUT;
     }
     return LA_OK;
 }
