@@ -21,8 +21,9 @@
 // compute T' and P of the blocks that follow; of the others one issues the
 // chain's MMAs, one loads K and Q and issues the prep warps' [K;Q] K^T, one
 // copies the outputs out, and one fetches the work, loads V and clears its rows
-// behind a request (prep warps that did so waited for V, which comes only after
-// the outputs of the block before the last: 65536 tokens 457 us for 453).
+// behind a request. (Prep warps that did so waited for V, which comes only after
+// the outputs of the block before the last: 65536 tokens 457 us for 452, 128
+// requests of 100 tokens 160 for 144, of 130 206 for 196; 256 of 40 190 for 195.)
 //
 // The chain's steps depend on one another, so what bounds a request is their
 // latency: three products (Z, R T'^T, U' K) with a conversion after each. High
@@ -31,8 +32,8 @@
 // outputs run in the gaps.
 //
 // Measured, bf16, d 128: two requests of 8192 tokens, 16 heads (32 CTAs, where the
-// blocks of 32 are faster): 427 us, 3.3 us or 6400 clocks a block; 96 requests of
-// 65536 tokens together, 16 heads: 447 us; 16 of 8191, 32 heads: 130 us. Of a
+// blocks of 32 are faster): 430 us, 3.3 us or 6400 clocks a block; 96 requests of
+// 65536 tokens together, 16 heads: 452 us; 16 of 8191, 32 heads: 129 us. Of a
 // block's clocks MMAs take 2700 (the tensor pipe is 34 % busy), the chain's
 // conversions 2500; the prep of a block takes 10000 to 12000, half of which two
 // groups make good. Issue slots are 53 % busy, and 8 % of the warps' waiting is
@@ -1068,6 +1069,10 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 B->item[i] = w;
                 mbar_arrive(&B->item_full[i]);
             }
+            if (have && !w.fresh) {   // the state, into L2
+                const float* st = a.states + (static_cast<size_t>(w.slot) * a.Hv + w.head) * DV * DK;
+                for (int x = lane; x < DV * DK / 32; x += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(st + 32 * x));
+            }
             if (keep < C) {   // those rows of V, zero (once the next item is out: the prep of its first blocks starts with it)
                 const int m = nb - 1;
                 // (the turn before is complete: V of block m was loaded after block m - 2's outputs had left)
@@ -1087,10 +1092,6 @@ tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             }
             if (!have) break;
             keep = w.len - (w.blocks - 1) * C;
-            if (!w.fresh) {   // the state, into L2
-                const float* st = a.states + (static_cast<size_t>(w.slot) * a.Hv + w.head) * DV * DK;
-                for (int x = lane; x < DV * DK / 32; x += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(st + 32 * x));
-            }
             for (int c = 0; c < w.blocks && !fail; ++c, ++nb) {
                 const int vs = nb & 1, row = w.row0 + c * C;
                 // more work only once this item's last loads are at hand: what waits here could run elsewhere
