@@ -72,9 +72,9 @@ bool blocks_of_64(const la_packed* h, int requests, int tokens) {
 }
 
 // Requests of up to so many tokens run token by token beside the others' blocks. Measured, us, 16 heads of 128, every
-// third request new, beside / all in blocks: 64 requests of one token 21 / 52, of four 35 / 52; 256 of one 87 / 186, of four 151 / 186; one prompt of
-// 1800 and 255 single tokens 130 / 195, and 63 single tokens 107 / 106, eight of 500 and 56 single tokens 57 / 73; 64
-// prompts of 600: 287 / 287, the second launch finds nothing to do.
+// third request new, beside / all in blocks: 64 requests of one token 21 / 52, of four 35 / 52; 256 of one 87 / 198, of
+// four 151 / 198; one prompt of 1800 and 255 single tokens 130 / 206, and 63 single tokens 107 / 106, eight of 500 and 56
+// single tokens 57 / 73; 64 prompts of 600: 287 / 287, the second launch finds nothing to do.
 constexpr int kShort = 4;
 
 int run_step(la_packed* h, const int* plan, const void* q, const void* k, const void* v, const float* gate,
